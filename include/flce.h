@@ -1,7 +1,9 @@
 /*
  * flce.h - C ABI of the language-model loss head for GB300 (sm_103a).
  *
- * Two operations, each split into a forward and a backward call:
+ * Two loss operations, each split into a forward and a backward call (and,
+ * in the sections at the end, the operators around them: the embedding lookup,
+ * the norms, and the head with 4-bit weights):
  *
  *   ce_logits_*  masked cross-entropy over GIVEN logits [N, V]; the backward can
  *                write the gradient into the logits storage (in place).
@@ -420,6 +422,129 @@ FLCE_API int flce_count_valid(const int64_t* labels, int64_t N, int64_t V, int64
 /* x[0..n) *= *g for x of dtype dt (device pointers); when *g == 1 nothing is
  * written.  Applies the incoming gradient to gradients computed with g = 1. */
 FLCE_API int flce_grad_scale(void* x, int dt, int64_t n, const float* g, flce_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Embedding lookup and its gradient                                        */
+/* ------------------------------------------------------------------------ */
+/* The other use of a tied table W [V, D]: the model's input
+ *   out[i] = scale * W[ids[i]]                                (one rounding to dt)
+ * and the gradient of the table
+ *   grad_W[v] (+)= scale * sum over i with ids[i] == v of grad_out[i],
+ * which joins the head's grad_W when accumulated.  The source pages only name
+ * the tied layout (Liger-Kernel issue #941); these calls have no counterpart
+ * there, and neither do the norms and the 4-bit head below. */
+
+/* Lookup.  ids: [N] int64; W: [V, ldw], out: [N, ldo], both of dtype dt with
+ * unit column stride (ldw, ldo >= D; any alignment of an element).  The
+ * product with scale is formed in fp32 and rounded once.  A row whose id lies
+ * outside [0, V) is written as zeros and sets FLCE_ELABEL in *status.  N == 0
+ * is valid.  out must not overlap W. */
+FLCE_API int embedding_fwd(const int64_t* ids, const void* W, int dt, int64_t N, int64_t D,
+                           int64_t V, int64_t ldw, float scale, void* out, int64_t ldo,
+                           int32_t* status, flce_stream_t stream);
+
+/* Bytes of device workspace embedding_bwd needs (0 for invalid sizes). */
+FLCE_API size_t embedding_bwd_workspace_bytes(int64_t N, int64_t D, int64_t V);
+
+/* Gradient of the table.  grad_out: [N, ldg] of dtype dt.  grad_W: [V, ldw] of
+ * dtype dt_grad: every element is written (rows no id names as zeros), or,
+ * with accumulate_grad_W != 0, rows that ids name are added to and the others
+ * left untouched.  Sums run in fp32 over the tokens of an id in a fixed order
+ * (two identical calls give identical bits) and are rounded once; adding to a
+ * FLCE_BF16 grad_W would round at every call and returns FLCE_ENOSUP.
+ * Tokens with id == padding_idx contribute nothing (their grad_out is not
+ * used); pass -1 for none.  Ids outside [0, V) contribute nothing and set
+ * FLCE_ELABEL.  Requires N < 2^31.  ws: embedding_bwd_workspace_bytes bytes,
+ * 16-byte aligned. */
+FLCE_API int embedding_bwd(const int64_t* ids, const void* grad_out, int dt, int64_t N, int64_t D,
+                           int64_t V, int64_t ldg, float scale, int64_t padding_idx,
+                           void* grad_W, int dt_grad, int64_t ldw, int accumulate_grad_W,
+                           void* ws, size_t ws_bytes, int32_t* status, flce_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Layer norm and RMS norm                                                  */
+/* ------------------------------------------------------------------------ */
+/* The norm that makes H.  Per row of x [N, D]:
+ *   mean = (1/D) sum_j x_j,  rstd = 1 / sqrt((1/D) sum_j (x_j - mean)^2 + eps)
+ *   h_j = (x_j - mean) rstd,  y_j = h_j weight_j + bias_j
+ * (rms_norm_*: mean = 0, no bias).  The sum of squares is taken around the
+ * mean in a second pass over the row (held on chip), so a mean far from 0
+ * costs no digits.  Backward, with u_j = grad_y_j weight_j:
+ *   grad_x_j = rstd (u_j - (1/D) sum u - h_j (1/D) sum u h)
+ *   grad_weight_j = sum over rows of grad_y_j h_j,  grad_bias_j = sum of grad_y_j
+ * (rms_norm_*: without the (1/D) sum u term).  All sums in fp32, in a fixed
+ * order.  x, y, grad_y, grad_x: dtype dt, row strides ldx, ... >= D, unit
+ * column stride, any alignment of an element.  weight and bias: [D] of dtype
+ * wdt, each may be NULL (1 and 0).  mean, rstd: [N] f32.  D >= 1; N == 0 is
+ * valid. */
+
+/* y may be x itself (then ldy == ldx); otherwise they must not overlap.
+ * mean and rstd may be NULL (not stored). */
+FLCE_API int layer_norm_fwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
+                            const void* weight, const void* bias, int wdt, float eps, void* y,
+                            int64_t ldy, float* mean, float* rstd, flce_stream_t stream);
+FLCE_API int rms_norm_fwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
+                          const void* weight, int wdt, float eps, void* y, int64_t ldy,
+                          float* rstd, flce_stream_t stream);
+
+/* Bytes of device workspace layer_norm_bwd and rms_norm_bwd need when
+ * grad_weight or grad_bias is asked for (0 for invalid sizes). */
+FLCE_API size_t norm_bwd_workspace_bytes(int64_t N, int64_t D);
+
+/* Each output may be NULL (not formed).  grad_x may be grad_y itself (then
+ * their strides are equal); otherwise it overlaps no input.  grad_weight and
+ * grad_bias: [D] f32, added to when accumulate != 0.  ws may be NULL when
+ * neither is asked for; 16-byte aligned. */
+FLCE_API int layer_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
+                            const void* grad_y, int64_t ldgy, const void* weight, int wdt,
+                            const float* mean, const float* rstd, void* grad_x, int64_t ldgx,
+                            float* grad_weight, float* grad_bias, int accumulate, void* ws,
+                            size_t ws_bytes, flce_stream_t stream);
+FLCE_API int rms_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
+                          const void* grad_y, int64_t ldgy, const void* weight, int wdt,
+                          const float* rstd, void* grad_x, int64_t ldgx, float* grad_weight,
+                          int accumulate, void* ws, size_t ws_bytes, flce_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The head with 4-bit weights: logits of a few tokens                      */
+/* ------------------------------------------------------------------------ */
+/* For answering rather than training: y = x Wq^T (+ bias) for M tokens, where
+ *   Wq[v, k] = (q[v, k] - z[v, k / group]) * scales[v, k / group],
+ * q in 0..15 and z the group's zero point (8 without zero points).  The
+ * weights are laid out once, by head4_quantize or by the caller:
+ *   packed  [V, ldp] bytes, ldp >= ceil(D / 128) * 64, a multiple of 16, base
+ *           16-byte aligned.  Each 128 columns of a row are 64 bytes, 16
+ *           little-endian 32-bit words; word 4 t + w (t, w in 0..3) holds the
+ *           columns 32 w + 8 t + j, j = 0..7, column j in bits 4 p .. 4 p + 3
+ *           with p = j / 2 + 4 (j mod 2).  Columns from D on may hold anything.
+ *   scales  [V, G] of dtype dt_s, contiguous, G = ceil(D / group)
+ *   zeros   [V, G] bytes in 0..15, contiguous, or NULL
+ *   group   32, 64 or 128 columns
+ * The products q x are summed within a group by tensor-core instructions with
+ * fp32 accumulation: (q - z) and bf16 x are exact there, and fp32 x is split
+ * into three bf16 parts that add up to it exactly.  The groups' sums times
+ * their scales add up in fp32, in a fixed order. */
+
+/* x: [M, ldx] of dtype dt; bias: [V] of dtype dt or NULL; y: [M, ldy] of dtype
+ * dt_y.  M == 0 is valid.  Made for M up to a few tens: the weights are read
+ * again for every 32 bf16 (10 fp32) tokens.  ws: head4_workspace_bytes bytes,
+ * 16-byte aligned (NULL when that is 0). */
+FLCE_API size_t head4_workspace_bytes(int dt, int64_t M, int64_t D, int64_t V);
+FLCE_API int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t ldx,
+                          const uint8_t* packed, int64_t ldp, const void* scales, int dt_s,
+                          const uint8_t* zeros, int group, int64_t V, const void* bias, void* y,
+                          int dt_y, int64_t ldy, void* ws, size_t ws_bytes, flce_stream_t stream);
+
+/* Rounds W [V, ldw] (dtype dt) to that layout.  Without zeros: scale =
+ * max |w| / 7 of the group, q = clamp(round(w / scale), -8, 7) + 8.  With
+ * zeros: the group's range widened to contain 0, scale = (max - min) / 15,
+ * z = round(-min / scale), q = clamp(round(w / scale) + z, 0, 15).  The scale
+ * is rounded to dt_s first and q formed with the rounded one; round is to the
+ * nearest, ties to even.  A group of zeros has scale 1.  Padding columns hold q = 0.
+ * W must be finite. */
+FLCE_API int head4_quantize(const void* W, int dt, int64_t V, int64_t D, int64_t ldw, int group,
+                            uint8_t* packed, int64_t ldp, void* scales, int dt_s, uint8_t* zeros,
+                            flce_stream_t stream);
 
 #ifdef __cplusplus
 }

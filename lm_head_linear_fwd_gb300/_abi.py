@@ -27,6 +27,7 @@ _i = ctypes.c_int
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _p = ctypes.c_void_p
+_f = ctypes.c_float
 
 _SIGNATURES = {
     "flce_status_string": (ctypes.c_char_p, [_i]),
@@ -69,6 +70,21 @@ _SIGNATURES = {
     "flce_mask_packed_labels": (_i, [_p, _p, _i64, _i64, _i64, _p]),
     "flce_gemm_set_pair": (_i, [_i]),
     "flce_gemm_pair_slots": (_i, []),
+    "embedding_fwd": (_i, [_p, _p, _i, _i64, _i64, _i64, _i64, _f, _p, _i64, _p, _p]),
+    "embedding_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "embedding_bwd": (_i, [_p, _p, _i, _i64, _i64, _i64, _i64, _f, _i64, _p, _i, _i64, _i, _p, _sz,
+                           _p, _p]),
+    "layer_norm_fwd": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _i, _f, _p, _i64, _p, _p, _p]),
+    "rms_norm_fwd": (_i, [_p, _i, _i64, _i64, _i64, _p, _i, _f, _p, _i64, _p, _p]),
+    "norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "layer_norm_bwd": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _p, _p, _i64, _p, _p,
+                            _i, _p, _sz, _p]),
+    "rms_norm_bwd": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _p, _i64, _p, _i, _p,
+                          _sz, _p]),
+    "head4_workspace_bytes": (_sz, [_i, _i64, _i64, _i64]),
+    "head4_logits": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _i, _i64, _p, _p, _i,
+                          _i64, _p, _sz, _p]),
+    "head4_quantize": (_i, [_p, _i, _i64, _i64, _i64, _i, _p, _i64, _p, _i, _p, _p]),
     "flce_gemm": (_i, [_i, _i, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _p]),
 }
 
@@ -154,3 +170,14 @@ flce_bounds_selftest = _call("flce_bounds_selftest")
 flce_mask_packed_labels = _call("flce_mask_packed_labels")
 flce_gemm_set_pair = _call("flce_gemm_set_pair")
 flce_gemm_pair_slots = _call("flce_gemm_pair_slots")
+embedding_fwd = _call("embedding_fwd")
+embedding_bwd_workspace_bytes = _call("embedding_bwd_workspace_bytes")
+embedding_bwd = _call("embedding_bwd")
+layer_norm_fwd = _call("layer_norm_fwd")
+rms_norm_fwd = _call("rms_norm_fwd")
+norm_bwd_workspace_bytes = _call("norm_bwd_workspace_bytes")
+layer_norm_bwd = _call("layer_norm_bwd")
+rms_norm_bwd = _call("rms_norm_bwd")
+head4_workspace_bytes = _call("head4_workspace_bytes")
+head4_logits = _call("head4_logits")
+head4_quantize = _call("head4_quantize")
