@@ -1,58 +1,653 @@
 // Embedding lookup and the gradient of the table.
 #include <algorithm>
+#include <atomic>
 
 #include "rows.cuh"
 
 namespace flce {
 
-template <typename T>
-__global__ void __launch_bounds__(256)
-    embedding_fwd_kernel(const int64_t* __restrict__ ids, const T* __restrict__ W, int64_t N,
-                         int64_t D, int64_t V, int64_t ldw, float scale, T* __restrict__ out,
-                         int64_t ldo, int32_t* status) {
-  for (int64_t i = blockIdx.x; i < N; i += gridDim.x) {
-    const int64_t v = ids[i];
-    const bool ok = label_ok(v, V);
-    if (!ok && threadIdx.x == 0) set_status(status, FLCE_ELABEL);
-    for (int64_t j = threadIdx.x; j < D; j += blockDim.x)
-      Elem<T>::store(out + i * ldo + j, ok ? Elem<T>::load(W + v * ldw + j) * scale : 0.0f);
+// VEC consecutive elements of T in fp32, loaded and stored as one access of
+// VEC * sizeof(T) bytes (2 to 16).
+template <typename T, int VEC>
+struct Vec {
+  static_assert(VEC * sizeof(T) <= 16, "one access");
+  float x[VEC];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == Elem<T>::kPerVec) {
+      Elem<T>::unpack(*reinterpret_cast<const uint4*>(p), x);
+    } else if constexpr (VEC == 2 && sizeof(T) == 2) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+      x[0] = bf16_lo(w);
+      x[1] = bf16_hi(w);
+    } else {
+      static_assert(VEC == 1, "16 or 4 bytes, or one element");
+      x[0] = Elem<T>::load(p);
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (VEC == Elem<T>::kPerVec) {
+      *reinterpret_cast<uint4*>(p) = Elem<T>::pack(x);
+    } else if constexpr (VEC == 2 && sizeof(T) == 2) {
+      *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x[0], x[1]);
+    } else {
+      static_assert(VEC == 1, "16 or 4 bytes, or one element");
+      Elem<T>::store(p, x[0]);
+    }
+  }
+};
+
+// VEC fp32 values stored as type G in accesses of at most 16 bytes.
+template <typename G, int VEC>
+__device__ __forceinline__ void load_as(const G* p, float (&x)[VEC]) {
+  constexpr int W = VEC < Elem<G>::kPerVec ? VEC : Elem<G>::kPerVec;
+#pragma unroll
+  for (int k = 0; k < VEC; k += W) {
+    if constexpr (W == 2 && sizeof(G) == 4) {
+      const float2 v = *reinterpret_cast<const float2*>(p + k);
+      x[k] = v.x;
+      x[k + 1] = v.y;
+    } else if constexpr (W == 4 && sizeof(G) == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + k);
+      x[k] = bf16_lo(v.x);
+      x[k + 1] = bf16_hi(v.x);
+      x[k + 2] = bf16_lo(v.y);
+      x[k + 3] = bf16_hi(v.y);
+    } else {
+      Vec<G, W> v;
+      v.load(p + k);
+#pragma unroll
+      for (int e = 0; e < W; ++e) x[k + e] = v.x[e];
+    }
   }
 }
 
-// One block per table row: the block scans all ids for its row and adds the
-// matching gradient rows in token order.
-template <typename T, typename G>
-__global__ void __launch_bounds__(256)
-    embedding_bwd_scan_kernel(const int64_t* __restrict__ ids, const T* __restrict__ dy, int64_t N,
-                              int64_t D, int64_t V, int64_t ldg, float scale, int64_t padding_idx,
-                              G* __restrict__ grad, int64_t ldw, int accumulate, int32_t* status) {
-  __shared__ uint8_t hit[256];
-  for (int64_t v = blockIdx.x; v < V; v += gridDim.x) {
-    for (int64_t j0 = 0; j0 < D; j0 += blockDim.x) {
-      const int64_t j = j0 + threadIdx.x;
-      float sum = 0.0f;
-      bool any = false;
-      for (int64_t i0 = 0; i0 < N; i0 += 256) {
-        const int64_t i = i0 + threadIdx.x;
-        const int64_t id = i < N ? ids[i] : -1;
-        if (i < N && v == 0 && j0 == 0 && !label_ok(id, V)) set_status(status, FLCE_ELABEL);
-        const bool h = i < N && id == v && id != padding_idx;
-        hit[threadIdx.x] = h;
-        if (__syncthreads_or(h)) {
-          for (int k = 0; k < 256; ++k) {
-            if (!hit[k]) continue;
-            any = true;
-            if (j < D) sum += Elem<T>::load(dy + (i0 + k) * ldg + j);
-          }
-          __syncthreads();
+template <typename G, int VEC>
+__device__ __forceinline__ void store_as(G* p, const float (&x)[VEC]) {
+  constexpr int W = VEC < Elem<G>::kPerVec ? VEC : Elem<G>::kPerVec;
+#pragma unroll
+  for (int k = 0; k < VEC; k += W) {
+    if constexpr (W == 2 && sizeof(G) == 4) {
+      *reinterpret_cast<float2*>(p + k) = make_float2(x[k], x[k + 1]);
+    } else if constexpr (W == 4 && sizeof(G) == 2) {
+      *reinterpret_cast<uint2*>(p + k) =
+          make_uint2(pack_bf16x2(x[k], x[k + 1]), pack_bf16x2(x[k + 2], x[k + 3]));
+    } else {
+      Vec<G, W> v;
+#pragma unroll
+      for (int e = 0; e < W; ++e) v.x[e] = x[k + e];
+      v.store(p + k);
+    }
+  }
+}
+
+// Elements per access that two row matrices allow: base addresses and row
+// strides of both are multiples of it (the columns' tail is masked).
+static int vec_width(const void* p, int dt, int64_t ld, const void* q, int dtq, int64_t ldq) {
+  const int most = dt == FLCE_BF16 ? 8 : 4;
+  for (int v = most; v > 1; v = v == 8 ? 2 : 1) {
+    // an access to q of v elements is split into 16-byte ones
+    const size_t a = dtype_size(dt) * v, b = std::min<size_t>(dtype_size(dtq) * v, 16);
+    if (aligned(p, a) && ld % v == 0 && aligned(q, b) && ldq % v == 0) return v;
+  }
+  return 1;
+}
+
+// ---------------------------------------------------------------------- lookup
+
+constexpr int kLookupThreads = 128;
+constexpr int kLookupLane = 32;  // elements of a row per lane and task
+
+// One warp copies 32 * kLookupLane elements of one row at a time, all its loads
+// in flight together.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kLookupThreads)
+    embedding_fwd_kernel(const int64_t* __restrict__ ids, const T* __restrict__ W, int64_t N,
+                         int64_t D, int64_t V, int64_t ldw, float scale, T* __restrict__ out,
+                         int64_t ldo, int64_t pieces, int32_t* status) {
+  constexpr int U = kLookupLane / VEC;
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kLookupThreads / 32);
+  const int64_t n = N * pieces;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kLookupThreads / 32) + (threadIdx.x >> 5);
+       t < n; t += step) {
+    const int64_t i = t / pieces;
+    const int64_t j0 = (t - i * pieces) * (32 * kLookupLane) + lane * VEC;
+    const int64_t v = ids[i];
+    T* o = out + i * ldo;
+    if (!label_ok(v, V)) {
+      if (lane == 0) set_status(status, FLCE_ELABEL);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int64_t j = j0 + u * 32 * VEC + e;
+          if (j < D) Elem<T>::store(o + j, 0.0f);
+        }
+      continue;
+    }
+    const T* w = W + v * ldw;
+    if (j0 - lane * VEC + 32 * kLookupLane <= D) {
+      Vec<T, VEC> r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u].load(w + j0 + u * 32 * VEC);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) r[u].x[e] *= scale;
+        r[u].store(o + j0 + u * 32 * VEC);
+      }
+    } else {
+      Vec<T, VEC> r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t j = j0 + u * 32 * VEC;
+        if (j + VEC <= D) {
+          r[u].load(w + j);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) r[u].x[e] = j + e < D ? Elem<T>::load(w + j + e) : 0.0f;
         }
       }
-      if (j < D && (any || !accumulate)) {
-        G* p = grad + v * ldw + j;
-        Elem<G>::store(p, accumulate ? Elem<G>::load(p) + sum * scale : sum * scale);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t j = j0 + u * 32 * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) r[u].x[e] *= scale;
+        if (j + VEC <= D) {
+          r[u].store(o + j);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (j + e < D) Elem<T>::store(o + j + e, r[u].x[e]);
+        }
       }
     }
   }
+}
+
+template <typename T, int VEC>
+static void launch_fwd(const int64_t* ids, const void* W, int64_t N, int64_t D, int64_t V,
+                       int64_t ldw, float scale, void* out, int64_t ldo, int32_t* status,
+                       cudaStream_t s) {
+  const int64_t pieces = (D + 32 * kLookupLane - 1) / (32 * kLookupLane);
+  constexpr int kWarps = kLookupThreads / 32;
+  const int64_t need = (N * pieces + kWarps - 1) / kWarps;
+  const int grid = static_cast<int>(std::min<int64_t>(need, sm_count() * 16));
+  embedding_fwd_kernel<T, VEC><<<grid, kLookupThreads, 0, s>>>(
+      ids, static_cast<const T*>(W), N, D, V, ldw, scale, static_cast<T*>(out), ldo, pieces,
+      status);
+}
+
+// -------------------------------------------------------------------- gradient
+//
+// grad_W[v] (+)= scale * sum over the tokens i of id v of dy[i].
+//
+// 1. embedding_sort_kernel: one cluster of CTAs sorts the tokens by id (least
+//    significant digit first, stable, so a row's tokens stay in token order and
+//    the sums do not depend on timing).  Tokens that contribute nothing (the
+//    padding id, ids out of range) get the key V and come last.  Meanwhile the
+//    other CTAs write zeros to the rows that no token names: each finds them by
+//    marking the ids that fall into its rows.
+// 2. embedding_reduce_kernel: the sorted tokens are cut into chunks of equal
+//    length, whatever the ids, so a frequent id costs no more than rare ones.
+//    A CTA adds up a chunk's rows over a tile of columns and writes the rows
+//    whose tokens all lie in its chunk.  A run of equal ids over several chunks
+//    leaves one partial sum per chunk; the last CTA to arrive (an integer
+//    ticket) adds the partial sums in chunk order and writes the row.
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxDigitBits = 9;
+constexpr int kFillRows = 1 << 16;  // rows marked at a time (one bit each)
+constexpr int kMaxSortCtas = 8;
+
+struct SortPlan {
+  int passes, bits;  // digits of `bits` bits
+};
+
+static SortPlan sort_plan(int64_t V) {  // keys 0..V
+  int total = 1;
+  while (total < 32 && (V >> total) != 0) ++total;
+  const int passes = (total + kMaxDigitBits - 1) / kMaxDigitBits;
+  return {passes, (total + passes - 1) / passes};
+}
+
+static int sort_ctas(int64_t N) {
+  int c = 1;
+  while (c < kMaxSortCtas && N > int64_t(4096) * c) c *= 2;
+  return c;
+}
+
+struct SortArgs {
+  const int64_t* ids;
+  int64_t N, V, padding_idx;
+  uint2* buf0;     // (key, token) pairs, written by the passes in turn
+  uint2* buf1;
+  int passes, bits;
+  int32_t* ticket;  // zeroed here for the reduction
+  int64_t tickets;
+  void* grad;       // null: nothing to fill
+  int64_t D, ldw;
+  int grad_es;
+  int32_t* status;
+};
+
+// Zeros for the rows of [v0, v1) that no id names.
+__device__ void fill_unnamed_rows(const SortArgs& a, int64_t v0, int64_t v1, uint32_t* mark) {
+  const int tid = threadIdx.x;
+  const int n = static_cast<int>(v1 - v0);
+  for (int k = tid; k < (n + 31) / 32; k += kSortThreads) mark[k] = 0;
+  __syncthreads();
+  for (int64_t i = tid; i < a.N; i += kSortThreads) {
+    const int64_t id = a.ids[i];
+    if (id >= v0 && id < v1 && id != a.padding_idx)
+      atomicOr(&mark[(id - v0) >> 5], 1u << ((id - v0) & 31));
+  }
+  __syncthreads();
+  const int64_t row_bytes = a.D * a.grad_es;
+  const int64_t ld_bytes = a.ldw * a.grad_es;
+  char* g = static_cast<char*>(a.grad) + v0 * ld_bytes;
+  if (((reinterpret_cast<uintptr_t>(g) | row_bytes | ld_bytes) & 15) == 0) {
+    const int64_t per = row_bytes / 16;
+    if (per >= 128) {
+      // a warp per row at a time
+      for (int r = tid >> 5; r < n; r += kSortWarps) {
+        if ((mark[r >> 5] >> (r & 31)) & 1u) continue;
+        uint4* p = reinterpret_cast<uint4*>(g + r * ld_bytes);
+        for (int64_t k = tid & 31; k < per; k += 32) __stcs(p + k, make_uint4(0, 0, 0, 0));
+      }
+      return;
+    }
+    for (int64_t k = tid; k < n * per; k += kSortThreads) {
+      const int64_t r = k / per;
+      if (!((mark[r >> 5] >> (r & 31)) & 1u))
+        __stcs(reinterpret_cast<uint4*>(g + r * ld_bytes) + (k - r * per), make_uint4(0, 0, 0, 0));
+    }
+    return;
+  }
+  for (int r = tid >> 5; r < n; r += kSortWarps) {
+    if ((mark[r >> 5] >> (r & 31)) & 1u) continue;
+    char* p = g + r * ld_bytes;
+    if (a.grad_es == 4) {
+      for (int64_t k = tid & 31; k < a.D; k += 32) reinterpret_cast<uint32_t*>(p)[k] = 0u;
+    } else {
+      for (int64_t k = tid & 31; k < a.D; k += 32) reinterpret_cast<uint16_t*>(p)[k] = 0;
+    }
+  }
+}
+
+// Two CTAs fit an SM, so the sort's cluster and all filling CTAs run at once.
+__global__ void __launch_bounds__(kSortThreads, 2) embedding_sort_kernel(SortArgs a) {
+  extern __shared__ uint32_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = static_cast<int>(cluster_nctarank());
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (blockIdx.x >= static_cast<unsigned>(C)) {
+    // rows of this CTA, a bitmap's worth at a time
+    const int64_t parts = static_cast<int64_t>(gridDim.x) - C;
+    const int64_t me = static_cast<int64_t>(blockIdx.x) - C;
+    const int64_t per = (a.V + parts - 1) / parts;
+    const int64_t end = min(a.V, (me + 1) * per);
+    for (int64_t v = me * per; v < end; v += kFillRows) {
+      fill_unnamed_rows(a, v, min(end, v + kFillRows), smem);
+      __syncthreads();
+    }
+    return;
+  }
+  for (int64_t k = rank * kSortThreads + tid; k < a.tickets; k += C * kSortThreads)
+    a.ticket[k] = 0;
+  const int R = 1 << a.bits;
+  uint32_t* count = smem;                    // [kSortWarps][R]
+  uint32_t* total = smem + kSortWarps * R;   // [kMaxSortCtas][R], written by every CTA
+  uint32_t* start = total + kMaxSortCtas * R;  // [R]
+  __shared__ uint32_t warp_sum[kSortWarps];
+  // this warp's share of the tokens, a multiple of 32 except at the end
+  const int64_t share = ((a.N + C * kSortWarps - 1) / (C * kSortWarps) + 31) / 32 * 32;
+  const int64_t i0 = min(a.N, (static_cast<int64_t>(rank) * kSortWarps + warp) * share);
+  const int64_t i1 = min(a.N, i0 + share);
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const uint2* src = (pass & 1) ? a.buf0 : a.buf1;
+    uint2* dst = (pass & 1) ? a.buf1 : a.buf0;
+    const int shift = pass * a.bits;
+    auto fetch = [&](int64_t i) -> uint2 {
+      if (pass > 0) return __ldcg(src + i);
+      const int64_t id = a.ids[i];
+      const bool ok = label_ok(id, a.V);
+      if (!ok) set_status(a.status, FLCE_ELABEL);
+      return make_uint2(static_cast<uint32_t>(ok && id != a.padding_idx ? id : a.V),
+                        static_cast<uint32_t>(i));
+    };
+    for (int k = tid; k < kSortWarps * R; k += kSortThreads) count[k] = 0;
+    __syncthreads();
+    uint32_t* mine = count + warp * R;
+    for (int64_t i = i0 + lane; i < i1; i += 32)
+      atomicAdd(&mine[(fetch(i).x >> shift) & (R - 1)], 1u);
+    __syncthreads();
+    // per digit: exclusive sums over this CTA's warps, and the CTA's total,
+    // handed to every CTA of the cluster
+    for (int d = warp; d < R; d += kSortWarps) {
+      const uint32_t c = count[lane * R + d];
+      uint32_t s = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
+      }
+      count[lane * R + d] = s - c;
+      const uint32_t sum = __shfl_sync(0xffffffffu, s, 31);
+      if (lane < C) {
+        const uint32_t at = mapa_shared(smem_u32(total + rank * R + d), lane);
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(sum) : "memory");
+      }
+    }
+    cluster_sync();
+    // first place of each digit: all smaller digits, then the CTAs before this
+    // one (R <= kSortThreads: one digit per thread)
+    uint32_t all = 0, before = 0;
+    if (tid < R) {
+      for (int c = 0; c < C; ++c) {
+        const uint32_t t = total[c * R + tid];
+        if (c < rank) before += t;
+        all += t;
+      }
+    }
+    uint32_t s = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += t;
+    }
+    if (lane == 31) warp_sum[warp] = s;
+    __syncthreads();
+    uint32_t base = 0;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    if (tid < R) start[tid] = base + s - all + before;
+    __syncthreads();
+    // each warp places its tokens in order; lanes of one digit by lane
+    for (int64_t i = i0; i < i1; i += 32) {
+      const bool in = i + lane < i1;
+      const uint2 e = in ? fetch(i + lane) : make_uint2(0, 0);
+      const uint32_t digit = in ? (e.x >> shift) & (R - 1) : R;
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      const int before_me = __popc(same & ((1u << lane) - 1u));
+      if (in) {
+        const uint32_t at = start[digit] + mine[digit] + before_me;
+        if (in_range(at, a.N, a.status)) __stcg(dst + at, e);
+      }
+      __syncwarp();
+      if (in && before_me == 0) mine[digit] += __popc(same);
+      __syncwarp();
+    }
+    cluster_sync();
+  }
+}
+
+constexpr int kReduceThreads = 128;
+constexpr int kReduceLane = 8;  // columns per thread
+constexpr int kReduceTile = kReduceThreads * kReduceLane;
+constexpr int kMaxChunk = 256;
+constexpr int kReduceAhead = 8;  // token rows loaded together
+
+struct ReducePlan {
+  int chunk;        // tokens per chunk, a power of two
+  int64_t chunks, tiles;
+};
+
+// About eight blocks for each SM; longer chunks for more tokens.
+static ReducePlan reduce_plan(int64_t N, int64_t D) {
+  const int64_t tiles = (D + kReduceTile - 1) / kReduceTile;
+  int chunk = 8;
+  while (chunk < kMaxChunk && N * tiles > int64_t(1216) * chunk) chunk *= 2;
+  return {chunk, (N + chunk - 1) / chunk, tiles};
+}
+
+struct ReduceArgs {
+  const uint2* sorted;
+  const void* dy;
+  int64_t N, D, V, ldg;
+  float scale;
+  void* grad;
+  int64_t ldw;
+  int accumulate;
+  int chunk;
+  int64_t chunks, tiles;
+  float* part;      // [chunks][2][D]
+  int32_t* ticket;  // [chunks][tiles]
+  int32_t* status;
+};
+
+template <typename T, typename G, int VEC>
+__global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(ReduceArgs a) {
+  constexpr int U = kReduceLane / VEC;
+  __shared__ uint2 tok[kMaxChunk];
+  __shared__ int64_t run_first, run_last;
+  __shared__ int last;
+  const int tid = threadIdx.x;
+  const T* dy = static_cast<const T*>(a.dy);
+  const int64_t items = a.chunks * a.tiles;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t c = item / a.tiles, tile = item - c * a.tiles;
+    const int64_t col0 = tile * kReduceTile + tid * VEC;
+    const int64_t t0 = c * a.chunk;
+    const int n = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.N - t0));
+    __syncthreads();  // tok is free again
+    for (int k = tid; k < n; k += kReduceThreads) tok[k] = a.sorted[t0 + k];
+    const uint32_t none = 0xffffffffu;
+    const uint32_t before = t0 > 0 ? a.sorted[t0 - 1].x : none;
+    const uint32_t after = t0 + n < a.N ? a.sorted[t0 + n].x : none;
+    __syncthreads();
+    const uint32_t V = static_cast<uint32_t>(a.V);
+
+    auto out_row = [&](uint32_t v, const float (&acc)[U][VEC]) {
+      G* g = static_cast<G*>(a.grad) + static_cast<int64_t>(v) * a.ldw;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t j = col0 + u * kReduceThreads * VEC;
+        float r[VEC];
+        if (j + VEC <= a.D) {
+          if (a.accumulate) {
+            load_as<G, VEC>(g + j, r);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) r[e] += acc[u][e] * a.scale;
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) r[e] = acc[u][e] * a.scale;
+          }
+          store_as<G, VEC>(g + j, r);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (j + e < a.D) {
+              const float old = a.accumulate ? Elem<G>::load(g + j + e) : 0.0f;
+              Elem<G>::store(g + j + e, old + acc[u][e] * a.scale);
+            }
+        }
+      }
+    };
+    auto part_row = [&](int64_t chunk, int slot) { return a.part + (chunk * 2 + slot) * a.D; };
+
+    float acc[U][VEC] = {};
+    uint32_t key = tok[0].x;
+    bool first = true;  // the run that the chunk begins with
+    int slots = 0;      // bit 0: partial of a run from before, bit 1: of one that goes on
+    auto flush = [&](bool goes_on) {
+      if (key == V) return;
+      const bool from_before = first && key == before;
+      if (!from_before && !goes_on) {
+        out_row(key, acc);
+      } else {
+        const int slot = from_before ? 0 : 1;
+        float* p = part_row(c, slot);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const int64_t j = col0 + u * kReduceThreads * VEC + e;
+            if (j < a.D) __stcg(p + j, acc[u][e]);
+          }
+        slots |= 1 << slot;
+      }
+    };
+    for (int k0 = 0; k0 < n; k0 += kReduceAhead) {
+      Vec<T, VEC> r[kReduceAhead][U];
+#pragma unroll
+      for (int k = 0; k < kReduceAhead; ++k) {
+        const bool in = k0 + k < n && tok[k0 + k].x != V;
+        const T* row = dy + static_cast<int64_t>(in ? tok[k0 + k].y : 0) * a.ldg;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t j = col0 + u * kReduceThreads * VEC;
+          if (in && j + VEC <= a.D) {
+            r[k][u].load(row + j);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+              r[k][u].x[e] = in && j + e < a.D ? Elem<T>::load(row + j + e) : 0.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kReduceAhead; ++k) {
+        if (k0 + k < n) {
+          const uint32_t next = tok[k0 + k].x;
+          if (next != key) {
+            flush(false);
+            first = false;
+            key = next;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) acc[u][e] = 0.0f;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[u][e] += r[k][u].x[e];
+        }
+      }
+    }
+    flush(key == after);
+
+    // runs over several chunks: the last CTA to arrive adds the partial sums
+    for (int slot = 0; slot < 2; ++slot) {
+      if (!(slots & (1 << slot))) continue;  // the same for all threads
+      const uint32_t v = slot == 0 ? before : key;
+      __threadfence();
+      __syncthreads();
+      if (tid < 32) {
+        // first chunk: the one whose predecessor ends in another id
+        int64_t lo = c;
+        if (slot == 0) {
+          for (int64_t b = c - 1;; b -= 32) {
+            const int64_t q = b - tid;
+            const bool stop = q <= 0 || a.sorted[q * a.chunk - 1].x != v;
+            const uint32_t m = __ballot_sync(0xffffffffu, stop);
+            if (m) {
+              lo = b - (__ffs(m) - 1);
+              break;
+            }
+          }
+        }
+        // last chunk: the one whose successor begins with another id
+        int64_t hi = c;
+        for (int64_t b = c;; b += 32) {
+          const int64_t q = b + tid;
+          const bool stop = (q + 1) * a.chunk >= a.N || a.sorted[(q + 1) * a.chunk].x != v;
+          const uint32_t m = __ballot_sync(0xffffffffu, stop);
+          if (m) {
+            hi = b + __ffs(m) - 1;
+            break;
+          }
+        }
+        if (tid == 0) {
+          run_first = lo;
+          run_last = hi;
+          const int arrived = atomicAdd(a.ticket + lo * a.tiles + tile, 1);
+          last = arrived == static_cast<int>(hi - lo);
+        }
+      }
+      __syncthreads();
+      if (last) {
+        __threadfence();
+        float sum[U][VEC] = {};
+        for (int64_t q = run_first; q <= run_last; ++q) {
+          const float* p = part_row(q, q == run_first ? 1 : 0);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              const int64_t j = col0 + u * kReduceThreads * VEC + e;
+              if (j < a.D) sum[u][e] += __ldcg(p + j);
+            }
+        }
+        out_row(v, sum);
+      }
+      __syncthreads();  // run_first, run_last and last are free again
+    }
+  }
+}
+
+template <typename T, typename G>
+static void launch_reduce(const ReduceArgs& a, int vec, cudaStream_t s) {
+  const unsigned grid =
+      static_cast<unsigned>(std::min<int64_t>(a.chunks * a.tiles, int64_t(1) << 30));
+  if (vec == Elem<T>::kPerVec)
+    embedding_reduce_kernel<T, G, Elem<T>::kPerVec><<<grid, kReduceThreads, 0, s>>>(a);
+  else if (vec == 2 && sizeof(T) == 2)
+    embedding_reduce_kernel<T, G, sizeof(T) == 2 ? 2 : 1><<<grid, kReduceThreads, 0, s>>>(a);
+  else
+    embedding_reduce_kernel<T, G, 1><<<grid, kReduceThreads, 0, s>>>(a);
+}
+
+static size_t sort_smem(int bits) {
+  const size_t sort = sizeof(uint32_t) * (size_t(1) << bits) * (kSortWarps + kMaxSortCtas + 1);
+  return std::max<size_t>(sort, kFillRows / 8);
+}
+
+static int launch_sort(const SortArgs& a, cudaStream_t s) {
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc != FLCE_OK) return rc;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(raised.load() & bit)) {
+    rc = cuda_status(cudaFuncSetAttribute(embedding_sort_kernel,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(sort_smem(kMaxDigitBits))),
+                     "cudaFuncSetAttribute(embedding_sort_kernel)");
+    if (rc != FLCE_OK) return rc;
+    raised.fetch_or(bit);
+  }
+  const int C = sort_ctas(a.N);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  const int fill = a.grad != nullptr ? std::max(1, sm_count() / C) * C : 0;
+  cfg.gridDim = dim3(static_cast<unsigned>(C + fill), 1, 1);
+  cfg.blockDim = dim3(kSortThreads, 1, 1);
+  cfg.dynamicSmemBytes = sort_smem(a.bits);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, embedding_sort_kernel, a),
+                     "cudaLaunchKernelEx(embedding_sort_kernel)");
+}
+
+struct BwdWorkspace {
+  size_t buf, ticket, part, total;
+};
+
+static BwdWorkspace bwd_workspace(int64_t N, int64_t D) {
+  const ReducePlan r = reduce_plan(N, D);
+  BwdWorkspace w;
+  w.buf = round_up(static_cast<size_t>(N) * sizeof(uint2), 256);
+  w.ticket = round_up(static_cast<size_t>(r.chunks * r.tiles) * sizeof(int32_t), 256);
+  w.part = round_up(static_cast<size_t>(r.chunks) * 2 * static_cast<size_t>(D) * 4, 256);
+  w.total = 2 * w.buf + w.ticket + w.part;
+  return w;
 }
 
 }  // namespace flce
@@ -72,22 +667,24 @@ extern "C" int embedding_fwd(const int64_t* ids, const void* W, int dt, int64_t 
   const size_t es = dtype_size(dt);
   if (overlap(W, span_bytes(V, D, ldw, es), out, span_bytes(N, D, ldo, es))) return FLCE_EINVAL;
   if (N == 0) return FLCE_OK;
-  const int grid = static_cast<int>(std::min<int64_t>(N, sm_count() * 8));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dt == FLCE_BF16)
-    embedding_fwd_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
-        ids, static_cast<const __nv_bfloat16*>(W), N, D, V, ldw, scale,
-        static_cast<__nv_bfloat16*>(out), ldo, status);
-  else
-    embedding_fwd_kernel<float><<<grid, 256, 0, s>>>(ids, static_cast<const float*>(W), N, D, V,
-                                                     ldw, scale, static_cast<float*>(out), ldo,
-                                                     status);
+  const int vec = vec_width(W, dt, ldw, out, dt, ldo);
+#define FLCE_FWD(T, VEC) launch_fwd<T, VEC>(ids, W, N, D, V, ldw, scale, out, ldo, status, s)
+  if (dt == FLCE_BF16) {
+    if (vec == 8) FLCE_FWD(__nv_bfloat16, 8);
+    else if (vec == 2) FLCE_FWD(__nv_bfloat16, 2);
+    else FLCE_FWD(__nv_bfloat16, 1);
+  } else {
+    if (vec == 4) FLCE_FWD(float, 4);
+    else FLCE_FWD(float, 1);
+  }
+#undef FLCE_FWD
   return launch_status("embedding_fwd_kernel launch");
 }
 
 extern "C" size_t embedding_bwd_workspace_bytes(int64_t N, int64_t D, int64_t V) {
-  (void)N, (void)D, (void)V;
-  return 0;
+  if (N < 1 || N >= (int64_t(1) << 31) || D < 1 || V < 1) return 0;
+  return bwd_workspace(N, D).total;
 }
 
 extern "C" int embedding_bwd(const int64_t* ids, const void* grad_out, int dt, int64_t N,
@@ -110,16 +707,54 @@ extern "C" int embedding_bwd(const int64_t* ids, const void* grad_out, int dt, i
   const size_t need = embedding_bwd_workspace_bytes(N, D, V);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return FLCE_EWORKSPACE;
   if (!aligned(ws, 16)) return FLCE_EALIGN;
+  if (N == 0 && accumulate_grad_W) return FLCE_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int grid = static_cast<int>(std::min<int64_t>(V, sm_count() * 8));
-#define FLCE_BWD(T, G)                                                                     \
-  embedding_bwd_scan_kernel<T, G><<<grid, 256, 0, s>>>(                                    \
-      ids, static_cast<const T*>(grad_out), N, D, V, ldg, scale, padding_idx,              \
-      static_cast<G*>(grad_W), ldw, accumulate_grad_W, status)
-  if (dt == FLCE_BF16 && dt_grad == FLCE_BF16) FLCE_BWD(__nv_bfloat16, __nv_bfloat16);
-  else if (dt == FLCE_BF16) FLCE_BWD(__nv_bfloat16, float);
-  else if (dt_grad == FLCE_BF16) FLCE_BWD(float, __nv_bfloat16);
-  else FLCE_BWD(float, float);
-#undef FLCE_BWD
-  return launch_status("embedding_bwd_scan_kernel launch");
+
+  const BwdWorkspace w = bwd_workspace(N, D);
+  const ReducePlan plan = reduce_plan(N, D);
+  const SortPlan sp = sort_plan(V);
+  char* base = static_cast<char*>(ws);
+  SortArgs sa{};
+  sa.ids = ids;
+  sa.N = N;
+  sa.V = V;
+  sa.padding_idx = padding_idx;
+  sa.buf0 = reinterpret_cast<uint2*>(base);
+  sa.buf1 = reinterpret_cast<uint2*>(base + w.buf);
+  sa.passes = sp.passes;
+  sa.bits = sp.bits;
+  sa.ticket = reinterpret_cast<int32_t*>(base + 2 * w.buf);
+  sa.tickets = plan.chunks * plan.tiles;
+  sa.grad = accumulate_grad_W ? nullptr : grad_W;
+  sa.D = D;
+  sa.ldw = ldw;
+  sa.grad_es = static_cast<int>(dtype_size(dt_grad));
+  sa.status = status;
+  rc = launch_sort(sa, s);
+  if (rc != FLCE_OK || N == 0) return rc;
+
+  ReduceArgs ra{};
+  ra.sorted = (sp.passes & 1) ? sa.buf0 : sa.buf1;
+  ra.dy = grad_out;
+  ra.N = N;
+  ra.D = D;
+  ra.V = V;
+  ra.ldg = ldg;
+  ra.scale = scale;
+  ra.grad = grad_W;
+  ra.ldw = ldw;
+  ra.accumulate = accumulate_grad_W;
+  ra.chunk = plan.chunk;
+  ra.chunks = plan.chunks;
+  ra.tiles = plan.tiles;
+  ra.ticket = sa.ticket;
+  ra.part = reinterpret_cast<float*>(base + 2 * w.buf + w.ticket);
+  ra.status = status;
+  const int vec = vec_width(grad_out, dt, ldg, grad_W, dt_grad, ldw);
+  using B = __nv_bfloat16;
+  if (dt == FLCE_BF16 && dt_grad == FLCE_BF16) launch_reduce<B, B>(ra, vec, s);
+  else if (dt == FLCE_BF16) launch_reduce<B, float>(ra, vec, s);
+  else if (dt_grad == FLCE_BF16) launch_reduce<float, B>(ra, vec, s);
+  else launch_reduce<float, float>(ra, vec, s);
+  return launch_status("embedding_reduce_kernel launch");
 }
