@@ -36,6 +36,47 @@ struct Vec {
   }
 };
 
+// VEC elements of T as they lie in memory, to be unpacked when used (half the
+// registers of Vec for bf16).
+template <typename T, int VEC>
+struct RawVec {
+  static constexpr int kWords = VEC * sizeof(T) >= 4 ? VEC * sizeof(T) / 4 : 1;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (VEC * sizeof(T) == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      static_assert(VEC * sizeof(T) == 2, "16, 4 or 2 bytes");
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  // the first `left` elements (none when left <= 0), zeros after them
+  __device__ __forceinline__ void load_part(const T* p, int64_t left) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = 0u;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (e >= left) continue;
+      if constexpr (sizeof(T) == 4)
+        w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+      else
+        w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[e]) << (16 * (e & 1));
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&x)[VEC]) const {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if constexpr (sizeof(T) == 4)
+        x[e] = __uint_as_float(w[e]);
+      else
+        x[e] = (e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    }
+  }
+};
+
 // VEC fp32 values stored as type G in accesses of at most 16 bytes.
 template <typename G, int VEC>
 __device__ __forceinline__ void load_as(const G* p, float (&x)[VEC]) {
@@ -200,6 +241,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigitBits = 9;
 constexpr int kFillRows = 1 << 16;  // rows marked at a time (one bit each)
 constexpr int kMaxSortCtas = 8;
+constexpr int kSortAhead = 4;       // tokens per lane loaded together
 
 struct SortPlan {
   int passes, bits;  // digits of `bits` bits
@@ -214,7 +256,7 @@ static SortPlan sort_plan(int64_t V) {  // keys 0..V
 
 static int sort_ctas(int64_t N) {
   int c = 1;
-  while (c < kMaxSortCtas && N > int64_t(4096) * c) c *= 2;
+  while (c < kMaxSortCtas && N > int64_t(kSortThreads) * c) c *= 2;
   return c;
 }
 
@@ -276,8 +318,7 @@ __device__ void fill_unnamed_rows(const SortArgs& a, int64_t v0, int64_t v1, uin
   }
 }
 
-// Two CTAs fit an SM, so the sort's cluster and all filling CTAs run at once.
-__global__ void __launch_bounds__(kSortThreads, 2) embedding_sort_kernel(SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a) {
   extern __shared__ uint32_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = static_cast<int>(cluster_nctarank());
@@ -297,8 +338,9 @@ __global__ void __launch_bounds__(kSortThreads, 2) embedding_sort_kernel(SortArg
   for (int64_t k = rank * kSortThreads + tid; k < a.tickets; k += C * kSortThreads)
     a.ticket[k] = 0;
   const int R = 1 << a.bits;
-  uint32_t* count = smem;                    // [kSortWarps][R]
-  uint32_t* total = smem + kSortWarps * R;   // [kMaxSortCtas][R], written by every CTA
+  const int S = R + 1;                       // a digit's counts of all warps in 32 banks
+  uint32_t* count = smem;                    // [kSortWarps][S]
+  uint32_t* total = smem + kSortWarps * S;   // [kMaxSortCtas][R], written by every CTA
   uint32_t* start = total + kMaxSortCtas * R;  // [R]
   __shared__ uint32_t warp_sum[kSortWarps];
   // this warp's share of the tokens, a multiple of 32 except at the end
@@ -317,23 +359,31 @@ __global__ void __launch_bounds__(kSortThreads, 2) embedding_sort_kernel(SortArg
       return make_uint2(static_cast<uint32_t>(ok && id != a.padding_idx ? id : a.V),
                         static_cast<uint32_t>(i));
     };
-    for (int k = tid; k < kSortWarps * R; k += kSortThreads) count[k] = 0;
+    for (int k = tid; k < kSortWarps * S; k += kSortThreads) count[k] = 0;
     __syncthreads();
-    uint32_t* mine = count + warp * R;
-    for (int64_t i = i0 + lane; i < i1; i += 32)
-      atomicAdd(&mine[(fetch(i).x >> shift) & (R - 1)], 1u);
+    uint32_t* mine = count + warp * S;
+    // kSortAhead loads in flight per lane, here and where the tokens are placed
+    for (int64_t i = i0 + lane; i < i1; i += 32 * kSortAhead) {
+      uint2 e[kSortAhead];
+#pragma unroll
+      for (int k = 0; k < kSortAhead; ++k)
+        if (i + 32 * k < i1) e[k] = fetch(i + 32 * k);
+#pragma unroll
+      for (int k = 0; k < kSortAhead; ++k)
+        if (i + 32 * k < i1) atomicAdd(&mine[(e[k].x >> shift) & (R - 1)], 1u);
+    }
     __syncthreads();
     // per digit: exclusive sums over this CTA's warps, and the CTA's total,
     // handed to every CTA of the cluster
     for (int d = warp; d < R; d += kSortWarps) {
-      const uint32_t c = count[lane * R + d];
+      const uint32_t c = count[lane * S + d];
       uint32_t s = c;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t t = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += t;
       }
-      count[lane * R + d] = s - c;
+      count[lane * S + d] = s - c;
       const uint32_t sum = __shfl_sync(0xffffffffu, s, 31);
       if (lane < C) {
         const uint32_t at = mapa_shared(smem_u32(total + rank * R + d), lane);
@@ -364,19 +414,25 @@ __global__ void __launch_bounds__(kSortThreads, 2) embedding_sort_kernel(SortArg
     if (tid < R) start[tid] = base + s - all + before;
     __syncthreads();
     // each warp places its tokens in order; lanes of one digit by lane
-    for (int64_t i = i0; i < i1; i += 32) {
-      const bool in = i + lane < i1;
-      const uint2 e = in ? fetch(i + lane) : make_uint2(0, 0);
-      const uint32_t digit = in ? (e.x >> shift) & (R - 1) : R;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      const int before_me = __popc(same & ((1u << lane) - 1u));
-      if (in) {
-        const uint32_t at = start[digit] + mine[digit] + before_me;
-        if (in_range(at, a.N, a.status)) __stcg(dst + at, e);
+    for (int64_t i = i0 + lane; i - lane < i1; i += 32 * kSortAhead) {
+      uint2 e[kSortAhead];
+#pragma unroll
+      for (int k = 0; k < kSortAhead; ++k)
+        e[k] = i + 32 * k < i1 ? fetch(i + 32 * k) : make_uint2(0, 0);
+#pragma unroll
+      for (int k = 0; k < kSortAhead; ++k) {
+        const bool in = i + 32 * k < i1;
+        const uint32_t digit = in ? (e[k].x >> shift) & (R - 1) : R;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        const int before_me = __popc(same & ((1u << lane) - 1u));
+        if (in) {
+          const uint32_t at = start[digit] + mine[digit] + before_me;
+          if (in_range(at, a.N, a.status)) __stcg(dst + at, e[k]);
+        }
+        __syncwarp();
+        if (in && before_me == 0) mine[digit] += __popc(same);
+        __syncwarp();
       }
-      __syncwarp();
-      if (in && before_me == 0) mine[digit] += __popc(same);
-      __syncwarp();
     }
     cluster_sync();
   }
@@ -411,32 +467,53 @@ struct ReduceArgs {
   int accumulate;
   int chunk;
   int64_t chunks, tiles;
-  float* part;      // [chunks][2][D]
+  float* part;      // [chunks][2][tiles][kReduceThreads][kReduceLane]
   int32_t* ticket;  // [chunks][tiles]
   int32_t* status;
 };
+
+// First chunk of the run of id v that chunk c begins inside (the one whose
+// predecessor ends in another id); by one warp.
+__device__ __forceinline__ int64_t run_first_chunk(const ReduceArgs& a, int64_t c, uint32_t v) {
+  for (int64_t b = c - 1;; b -= 32) {
+    const int64_t q = b - (threadIdx.x & 31);
+    const bool stop = q <= 0 || a.sorted[q * a.chunk - 1].x != v;
+    const uint32_t m = __ballot_sync(0xffffffffu, stop);
+    if (m) return b - (__ffs(m) - 1);
+  }
+}
+
+// Last chunk of the run of id v that chunk c ends in or holds.
+__device__ __forceinline__ int64_t run_last_chunk(const ReduceArgs& a, int64_t c, uint32_t v) {
+  for (int64_t b = c;; b += 32) {
+    const int64_t q = b + (threadIdx.x & 31);
+    const bool stop = (q + 1) * a.chunk >= a.N || a.sorted[(q + 1) * a.chunk].x != v;
+    const uint32_t m = __ballot_sync(0xffffffffu, stop);
+    if (m) return b + __ffs(m) - 1;
+  }
+}
 
 template <typename T, typename G, int VEC>
 __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(ReduceArgs a) {
   constexpr int U = kReduceLane / VEC;
   __shared__ uint2 tok[kMaxChunk];
-  __shared__ int64_t run_first, run_last;
-  __shared__ int last;
-  const int tid = threadIdx.x;
+  __shared__ int64_t run_first[2], run_last[2];
+  __shared__ int last[2];
+  const int tid = threadIdx.x, warp = tid >> 5;
   const T* dy = static_cast<const T*>(a.dy);
+  const uint32_t V = static_cast<uint32_t>(a.V);
   const int64_t items = a.chunks * a.tiles;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t c = item / a.tiles, tile = item - c * a.tiles;
     const int64_t col0 = tile * kReduceTile + tid * VEC;
     const int64_t t0 = c * a.chunk;
     const int n = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.N - t0));
-    __syncthreads();  // tok is free again
+    __syncthreads();  // tok and the run's words are free again
     for (int k = tid; k < n; k += kReduceThreads) tok[k] = a.sorted[t0 + k];
     const uint32_t none = 0xffffffffu;
     const uint32_t before = t0 > 0 ? a.sorted[t0 - 1].x : none;
     const uint32_t after = t0 + n < a.N ? a.sorted[t0 + n].x : none;
     __syncthreads();
-    const uint32_t V = static_cast<uint32_t>(a.V);
 
     auto out_row = [&](uint32_t v, const float (&acc)[U][VEC]) {
       G* g = static_cast<G*>(a.grad) + static_cast<int64_t>(v) * a.ldw;
@@ -464,11 +541,15 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(Reduce
         }
       }
     };
-    auto part_row = [&](int64_t chunk, int slot) { return a.part + (chunk * 2 + slot) * a.D; };
+    // this thread's eight columns of a chunk's partial sum, next to each other
+    auto part_of = [&](int64_t chunk, int slot) {
+      return reinterpret_cast<float4*>(
+          a.part + (((chunk * 2 + slot) * a.tiles + tile) * kReduceThreads + tid) * kReduceLane);
+    };
 
     float acc[U][VEC] = {};
     uint32_t key = tok[0].x;
-    bool first = true;  // the run that the chunk begins with
+    bool first = true;  // in the run that the chunk begins with
     int slots = 0;      // bit 0: partial of a run from before, bit 1: of one that goes on
     auto flush = [&](bool goes_on) {
       if (key == V) return;
@@ -477,19 +558,15 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(Reduce
         out_row(key, acc);
       } else {
         const int slot = from_before ? 0 : 1;
-        float* p = part_row(c, slot);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const int64_t j = col0 + u * kReduceThreads * VEC + e;
-            if (j < a.D) __stcg(p + j, acc[u][e]);
-          }
+        const float* f = &acc[0][0];
+        float4* p = part_of(c, slot);
+        __stcg(p, make_float4(f[0], f[1], f[2], f[3]));
+        __stcg(p + 1, make_float4(f[4], f[5], f[6], f[7]));
         slots |= 1 << slot;
       }
     };
     for (int k0 = 0; k0 < n; k0 += kReduceAhead) {
-      Vec<T, VEC> r[kReduceAhead][U];
+      RawVec<T, VEC> r[kReduceAhead][U];
 #pragma unroll
       for (int k = 0; k < kReduceAhead; ++k) {
         const bool in = k0 + k < n && tok[k0 + k].x != V;
@@ -497,13 +574,10 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(Reduce
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int64_t j = col0 + u * kReduceThreads * VEC;
-          if (in && j + VEC <= a.D) {
+          if (in && j + VEC <= a.D)
             r[k][u].load(row + j);
-          } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-              r[k][u].x[e] = in && j + e < a.D ? Elem<T>::load(row + j + e) : 0.0f;
-          }
+          else
+            r[k][u].load_part(row + j, in ? a.D - j : 0);
         }
       }
 #pragma unroll
@@ -520,69 +594,58 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(Reduce
               for (int e = 0; e < VEC; ++e) acc[u][e] = 0.0f;
           }
 #pragma unroll
-          for (int u = 0; u < U; ++u)
+          for (int u = 0; u < U; ++u) {
+            float x[VEC];
+            r[k][u].unpack(x);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[u][e] += r[k][u].x[e];
+            for (int e = 0; e < VEC; ++e) acc[u][e] += x[e];
+          }
         }
       }
     }
     flush(key == after);
 
     // runs over several chunks: the last CTA to arrive adds the partial sums
+    if (slots == 0) continue;  // the same for all threads
+    __threadfence();
+    __syncthreads();
+    if (warp < 2 && (slots >> warp & 1)) {
+      const uint32_t v = warp == 0 ? before : key;
+      const int64_t lo = warp == 0 ? run_first_chunk(a, c, v) : c;
+      const int64_t hi = run_last_chunk(a, c, v);
+      if ((tid & 31) == 0) {
+        run_first[warp] = lo;
+        run_last[warp] = hi;
+        last[warp] = atomicAdd(a.ticket + lo * a.tiles + tile, 1) == static_cast<int>(hi - lo);
+      }
+    }
+    __syncthreads();
+#pragma unroll
     for (int slot = 0; slot < 2; ++slot) {
-      if (!(slots & (1 << slot))) continue;  // the same for all threads
-      const uint32_t v = slot == 0 ? before : key;
+      if (!(slots >> slot & 1) || !last[slot]) continue;
       __threadfence();
-      __syncthreads();
-      if (tid < 32) {
-        // first chunk: the one whose predecessor ends in another id
-        int64_t lo = c;
-        if (slot == 0) {
-          for (int64_t b = c - 1;; b -= 32) {
-            const int64_t q = b - tid;
-            const bool stop = q <= 0 || a.sorted[q * a.chunk - 1].x != v;
-            const uint32_t m = __ballot_sync(0xffffffffu, stop);
-            if (m) {
-              lo = b - (__ffs(m) - 1);
-              break;
-            }
+      float sum[U][VEC] = {};
+      float* f = &sum[0][0];
+      constexpr int kAhead = 4;
+      for (int64_t q0 = run_first[slot]; q0 <= run_last[slot]; q0 += kAhead) {
+        float4 lo4[kAhead], hi4[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int64_t q = q0 + k;
+          lo4[k] = hi4[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (q <= run_last[slot]) {
+            const float4* p = part_of(q, q == run_first[slot] ? 1 : 0);
+            lo4[k] = __ldcg(p);
+            hi4[k] = __ldcg(p + 1);
           }
         }
-        // last chunk: the one whose successor begins with another id
-        int64_t hi = c;
-        for (int64_t b = c;; b += 32) {
-          const int64_t q = b + tid;
-          const bool stop = (q + 1) * a.chunk >= a.N || a.sorted[(q + 1) * a.chunk].x != v;
-          const uint32_t m = __ballot_sync(0xffffffffu, stop);
-          if (m) {
-            hi = b + __ffs(m) - 1;
-            break;
-          }
-        }
-        if (tid == 0) {
-          run_first = lo;
-          run_last = hi;
-          const int arrived = atomicAdd(a.ticket + lo * a.tiles + tile, 1);
-          last = arrived == static_cast<int>(hi - lo);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          f[0] += lo4[k].x, f[1] += lo4[k].y, f[2] += lo4[k].z, f[3] += lo4[k].w;
+          f[4] += hi4[k].x, f[5] += hi4[k].y, f[6] += hi4[k].z, f[7] += hi4[k].w;
         }
       }
-      __syncthreads();
-      if (last) {
-        __threadfence();
-        float sum[U][VEC] = {};
-        for (int64_t q = run_first; q <= run_last; ++q) {
-          const float* p = part_row(q, q == run_first ? 1 : 0);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const int64_t j = col0 + u * kReduceThreads * VEC + e;
-              if (j < a.D) sum[u][e] += __ldcg(p + j);
-            }
-        }
-        out_row(v, sum);
-      }
-      __syncthreads();  // run_first, run_last and last are free again
+      out_row(slot == 0 ? before : key, sum);
     }
   }
 }
@@ -600,24 +663,38 @@ static void launch_reduce(const ReduceArgs& a, int vec, cudaStream_t s) {
 }
 
 static size_t sort_smem(int bits) {
-  const size_t sort = sizeof(uint32_t) * (size_t(1) << bits) * (kSortWarps + kMaxSortCtas + 1);
+  const size_t R = size_t(1) << bits;
+  const size_t sort = sizeof(uint32_t) * ((R + 1) * kSortWarps + R * (kMaxSortCtas + 1));
   return std::max<size_t>(sort, kFillRows / 8);
 }
 
-static int launch_sort(const SortArgs& a, cudaStream_t s) {
-  static std::atomic<uint64_t> raised{0};
+// Clusters of the sort's launch that run at once on the current device.
+static int sort_clusters(cudaLaunchConfig_t cfg, int* clusters) {
+  static std::atomic<int> cache[64][4][kMaxDigitBits + 1];
   int dev = 0;
   int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
   if (rc != FLCE_OK) return rc;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(raised.load() & bit)) {
+  int c = 0, bits = 1;
+  while ((2 << c) <= static_cast<int>(cfg.attrs[0].val.clusterDim.x)) ++c;
+  while (bits < kMaxDigitBits && sort_smem(bits) < cfg.dynamicSmemBytes) ++bits;
+  std::atomic<int>& known = cache[dev & 63][c][bits];
+  if (known.load() == 0) {
     rc = cuda_status(cudaFuncSetAttribute(embedding_sort_kernel,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(sort_smem(kMaxDigitBits))),
                      "cudaFuncSetAttribute(embedding_sort_kernel)");
     if (rc != FLCE_OK) return rc;
-    raised.fetch_or(bit);
+    int n = 0;
+    rc = cuda_status(cudaOccupancyMaxActiveClusters(&n, embedding_sort_kernel, &cfg),
+                     "cudaOccupancyMaxActiveClusters(embedding_sort_kernel)");
+    if (rc != FLCE_OK) return rc;
+    known.store(std::max(n, 2));
   }
+  *clusters = known.load();
+  return FLCE_OK;
+}
+
+static int launch_sort(const SortArgs& a, cudaStream_t s) {
   const int C = sort_ctas(a.N);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -625,13 +702,16 @@ static int launch_sort(const SortArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.x = static_cast<unsigned>(C);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  const int fill = a.grad != nullptr ? std::max(1, sm_count() / C) * C : 0;
-  cfg.gridDim = dim3(static_cast<unsigned>(C + fill), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(C), 1, 1);
   cfg.blockDim = dim3(kSortThreads, 1, 1);
   cfg.dynamicSmemBytes = sort_smem(a.bits);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  int clusters = 1;
+  const int rc = sort_clusters(cfg, &clusters);
+  if (rc != FLCE_OK) return rc;
+  if (a.grad != nullptr) cfg.gridDim.x = static_cast<unsigned>(C * clusters);
   return cuda_status(cudaLaunchKernelEx(&cfg, embedding_sort_kernel, a),
                      "cudaLaunchKernelEx(embedding_sort_kernel)");
 }
@@ -645,7 +725,7 @@ static BwdWorkspace bwd_workspace(int64_t N, int64_t D) {
   BwdWorkspace w;
   w.buf = round_up(static_cast<size_t>(N) * sizeof(uint2), 256);
   w.ticket = round_up(static_cast<size_t>(r.chunks * r.tiles) * sizeof(int32_t), 256);
-  w.part = round_up(static_cast<size_t>(r.chunks) * 2 * static_cast<size_t>(D) * 4, 256);
+  w.part = static_cast<size_t>(r.chunks * r.tiles) * 2 * kReduceTile * sizeof(float);
   w.total = 2 * w.buf + w.ticket + w.part;
   return w;
 }
