@@ -53,19 +53,6 @@ struct RawVec {
       w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
   }
-  // the first `left` elements (none when left <= 0), zeros after them
-  __device__ __forceinline__ void load_part(const T* p, int64_t left) {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) w[k] = 0u;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if (e >= left) continue;
-      if constexpr (sizeof(T) == 4)
-        w[e] = reinterpret_cast<const uint32_t*>(p)[e];
-      else
-        w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[e]) << (16 * (e & 1));
-    }
-  }
   __device__ __forceinline__ void unpack(float (&x)[VEC]) const {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -78,27 +65,20 @@ struct RawVec {
 };
 
 // VEC fp32 values stored as type G in accesses of at most 16 bytes.
-template <typename G, int VEC>
-__device__ __forceinline__ void load_as(const G* p, float (&x)[VEC]) {
-  constexpr int W = VEC < Elem<G>::kPerVec ? VEC : Elem<G>::kPerVec;
+// p[k] += x[k] at the memory, without waiting for the old values.  Each element
+// of a gradient is added to once per call, so the result does not depend on the
+// order of the adds.
+template <int VEC>
+__device__ __forceinline__ void add_to(float* p, const float (&x)[VEC]) {
+  if constexpr (VEC % 4 == 0) {
 #pragma unroll
-  for (int k = 0; k < VEC; k += W) {
-    if constexpr (W == 2 && sizeof(G) == 4) {
-      const float2 v = *reinterpret_cast<const float2*>(p + k);
-      x[k] = v.x;
-      x[k + 1] = v.y;
-    } else if constexpr (W == 4 && sizeof(G) == 2) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p + k);
-      x[k] = bf16_lo(v.x);
-      x[k + 1] = bf16_hi(v.x);
-      x[k + 2] = bf16_lo(v.y);
-      x[k + 3] = bf16_hi(v.y);
-    } else {
-      Vec<G, W> v;
-      v.load(p + k);
+    for (int k = 0; k < VEC; k += 4)
+      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + k), "f"(x[k]),
+                   "f"(x[k + 1]), "f"(x[k + 2]), "f"(x[k + 3])
+                   : "memory");
+  } else {
 #pragma unroll
-      for (int e = 0; e < W; ++e) x[k + e] = v.x[e];
-    }
+    for (int k = 0; k < VEC; ++k) atomicAdd(p + k, x[k]);
   }
 }
 
@@ -121,14 +101,15 @@ __device__ __forceinline__ void store_as(G* p, const float (&x)[VEC]) {
   }
 }
 
-// Elements per access that two row matrices allow: base addresses and row
-// strides of both are multiples of it (the columns' tail is masked).
-static int vec_width(const void* p, int dt, int64_t ld, const void* q, int dtq, int64_t ldq) {
+// Elements per access that two row matrices allow: base addresses, row strides
+// and, where the kernel has no tail, the columns (else D = 0) are multiples of it.
+static int vec_width(int64_t D, const void* p, int dt, int64_t ld, const void* q, int dtq,
+                     int64_t ldq) {
   const int most = dt == FLCE_BF16 ? 8 : 4;
   for (int v = most; v > 1; v = v == 8 ? 2 : 1) {
     // an access to q of v elements is split into 16-byte ones
     const size_t a = dtype_size(dt) * v, b = std::min<size_t>(dtype_size(dtq) * v, 16);
-    if (aligned(p, a) && ld % v == 0 && aligned(q, b) && ldq % v == 0) return v;
+    if (D % v == 0 && aligned(p, a) && ld % v == 0 && aligned(q, b) && ldq % v == 0) return v;
   }
   return 1;
 }
@@ -213,7 +194,7 @@ static void launch_fwd(const int64_t* ids, const void* W, int64_t N, int64_t D, 
   const int64_t pieces = (D + 32 * kLookupLane - 1) / (32 * kLookupLane);
   constexpr int kWarps = kLookupThreads / 32;
   const int64_t need = (N * pieces + kWarps - 1) / kWarps;
-  const int grid = static_cast<int>(std::min<int64_t>(need, sm_count() * 16));
+  const int grid = static_cast<int>(std::min<int64_t>(need, int64_t(1) << 30));
   embedding_fwd_kernel<T, VEC><<<grid, kLookupThreads, 0, s>>>(
       ids, static_cast<const T*>(W), N, D, V, ldw, scale, static_cast<T*>(out), ldo, pieces,
       status);
@@ -274,46 +255,65 @@ struct SortArgs {
   int32_t* status;
 };
 
-// Zeros for the rows of [v0, v1) that no id names.
-__device__ void fill_unnamed_rows(const SortArgs& a, int64_t v0, int64_t v1, uint32_t* mark) {
-  const int tid = threadIdx.x;
-  const int n = static_cast<int>(v1 - v0);
-  for (int k = tid; k < (n + 31) / 32; k += kSortThreads) mark[k] = 0;
+// The key a token is sorted by: its id, or V (after every id) when it
+// contributes nothing.
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t id, bool* ok) {
+  *ok = label_ok(id, a.V);
+  return static_cast<uint32_t>(*ok && id != a.padding_idx ? id : a.V);
+}
+
+// Bitmap of the rows of [v0, v1) that some token names.
+__device__ __forceinline__ void mark_row(uint32_t* mark, int64_t v0, int64_t v1, uint32_t key) {
+  if (key >= v0 && key < v1) atomicOr(&mark[(key - v0) >> 5], 1u << ((key - v0) & 31));
+}
+
+__device__ void mark_rows(const SortArgs& a, int64_t v0, int64_t v1, uint32_t* mark) {
+  for (int k = threadIdx.x; k < (v1 - v0 + 31) / 32; k += kSortThreads) mark[k] = 0;
   __syncthreads();
-  for (int64_t i = tid; i < a.N; i += kSortThreads) {
-    const int64_t id = a.ids[i];
-    if (id >= v0 && id < v1 && id != a.padding_idx)
-      atomicOr(&mark[(id - v0) >> 5], 1u << ((id - v0) & 31));
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < a.N; i += kSortThreads) {
+    bool ok;
+    mark_row(mark, v0, v1, sort_key(a, a.ids[i], &ok));
   }
   __syncthreads();
+}
+
+// Zeros for the rows of [v0, v1) that are not marked.  A warp takes the next
+// rows from *next (shared, 0 at the start), so warps may join at any time.
+__device__ void zero_rows(const SortArgs& a, int64_t v0, int64_t v1, const uint32_t* mark,
+                          int* next) {
+  const int lane = threadIdx.x & 31;
+  const int n = static_cast<int>(v1 - v0);
   const int64_t row_bytes = a.D * a.grad_es;
   const int64_t ld_bytes = a.ldw * a.grad_es;
   char* g = static_cast<char*>(a.grad) + v0 * ld_bytes;
-  if (((reinterpret_cast<uintptr_t>(g) | row_bytes | ld_bytes) & 15) == 0) {
-    const int64_t per = row_bytes / 16;
-    if (per >= 128) {
-      // a warp per row at a time
-      for (int r = tid >> 5; r < n; r += kSortWarps) {
-        if ((mark[r >> 5] >> (r & 31)) & 1u) continue;
-        uint4* p = reinterpret_cast<uint4*>(g + r * ld_bytes);
-        for (int64_t k = tid & 31; k < per; k += 32) __stcs(p + k, make_uint4(0, 0, 0, 0));
+  // at least 4 KB at a time
+  const int take = static_cast<int>(max(int64_t(1), min(int64_t(64), 4096 / row_bytes)));
+  while (true) {
+    int r0 = 0;
+    if (lane == 0) r0 = atomicAdd(next, take);
+    r0 = __shfl_sync(0xffffffffu, r0, 0);
+    if (r0 >= n) return;
+    const int r1 = min(n, r0 + take);
+    for (int r = r0; r < r1; ++r) {
+      if ((mark[r >> 5] >> (r & 31)) & 1u) continue;
+      // whole 16-byte blocks, and the elements before and after them
+      char* p = g + r * ld_bytes;
+      const int64_t head = min(
+          row_bytes, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15));
+      char* end = p + row_bytes;
+      char* first = p + head;
+      char* last = first + (row_bytes - head) / 16 * 16;
+      for (char* q = first + 16 * lane; q < last; q += 512)
+        __stcs(reinterpret_cast<uint4*>(q), make_uint4(0, 0, 0, 0));
+      const int edge = lane < 8 ? lane : lane - 8;
+      char* q = (lane < 8 ? p : last) + edge * a.grad_es;
+      if (lane < 16 && q < (lane < 8 ? first : end)) {
+        if (a.grad_es == 4)
+          *reinterpret_cast<uint32_t*>(q) = 0u;
+        else
+          *reinterpret_cast<uint16_t*>(q) = 0;
       }
-      return;
-    }
-    for (int64_t k = tid; k < n * per; k += kSortThreads) {
-      const int64_t r = k / per;
-      if (!((mark[r >> 5] >> (r & 31)) & 1u))
-        __stcs(reinterpret_cast<uint4*>(g + r * ld_bytes) + (k - r * per), make_uint4(0, 0, 0, 0));
-    }
-    return;
-  }
-  for (int r = tid >> 5; r < n; r += kSortWarps) {
-    if ((mark[r >> 5] >> (r & 31)) & 1u) continue;
-    char* p = g + r * ld_bytes;
-    if (a.grad_es == 4) {
-      for (int64_t k = tid & 31; k < a.D; k += 32) reinterpret_cast<uint32_t*>(p)[k] = 0u;
-    } else {
-      for (int64_t k = tid & 31; k < a.D; k += 32) reinterpret_cast<uint16_t*>(p)[k] = 0;
     }
   }
 }
@@ -321,6 +321,7 @@ __device__ void fill_unnamed_rows(const SortArgs& a, int64_t v0, int64_t v1, uin
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a) {
   extern __shared__ uint32_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int next_row;
   const int C = static_cast<int>(cluster_nctarank());
   const int rank = static_cast<int>(cluster_ctarank());
   if (blockIdx.x >= static_cast<unsigned>(C)) {
@@ -330,7 +331,9 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
     const int64_t per = (a.V + parts - 1) / parts;
     const int64_t end = min(a.V, (me + 1) * per);
     for (int64_t v = me * per; v < end; v += kFillRows) {
-      fill_unnamed_rows(a, v, min(end, v + kFillRows), smem);
+      if (tid == 0) next_row = 0;
+      mark_rows(a, v, min(end, v + kFillRows), smem);
+      zero_rows(a, v, min(end, v + kFillRows), smem, &next_row);
       __syncthreads();
     }
     return;
@@ -353,11 +356,10 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
     const int shift = pass * a.bits;
     auto fetch = [&](int64_t i) -> uint2 {
       if (pass > 0) return __ldcg(src + i);
-      const int64_t id = a.ids[i];
-      const bool ok = label_ok(id, a.V);
+      bool ok;
+      const uint32_t key = sort_key(a, a.ids[i], &ok);
       if (!ok) set_status(a.status, FLCE_ELABEL);
-      return make_uint2(static_cast<uint32_t>(ok && id != a.padding_idx ? id : a.V),
-                        static_cast<uint32_t>(i));
+      return make_uint2(key, static_cast<uint32_t>(i));
     };
     for (int k = tid; k < kSortWarps * S; k += kSortThreads) count[k] = 0;
     __syncthreads();
@@ -438,23 +440,113 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
   }
 }
 
-constexpr int kReduceThreads = 128;
+// The sort of up to kRankShare tokens per SM: every CTA finds the places of its
+// share of the tokens by itself.  It orders its share, then runs over all ids
+// and looks up by bisection between which of its tokens each belongs; the
+// running sum of these counts is the number of tokens before each of its own.
+// No passes, and no CTA waits for another.  Where rows are to be filled, half of
+// the warps start on that at once and the others join them.
+// The work grows with N times the bisection's steps on every SM, the cluster's
+// sort with N alone but it starts higher: 8192 tokens 10.7 against 20 us, 32768
+// tokens 49 against 28 us (with the launch, cold caches).
+constexpr int kRankShare = 128;
+
+__global__ void __launch_bounds__(kSortThreads) embedding_rank_kernel(SortArgs a) {
+  __shared__ uint64_t own[kRankShare], ordered[kRankShare];
+  __shared__ uint32_t before[kRankShare + 1];
+  __shared__ uint32_t mark[kFillRows / 32];
+  __shared__ int next_row;
+  const int tid = threadIdx.x;
+  for (int64_t k = blockIdx.x * int64_t(kSortThreads) + tid; k < a.tickets;
+       k += gridDim.x * int64_t(kSortThreads))
+    a.ticket[k] = 0;
+  const int64_t rows = (a.V + gridDim.x - 1) / gridDim.x;
+  const int64_t v0 = min(a.V, blockIdx.x * rows), v_end = min(a.V, v0 + rows);
+  const int64_t v1 = min(v_end, v0 + kFillRows);
+  const bool fill = a.grad != nullptr;
+  int team = kSortThreads;  // threads that sort
+  if (fill) {
+    if (tid == 0) next_row = 0;
+    mark_rows(a, v0, v1, mark);
+    team = kSortThreads / 2;
+  }
+  if (tid < team) {
+    const int64_t share = (a.N + gridDim.x - 1) / gridDim.x;
+    const int64_t t0 = blockIdx.x * share;
+    const int m = static_cast<int>(max(int64_t(0), min(share, a.N - t0)));
+    if (tid <= kRankShare) before[tid] = 0;
+    // a token as one number: by key, then by index
+    uint64_t e = 0;
+    if (tid < m) {
+      bool ok;
+      const uint32_t key = sort_key(a, a.ids[t0 + tid], &ok);
+      if (!ok) set_status(a.status, FLCE_ELABEL);
+      e = static_cast<uint64_t>(key) << 32 | static_cast<uint64_t>(t0 + tid);
+      own[tid] = e;
+    }
+    named_barrier(1, team);
+    if (tid < m) {
+      int r = 0;
+      for (int j = 0; j < m; ++j) r += own[j] < e;
+      ordered[r] = e;
+    }
+    named_barrier(1, team);
+    if (m > 0) {
+#pragma unroll 4
+      for (int64_t i = tid; i < a.N; i += team) {
+        bool ok;
+        const uint32_t key = sort_key(a, a.ids[i], &ok);
+        const uint64_t x = static_cast<uint64_t>(key) << 32 | static_cast<uint64_t>(i);
+        int lo = 0;  // number of own tokens up to x
+#pragma unroll
+        for (int step = kRankShare / 2; step > 0; step /= 2)
+          if (lo + step <= m && ordered[lo + step - 1] <= x) lo += step;
+        if (lo < m && ordered[lo] <= x) ++lo;
+        if (lo < m) atomicAdd(&before[lo], 1u);
+      }
+    }
+    named_barrier(1, team);
+    if (tid < m) {
+      uint32_t s = 0;
+      for (int j = 0; j <= tid; ++j) s += before[j];
+      if (in_range(s, a.N, a.status))
+        a.buf0[s] = make_uint2(static_cast<uint32_t>(ordered[tid] >> 32),
+                               static_cast<uint32_t>(ordered[tid]));
+    }
+  }
+  if (!fill) return;
+  zero_rows(a, v0, v1, mark, &next_row);
+  for (int64_t v = v1; v < v_end; v += kFillRows) {
+    __syncthreads();
+    if (tid == 0) next_row = 0;
+    mark_rows(a, v, min(v_end, v + kFillRows), mark);
+    zero_rows(a, v, min(v_end, v + kFillRows), mark, &next_row);
+  }
+}
+
 constexpr int kReduceLane = 8;  // columns per thread
-constexpr int kReduceTile = kReduceThreads * kReduceLane;
-constexpr int kMaxChunk = 256;
+constexpr int kMinChunk = 16, kMaxChunk = 128;
 constexpr int kReduceAhead = 8;  // token rows loaded together
 
 struct ReducePlan {
-  int chunk;        // tokens per chunk, a power of two
+  int chunk;        // tokens per chunk, a multiple of kReduceAhead
   int64_t chunks, tiles;
 };
 
-// About eight blocks for each SM; longer chunks for more tokens.
+// Threads of a block: one warp for rows it can hold alone.
+static int reduce_threads(int64_t D) { return D <= 32 * kReduceLane ? 32 : 128; }
+
+// One wave of blocks (24 warps to an SM) while a chunk stays within kMaxChunk
+// tokens, and no chunk shorter than sqrt(N / 8) tokens: a run over an eighth of
+// all tokens is then joined from as many partial sums as a chunk has tokens.
 static ReducePlan reduce_plan(int64_t N, int64_t D) {
-  const int64_t tiles = (D + kReduceTile - 1) / kReduceTile;
-  int chunk = 8;
-  while (chunk < kMaxChunk && N * tiles > int64_t(1216) * chunk) chunk *= 2;
-  return {chunk, (N + chunk - 1) / chunk, tiles};
+  const int64_t tile = reduce_threads(D) * kReduceLane;
+  const int64_t tiles = (D + tile - 1) / tile;
+  const int64_t wave = 152 * 24 * 32 / reduce_threads(D);
+  int64_t chunk = std::max<int64_t>(kMinChunk, (N * tiles + wave - 1) / wave);
+  while (chunk < kMaxChunk && chunk * chunk < N / 8) ++chunk;
+  chunk = std::min<int64_t>(kMaxChunk, (chunk + kReduceAhead - 1) / kReduceAhead * kReduceAhead);
+  return {static_cast<int>(chunk), (N + chunk - 1) / chunk, tiles};
 }
 
 struct ReduceArgs {
@@ -467,84 +559,83 @@ struct ReduceArgs {
   int accumulate;
   int chunk;
   int64_t chunks, tiles;
-  float* part;      // [chunks][2][tiles][kReduceThreads][kReduceLane]
+  float* part;      // [chunks][2][tiles][threads of a block][kReduceLane]
   int32_t* ticket;  // [chunks][tiles]
   int32_t* status;
 };
 
 // First chunk of the run of id v that chunk c begins inside (the one whose
-// predecessor ends in another id); by one warp.
-__device__ __forceinline__ int64_t run_first_chunk(const ReduceArgs& a, int64_t c, uint32_t v) {
+// predecessor ends in another id), by one warp.  `word` is the lane's first
+// candidate, the id that ends chunk c - 2 - lane.
+__device__ __forceinline__ int64_t run_first_chunk(const ReduceArgs& a, int64_t c, uint32_t v,
+                                                   uint32_t word) {
   for (int64_t b = c - 1;; b -= 32) {
     const int64_t q = b - (threadIdx.x & 31);
-    const bool stop = q <= 0 || a.sorted[q * a.chunk - 1].x != v;
-    const uint32_t m = __ballot_sync(0xffffffffu, stop);
+    if (b != c - 1 && q > 0) word = a.sorted[q * a.chunk - 1].x;
+    const uint32_t m = __ballot_sync(0xffffffffu, q <= 0 || word != v);
     if (m) return b - (__ffs(m) - 1);
   }
 }
 
-// Last chunk of the run of id v that chunk c ends in or holds.
-__device__ __forceinline__ int64_t run_last_chunk(const ReduceArgs& a, int64_t c, uint32_t v) {
+// Last chunk of the run of id v that chunk c ends in or holds; `word` is the id
+// that begins chunk c + 1 + lane.
+__device__ __forceinline__ int64_t run_last_chunk(const ReduceArgs& a, int64_t c, uint32_t v,
+                                                  uint32_t word) {
   for (int64_t b = c;; b += 32) {
-    const int64_t q = b + (threadIdx.x & 31);
-    const bool stop = (q + 1) * a.chunk >= a.N || a.sorted[(q + 1) * a.chunk].x != v;
-    const uint32_t m = __ballot_sync(0xffffffffu, stop);
+    const int64_t at = (b + (threadIdx.x & 31) + 1) * a.chunk;
+    if (b != c && at < a.N) word = a.sorted[at].x;
+    const uint32_t m = __ballot_sync(0xffffffffu, at >= a.N || word != v);
     if (m) return b + __ffs(m) - 1;
   }
 }
 
-template <typename T, typename G, int VEC>
-__global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(ReduceArgs a) {
+template <typename T, typename G, int VEC, int kThreads>
+__global__ void __launch_bounds__(kThreads, VEC == 8 ? 24 * 32 / kThreads : 1)
+    embedding_reduce_kernel(ReduceArgs a) {
   constexpr int U = kReduceLane / VEC;
+  constexpr int kTile = kThreads * kReduceLane;
   __shared__ uint2 tok[kMaxChunk];
   __shared__ int64_t run_first[2], run_last[2];
   __shared__ int last[2];
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* dy = static_cast<const T*>(a.dy);
   const uint32_t V = static_cast<uint32_t>(a.V);
   const int64_t items = a.chunks * a.tiles;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t c = item / a.tiles, tile = item - c * a.tiles;
-    const int64_t col0 = tile * kReduceTile + tid * VEC;
+    const int64_t col0 = tile * kTile + tid * VEC;
     const int64_t t0 = c * a.chunk;
     const int n = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.N - t0));
     __syncthreads();  // tok and the run's words are free again
-    for (int k = tid; k < n; k += kReduceThreads) tok[k] = a.sorted[t0 + k];
+    for (int k = tid; k < n; k += kThreads) tok[k] = a.sorted[t0 + k];
     const uint32_t none = 0xffffffffu;
     const uint32_t before = t0 > 0 ? a.sorted[t0 - 1].x : none;
     const uint32_t after = t0 + n < a.N ? a.sorted[t0 + n].x : none;
+    // the ends of the chunks next to this one, for runs that leave it
+    const int64_t prev_at = (c - 1 - lane) * a.chunk - 1, next_at = (c + 1 + lane) * a.chunk;
+    const uint32_t prev_word = prev_at >= 0 ? a.sorted[prev_at].x : none;
+    const uint32_t next_word = next_at < a.N ? a.sorted[next_at].x : none;
     __syncthreads();
 
     auto out_row = [&](uint32_t v, const float (&acc)[U][VEC]) {
       G* g = static_cast<G*>(a.grad) + static_cast<int64_t>(v) * a.ldw;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t j = col0 + u * kReduceThreads * VEC;
+        const int64_t j = col0 + u * kThreads * VEC;
+        if (j >= a.D) break;  // D is a multiple of VEC
         float r[VEC];
-        if (j + VEC <= a.D) {
-          if (a.accumulate) {
-            load_as<G, VEC>(g + j, r);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) r[e] += acc[u][e] * a.scale;
-          } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) r[e] = acc[u][e] * a.scale;
-          }
+        for (int e = 0; e < VEC; ++e) r[e] = acc[u][e] * a.scale;
+        if (a.accumulate)
+          add_to<VEC>(reinterpret_cast<float*>(g + j), r);
+        else
           store_as<G, VEC>(g + j, r);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (j + e < a.D) {
-              const float old = a.accumulate ? Elem<G>::load(g + j + e) : 0.0f;
-              Elem<G>::store(g + j + e, old + acc[u][e] * a.scale);
-            }
-        }
       }
     };
     // this thread's eight columns of a chunk's partial sum, next to each other
     auto part_of = [&](int64_t chunk, int slot) {
       return reinterpret_cast<float4*>(
-          a.part + (((chunk * 2 + slot) * a.tiles + tile) * kReduceThreads + tid) * kReduceLane);
+          a.part + (((chunk * 2 + slot) * a.tiles + tile) * kThreads + tid) * kReduceLane);
     };
 
     float acc[U][VEC] = {};
@@ -566,19 +657,15 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(Reduce
       }
     };
     for (int k0 = 0; k0 < n; k0 += kReduceAhead) {
+      // loads without conditions: past the chunk's end its last token again, past
+      // the last column the last ones again (neither is used), and the rows of
+      // tokens that contribute nothing (their run, the key V, is never written)
       RawVec<T, VEC> r[kReduceAhead][U];
 #pragma unroll
       for (int k = 0; k < kReduceAhead; ++k) {
-        const bool in = k0 + k < n && tok[k0 + k].x != V;
-        const T* row = dy + static_cast<int64_t>(in ? tok[k0 + k].y : 0) * a.ldg;
+        const T* row = dy + static_cast<int64_t>(tok[min(k0 + k, n - 1)].y) * a.ldg;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t j = col0 + u * kReduceThreads * VEC;
-          if (in && j + VEC <= a.D)
-            r[k][u].load(row + j);
-          else
-            r[k][u].load_part(row + j, in ? a.D - j : 0);
-        }
+        for (int u = 0; u < U; ++u) r[k][u].load(row + min(col0 + u * kThreads * VEC, a.D - VEC));
       }
 #pragma unroll
       for (int k = 0; k < kReduceAhead; ++k) {
@@ -609,14 +696,17 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(Reduce
     if (slots == 0) continue;  // the same for all threads
     __threadfence();
     __syncthreads();
-    if (warp < 2 && (slots >> warp & 1)) {
-      const uint32_t v = warp == 0 ? before : key;
-      const int64_t lo = warp == 0 ? run_first_chunk(a, c, v) : c;
-      const int64_t hi = run_last_chunk(a, c, v);
-      if ((tid & 31) == 0) {
-        run_first[warp] = lo;
-        run_last[warp] = hi;
-        last[warp] = atomicAdd(a.ticket + lo * a.tiles + tile, 1) == static_cast<int>(hi - lo);
+    // one warp for each of the two runs, or one for both
+#pragma unroll
+    for (int slot = 0; slot < 2; ++slot) {
+      if (warp != (kThreads > 32 ? slot : 0) || !(slots >> slot & 1)) continue;
+      const uint32_t v = slot == 0 ? before : key;
+      const int64_t lo = slot == 0 ? run_first_chunk(a, c, v, prev_word) : c;
+      const int64_t hi = run_last_chunk(a, c, v, next_word);
+      if (lane == 0) {
+        run_first[slot] = lo;
+        run_last[slot] = hi;
+        last[slot] = atomicAdd(a.ticket + lo * a.tiles + tile, 1) == static_cast<int>(hi - lo);
       }
     }
     __syncthreads();
@@ -626,7 +716,7 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(Reduce
       __threadfence();
       float sum[U][VEC] = {};
       float* f = &sum[0][0];
-      constexpr int kAhead = 4;
+      constexpr int kAhead = 8;
       for (int64_t q0 = run_first[slot]; q0 <= run_last[slot]; q0 += kAhead) {
         float4 lo4[kAhead], hi4[kAhead];
 #pragma unroll
@@ -650,16 +740,23 @@ __global__ void __launch_bounds__(kReduceThreads) embedding_reduce_kernel(Reduce
   }
 }
 
-template <typename T, typename G>
-static void launch_reduce(const ReduceArgs& a, int vec, cudaStream_t s) {
+template <typename T, typename G, int VEC, int kThreads>
+static int launch_reduce_k(const ReduceArgs& a, cudaStream_t s) {
   const unsigned grid =
       static_cast<unsigned>(std::min<int64_t>(a.chunks * a.tiles, int64_t(1) << 30));
-  if (vec == Elem<T>::kPerVec)
-    embedding_reduce_kernel<T, G, Elem<T>::kPerVec><<<grid, kReduceThreads, 0, s>>>(a);
-  else if (vec == 2 && sizeof(T) == 2)
-    embedding_reduce_kernel<T, G, sizeof(T) == 2 ? 2 : 1><<<grid, kReduceThreads, 0, s>>>(a);
-  else
-    embedding_reduce_kernel<T, G, 1><<<grid, kReduceThreads, 0, s>>>(a);
+  embedding_reduce_kernel<T, G, VEC, kThreads><<<grid, kThreads, 0, s>>>(a);
+  return launch_status("embedding_reduce_kernel launch");
+}
+
+template <typename T, typename G>
+static int launch_reduce(const ReduceArgs& a, int vec, cudaStream_t s) {
+  constexpr int V16 = Elem<T>::kPerVec, V4 = sizeof(T) == 2 ? 2 : 1;
+  const bool narrow = reduce_threads(a.D) == 32;
+  if (vec == V16)
+    return narrow ? launch_reduce_k<T, G, V16, 32>(a, s) : launch_reduce_k<T, G, V16, 128>(a, s);
+  if (vec == 2)
+    return narrow ? launch_reduce_k<T, G, V4, 32>(a, s) : launch_reduce_k<T, G, V4, 128>(a, s);
+  return narrow ? launch_reduce_k<T, G, 1, 32>(a, s) : launch_reduce_k<T, G, 1, 128>(a, s);
 }
 
 static size_t sort_smem(int bits) {
@@ -725,7 +822,8 @@ static BwdWorkspace bwd_workspace(int64_t N, int64_t D) {
   BwdWorkspace w;
   w.buf = round_up(static_cast<size_t>(N) * sizeof(uint2), 256);
   w.ticket = round_up(static_cast<size_t>(r.chunks * r.tiles) * sizeof(int32_t), 256);
-  w.part = static_cast<size_t>(r.chunks * r.tiles) * 2 * kReduceTile * sizeof(float);
+  w.part = static_cast<size_t>(r.chunks * r.tiles) * 2 * reduce_threads(D) * kReduceLane *
+           sizeof(float);
   w.total = 2 * w.buf + w.ticket + w.part;
   return w;
 }
@@ -748,7 +846,7 @@ extern "C" int embedding_fwd(const int64_t* ids, const void* W, int dt, int64_t 
   if (overlap(W, span_bytes(V, D, ldw, es), out, span_bytes(N, D, ldo, es))) return FLCE_EINVAL;
   if (N == 0) return FLCE_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int vec = vec_width(W, dt, ldw, out, dt, ldo);
+  const int vec = vec_width(0, W, dt, ldw, out, dt, ldo);
 #define FLCE_FWD(T, VEC) launch_fwd<T, VEC>(ids, W, N, D, V, ldw, scale, out, ldo, status, s)
   if (dt == FLCE_BF16) {
     if (vec == 8) FLCE_FWD(__nv_bfloat16, 8);
@@ -810,11 +908,17 @@ extern "C" int embedding_bwd(const int64_t* ids, const void* grad_out, int dt, i
   sa.ldw = ldw;
   sa.grad_es = static_cast<int>(dtype_size(dt_grad));
   sa.status = status;
-  rc = launch_sort(sa, s);
+  const bool rank = N <= int64_t(kRankShare) * sm_count();
+  if (rank) {
+    embedding_rank_kernel<<<sm_count(), kSortThreads, 0, s>>>(sa);
+    rc = launch_status("embedding_rank_kernel launch");
+  } else {
+    rc = launch_sort(sa, s);
+  }
   if (rc != FLCE_OK || N == 0) return rc;
 
   ReduceArgs ra{};
-  ra.sorted = (sp.passes & 1) ? sa.buf0 : sa.buf1;
+  ra.sorted = rank || (sp.passes & 1) ? sa.buf0 : sa.buf1;
   ra.dy = grad_out;
   ra.N = N;
   ra.D = D;
@@ -830,11 +934,10 @@ extern "C" int embedding_bwd(const int64_t* ids, const void* grad_out, int dt, i
   ra.ticket = sa.ticket;
   ra.part = reinterpret_cast<float*>(base + 2 * w.buf + w.ticket);
   ra.status = status;
-  const int vec = vec_width(grad_out, dt, ldg, grad_W, dt_grad, ldw);
+  const int vec = vec_width(D, grad_out, dt, ldg, grad_W, dt_grad, ldw);
   using B = __nv_bfloat16;
-  if (dt == FLCE_BF16 && dt_grad == FLCE_BF16) launch_reduce<B, B>(ra, vec, s);
-  else if (dt == FLCE_BF16) launch_reduce<B, float>(ra, vec, s);
-  else if (dt_grad == FLCE_BF16) launch_reduce<float, B>(ra, vec, s);
-  else launch_reduce<float, float>(ra, vec, s);
-  return launch_status("embedding_reduce_kernel launch");
+  if (dt == FLCE_BF16)
+    return dt_grad == FLCE_BF16 ? launch_reduce<B, B>(ra, vec, s) : launch_reduce<B, float>(ra, vec, s);
+  return dt_grad == FLCE_BF16 ? launch_reduce<float, B>(ra, vec, s)
+                              : launch_reduce<float, float>(ra, vec, s);
 }
