@@ -1,59 +1,452 @@
 // The head with 4-bit weights and group scales: logits of a few tokens, and
 // the rounding of a table to that layout.
 #include <algorithm>
+#include <atomic>
 
 #include "rows.cuh"
 
 namespace flce {
 
+// Logits.  Bound by the weights' bytes (V D / 2) for a few tokens.  Every weight
+// is read once, unpacked in registers and multiplied by tensor-core instructions
+// whose 16 rows are vocabulary rows and whose 8 columns are tokens, so up to 8
+// tokens cost the same instructions as one.
+//
+// A persistent block per SM keeps the tokens in shared memory as bf16 (all
+// columns, or a chunk of them at a time) and W warps that share nothing else:
+// each streams its own R tiles of 16 rows through a ring of S stages of 256
+// columns (128 bytes of each row, cp.async) without waiting for other warps.
+// Where there are fewer tiles than warps, WK warps split the columns of a tile
+// and add up their sums in warp order.
+//
+// In a stage a lane holds, for rows g and g + 8 of a tile (g = lane / 4), the
+// 32-bit words w = 0..3 of its t = lane % 4: word w of the four lanes covers the
+// columns 32 w .. 32 w + 31, so each pair of instructions stays within 32
+// columns and any group of 32, 64 or 128 columns can be scaled on its own.  A
+// word's nibble pairs (p, p + 4) become bf16 pairs by putting the nibble into the
+// mantissa of 128: 128 + q, and one fused multiply-add to (q - z) 2^-11, both
+// exact.  The power of two keeps a group's sum (up to 128 * 15 |x|) within fp32
+// for any x; the scales carry its inverse.
+
+constexpr int kStageCols = 256;
+constexpr int kStageBytes = kStageCols / 2;
+constexpr int kXPad = 64;  // bytes after a token's row: eight lanes' reads in 32 banks
+
 struct Head4Args {
   const void* x;
-  int64_t M, D, ldx;
+  int x_f32, M;          // tokens of this launch
+  int64_t D, ldx;
   const uint8_t* packed;
   int64_t ldp;
   const void* scales;
+  int s_f32;
   const uint8_t* zeros;
-  int group;
   int64_t V, G;
   const void* bias;
   void* y;
+  int y_f32;
   int64_t ldy;
+  int cols;              // token columns: M, or 3 M for fp32 tokens
+  int64_t chunk;         // columns of x in shared memory (a multiple of kStageCols)
+  int wk;                // warps that share a tile's columns
+  int64_t tiles;         // of 16 R rows
 };
 
-// Byte (from the row's start) and shift of column k in the packed layout.
-__device__ __forceinline__ int64_t packed_byte(int64_t k, int* shift) {
-  const int r = static_cast<int>(k & 127);
-  const int w = r >> 5, t = (r >> 3) & 3, j = r & 7;
-  const int p = (j >> 1) + 4 * (j & 1);
-  *shift = 4 * (p & 1);
-  return (k >> 7) * 64 + (4 * t + w) * 4 + (p >> 1);
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // the rest is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One warp per (token, vocabulary row).
-template <typename T, typename S, typename Y>
-__global__ void __launch_bounds__(256) head4_rows_kernel(Head4Args a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t n = a.M * a.V;
-  for (int64_t o = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); o < n;
-       o += static_cast<int64_t>(gridDim.x) * 8) {
-    const int64_t m = o / a.V, v = o % a.V;
-    const T* x = static_cast<const T*>(a.x) + m * a.ldx;
-    float sum = 0.0f;
-    for (int64_t k = lane; k < a.D; k += 32) {
-      int shift;
-      const int64_t at = packed_byte(k, &shift);
-      const int q = (a.packed[v * a.ldp + at] >> shift) & 15;
-      const int64_t gi = v * a.G + k / a.group;
-      const int z = a.zeros != nullptr ? a.zeros[gi] & 15 : 8;
-      sum += Elem<T>::load(x + k) * (static_cast<float>(q - z) *
-                                     Elem<S>::load(static_cast<const S*>(a.scales) + gi));
-    }
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) {
-      if (a.bias != nullptr) sum += Elem<T>::load(static_cast<const T*>(a.bias) + v);
-      Elem<Y>::store(static_cast<Y*>(a.y) + m * a.ldy + v, sum);
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+// c += a b for 16 rows x 16 columns by 16 x 8, bf16 with fp32 sums.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// (q - z) 2^-11 of nibbles P and P + 4 as a bf16 pair; minus_z = -(128 + z) 2^-11
+// in both halves.
+template <int P>
+__device__ __forceinline__ uint32_t unpack_pair(uint32_t word, uint32_t minus_z) {
+  const uint32_t v = ((word >> (4 * P)) & 0x000f000fu) | 0x43004300u;
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x3a003a00u), "r"(minus_z));
+  return r;
+}
+
+// Columns [k0, k0 + chunk) of the tokens to shared memory as bf16, zeros from D
+// on.  An fp32 value becomes three rows: its upper 16 bits, the upper 16 bits of
+// what is left, and the rest (each at most 8 significant bits: exact).
+__device__ void stage_tokens(const Head4Args& a, int64_t k0, char* xs, int64_t stride) {
+  const int per = static_cast<int>(a.chunk / 8);
+  const bool wide = !a.x_f32 && a.ldx % 8 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
+  for (int i = threadIdx.x; i < a.M * per; i += blockDim.x) {
+    const int m = i / per, j = i - m * per;
+    const int64_t k = k0 + 8 * j;
+    if (!a.x_f32) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.x) + m * a.ldx + k;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (wide && k + 8 <= a.D) {
+        v = *reinterpret_cast<const uint4*>(p);
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (k + e < a.D)
+            w[e / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[e])
+                        << (16 * (e & 1));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      *reinterpret_cast<uint4*>(xs + m * stride + 16 * j) = v;
+    } else {
+      const float* p = static_cast<const float*>(a.x) + m * a.ldx + k;
+      uint32_t w[3][4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float v = k + e < a.D ? p[e] : 0.0f;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const uint32_t top = (__float_as_uint(v) >> 16) | (v != v ? 0x40u : 0u);
+          w[part][e / 2] = (e & 1) ? w[part][e / 2] | (top << 16) : top;
+          const float head = __uint_as_float(top << 16);
+          // an infinity or NaN stands in the first part alone
+          v = fabsf(head) <= 3.4e38f ? v - head : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+        *reinterpret_cast<uint4*>(xs + (3 * m + part) * stride + 16 * j) =
+            make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
     }
   }
+}
+
+// G32: 32-column pieces per group; NT: instructions' widths of 8 token columns.
+template <int G32, int NT, int R, int W, int S>
+__global__ void __launch_bounds__(32 * W, 1) head4_kernel(const __grid_constant__ Head4Args a) {
+  extern __shared__ __align__(128) char smem[];
+  constexpr int kRows = 16 * R;
+  constexpr int kSlot = kRows * kStageBytes;
+  constexpr int GP = 8 / G32;        // groups of a row in a stage
+  constexpr int RR = kRows / 32;     // rows whose scales a lane fetches
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * (S * kSlot);
+  char* xs = smem + W * S * kSlot;
+  const uint32_t xs_a = smem_u32(xs);
+  const uint32_t xstride = static_cast<uint32_t>(a.chunk * 2 + kXPad);
+
+  const int wk = a.wk, wr = warp / wk, kw = warp - wr * wk;
+  const int per_round = W / wk;
+  const int64_t span = static_cast<int64_t>(per_round) * gridDim.x;
+  const int rounds = static_cast<int>((a.tiles + span - 1) / span);
+  const int stages = static_cast<int>((a.D + kStageCols - 1) / kStageCols);
+  const int chunk_stages = static_cast<int>(a.chunk / kStageCols);
+  const int chunks = (stages + chunk_stages - 1) / chunk_stages;
+  const int64_t row_bytes = (a.D + 127) / 128 * 64;
+
+  // the warp's stages in order: round by round, within each its columns
+  struct Place {
+    int round, stage;
+  };
+  auto first_row = [&](int round) {
+    return ((static_cast<int64_t>(round) * per_round + wr) * gridDim.x + blockIdx.x) * kRows;
+  };
+  auto advance = [&](Place& p) {
+    p.stage += wk;
+    if (p.stage >= stages) {
+      p.stage = kw;
+      ++p.round;
+    }
+  };
+  // stages of rows that do not exist are not fetched
+  auto fetch = [&](const Place& p, int slot) {
+    const int64_t row0 = first_row(p.round);
+    if (p.round < rounds && p.stage < stages && row0 < a.V) {
+      const int64_t at = static_cast<int64_t>(p.stage) * kStageBytes + (lane & 7) * 16;
+      const bool valid = at < row_bytes;
+#pragma unroll
+      for (int i = 0; i < kRows / 4; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        const uint8_t* src =
+            a.packed + min(row0 + r, a.V - 1) * a.ldp + (valid ? at : int64_t(0));
+        cp_async16(ring + slot * kSlot + r * kStageBytes + (((lane & 7) ^ ((r & 1) * 4)) * 16),
+                   src, valid);
+      }
+    }
+    cp_async_commit();
+  };
+  // scales (and zero points) of a stage: lane l fetches rows l, l + 32
+  auto fetch_scales = [&](const Place& p, float (&sc)[RR][GP], uint32_t (&zp)[RR][GP]) {
+    const int64_t row0 = first_row(p.round);
+    const bool in = p.round < rounds && p.stage < stages && row0 < a.V;
+#pragma unroll
+    for (int q = 0; q < RR; ++q) {
+      const int64_t base = min(row0 + lane + 32 * q, a.V - 1) * a.G;
+#pragma unroll
+      for (int k = 0; k < GP; ++k) {
+        const int64_t gi = static_cast<int64_t>(p.stage) * GP + k;
+        sc[q][k] = 0.0f;
+        zp[q][k] = 8u;
+        if (in && gi < a.G) {
+          sc[q][k] = a.s_f32 ? static_cast<const float*>(a.scales)[base + gi]
+                             : Elem<__nv_bfloat16>::load(
+                                   static_cast<const __nv_bfloat16*>(a.scales) + base + gi);
+          sc[q][k] *= 2048.0f;
+          if (a.zeros != nullptr) zp[q][k] = a.zeros[base + gi] & 15u;
+        }
+      }
+    }
+  };
+
+  Place ahead{0, kw}, here{0, kw};
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) {
+    fetch(ahead, s);
+    advance(ahead);
+  }
+  float sc[RR][GP];
+  uint32_t zp[RR][GP];
+  fetch_scales(here, sc, zp);
+  if (chunks == 1) {
+    stage_tokens(a, 0, xs, xstride);
+    __syncthreads();
+  }
+  int slot = 0;
+  float acc[R][NT][4];
+  for (int round = 0; round < rounds; ++round) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][n][e] = 0.0f;
+    const bool real = first_row(round) < a.V;
+    for (int c = 0; c < chunks; ++c) {
+      if (chunks > 1) {
+        __syncthreads();  // everyone is done with the last chunk
+        stage_tokens(a, c * a.chunk, xs, xstride);
+        __syncthreads();
+      }
+      const int end = min(stages, (c + 1) * chunk_stages);
+      while (here.round == round && here.stage < end) {
+        fetch(ahead, slot + S - 1 < S ? slot + S - 1 : slot - 1);
+        advance(ahead);
+        float next_sc[RR][GP];
+        uint32_t next_zp[RR][GP];
+        Place next = here;
+        advance(next);
+        fetch_scales(next, next_sc, next_zp);
+        cp_async_wait<S - 1>();
+        __syncwarp();
+        if (real) {
+          const uint32_t x0 =
+              xs_a + (here.stage - c * chunk_stages) * (kStageCols * 2) + g * xstride + t * 16;
+          const uint32_t w0 = ring + slot * kSlot + g * kStageBytes;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // blocks of 128 columns
+            uint4 lo[R], hi[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const uint32_t at = w0 + r * 16 * kStageBytes + (((h * 4 + t) ^ ((g & 1) * 4)) * 16);
+              lo[r] = lds128(at);
+              hi[r] = lds128(at + 8 * kStageBytes);
+            }
+            float part[R][NT][4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int gi = (h * 4 + w) / G32;
+              uint4 b[NT];
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                b[n] = n * 8 + g < a.cols ? lds128(x0 + n * 8 * xstride + (h * 4 + w) * 64)
+                                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                uint32_t zl = 0xbd88bd88u, zh = 0xbd88bd88u;
+                if (a.zeros != nullptr) {
+                  zl = __shfl_sync(0xffffffffu, zp[r / 2][gi], (r & 1) * 16 + g) * 0x10001u |
+                       0xbd80bd80u;
+                  zh = __shfl_sync(0xffffffffu, zp[r / 2][gi], (r & 1) * 16 + g + 8) * 0x10001u |
+                       0xbd80bd80u;
+                }
+                const uint32_t wl = w == 0 ? lo[r].x : w == 1 ? lo[r].y : w == 2 ? lo[r].z : lo[r].w;
+                const uint32_t wh = w == 0 ? hi[r].x : w == 1 ? hi[r].y : w == 2 ? hi[r].z : hi[r].w;
+                if (w % G32 == 0) {
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) part[r][n][e] = 0.0f;
+                }
+                {
+                  const uint32_t a0 = unpack_pair<0>(wl, zl), a1 = unpack_pair<0>(wh, zh);
+                  const uint32_t a2 = unpack_pair<1>(wl, zl), a3 = unpack_pair<1>(wh, zh);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) mma_bf16(part[r][n], a0, a1, a2, a3, b[n].x, b[n].y);
+                }
+                {
+                  const uint32_t a0 = unpack_pair<2>(wl, zl), a1 = unpack_pair<2>(wh, zh);
+                  const uint32_t a2 = unpack_pair<3>(wl, zl), a3 = unpack_pair<3>(wh, zh);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) mma_bf16(part[r][n], a0, a1, a2, a3, b[n].z, b[n].w);
+                }
+                if (w % G32 == G32 - 1) {
+                  const float sl = __shfl_sync(0xffffffffu, sc[r / 2][gi], (r & 1) * 16 + g);
+                  const float sh = __shfl_sync(0xffffffffu, sc[r / 2][gi], (r & 1) * 16 + g + 8);
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) {
+                    acc[r][n][0] += part[r][n][0] * sl;
+                    acc[r][n][1] += part[r][n][1] * sl;
+                    acc[r][n][2] += part[r][n][2] * sh;
+                    acc[r][n][3] += part[r][n][3] * sh;
+                  }
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();  // the slot may be filled again
+        slot = slot + 1 < S ? slot + 1 : 0;
+        here = next;
+#pragma unroll
+        for (int q = 0; q < RR; ++q)
+#pragma unroll
+          for (int k = 0; k < GP; ++k) {
+            sc[q][k] = next_sc[q][k];
+            zp[q][k] = next_zp[q][k];
+          }
+      }
+    }
+    if (wk > 1) {
+      // one round: the ring is no longer needed
+      cp_async_wait<0>();
+      __syncthreads();
+      float* red = reinterpret_cast<float*>(smem);
+      constexpr int kAcc = R * NT * 4;
+      const float* f = &acc[0][0][0];
+      if (kw > 0) {
+#pragma unroll
+        for (int e = 0; e < kAcc; ++e) red[(warp * kAcc + e) * 32 + lane] = f[e];
+      }
+      __syncthreads();
+      if (kw > 0) continue;
+      for (int k = 1; k < wk; ++k) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[r][n][e] += red[((warp + k) * kAcc + (r * NT + n) * 4 + e) * 32 + lane];
+      }
+    }
+    if (!real) continue;
+    auto put = [&](int64_t v, int m, float val) {
+      if (v >= a.V || m >= a.M) return;
+      if (a.bias != nullptr)
+        val += a.x_f32 ? static_cast<const float*>(a.bias)[v]
+                       : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.bias) + v);
+      const int64_t at = m * a.ldy + v;
+      if (a.y_f32)
+        static_cast<float*>(a.y)[at] = val;
+      else
+        Elem<__nv_bfloat16>::store(static_cast<__nv_bfloat16*>(a.y) + at, val);
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t v = first_row(round) + r * 16 + g;
+      if (!a.x_f32) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          put(v, n * 8 + 2 * t, acc[r][n][0]);
+          put(v, n * 8 + 2 * t + 1, acc[r][n][1]);
+          put(v + 8, n * 8 + 2 * t, acc[r][n][2]);
+          put(v + 8, n * 8 + 2 * t + 1, acc[r][n][3]);
+        }
+      } else {
+        // token m's three columns lie in the lanes and registers of their number
+#pragma unroll
+        for (int m = 0; m < (8 * NT) / 3; ++m) {
+          float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+          for (int part = 2; part >= 0; --part) {  // the smallest first
+            const int col = 3 * m + part;
+            const int src = (lane & 28) | ((col & 7) >> 1);
+            lo += __shfl_sync(0xffffffffu, acc[r][col / 8][col & 1], src);
+            hi += __shfl_sync(0xffffffffu, acc[r][col / 8][2 + (col & 1)], src);
+          }
+          if (t == (m & 3)) {
+            put(v, m, lo);
+            put(v + 8, m, hi);
+          }
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+}
+
+constexpr int kSmemMost = 227 * 1024;
+
+template <int G32, int NT, int R, int W, int S>
+static int launch_head4_k(Head4Args a, cudaStream_t s) {
+  constexpr int kRing = W * S * 16 * R * kStageBytes;
+  static std::atomic<uint64_t> raised{0};
+  int dev = 0;
+  int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc != FLCE_OK) return rc;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(raised.load() & bit)) {
+    rc = cuda_status(cudaFuncSetAttribute(head4_kernel<G32, NT, R, W, S>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost),
+                     "cudaFuncSetAttribute(head4_kernel)");
+    if (rc != FLCE_OK) return rc;
+    raised.fetch_or(bit);
+  }
+  const int64_t stages = (a.D + kStageCols - 1) / kStageCols;
+  const int64_t fit = ((kSmemMost - kRing) / a.cols - kXPad) / (2 * kStageCols);
+  a.chunk = std::min(stages, fit) * kStageCols;
+  a.tiles = (a.V + 16 * R - 1) / (16 * R);
+  const int sms = sm_count();
+  a.wk = 1;
+  while (a.wk < W && 2 * a.wk <= std::min(stages, fit) && a.tiles * 2 * a.wk <= int64_t(sms) * W)
+    a.wk *= 2;
+  const int64_t smem = kRing + a.cols * (a.chunk * 2 + kXPad);
+  const int grid = static_cast<int>(std::min<int64_t>(a.tiles, sms));
+  head4_kernel<G32, NT, R, W, S><<<grid, 32 * W, static_cast<size_t>(smem), s>>>(a);
+  return launch_status("head4_kernel launch");
+}
+
+// Two tiles to each of 16 warps; from 17 token columns on four to each of 8, so
+// that the tokens read from shared memory serve twice the weights.  A third
+// stage where the tokens leave room for it.
+template <int G32>
+static int launch_head4(const Head4Args& a, cudaStream_t s) {
+  if (a.cols > 16) return launch_head4_k<G32, 4, 4, 8, 2>(a, s);
+  if (a.cols > 8) return launch_head4_k<G32, 2, 2, 16, 2>(a, s);
+  const int64_t stages = (a.D + kStageCols - 1) / kStageCols;
+  const int64_t x = a.cols * (stages * kStageCols * 2 + kXPad);
+  if (x <= kSmemMost - 16 * 3 * 32 * kStageBytes) return launch_head4_k<G32, 1, 2, 16, 3>(a, s);
+  return launch_head4_k<G32, 1, 2, 16, 2>(a, s);
 }
 
 struct Quant4Args {
@@ -164,27 +557,31 @@ extern "C" int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return FLCE_EWORKSPACE;
   if (!aligned(ws, 16)) return FLCE_EALIGN;
   if (M == 0) return FLCE_OK;
-  const Head4Args a{x, M, D, ldx, packed, ldp, scales, zeros, group, V, (D + group - 1) / group,
-                    bias, y, ldy};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int grid = static_cast<int>(std::min<int64_t>((M * V + 7) / 8, sm_count() * 8));
-  using B = __nv_bfloat16;
-#define FLCE_H4(T, S, Y) head4_rows_kernel<T, S, Y><<<grid, 256, 0, s>>>(a)
-  if (dt == FLCE_BF16) {
-    if (dt_s == FLCE_BF16) {
-      if (dt_y == FLCE_BF16) FLCE_H4(B, B, B); else FLCE_H4(B, B, float);
-    } else {
-      if (dt_y == FLCE_BF16) FLCE_H4(B, float, B); else FLCE_H4(B, float, float);
-    }
-  } else {
-    if (dt_s == FLCE_BF16) {
-      if (dt_y == FLCE_BF16) FLCE_H4(float, B, B); else FLCE_H4(float, B, float);
-    } else {
-      if (dt_y == FLCE_BF16) FLCE_H4(float, float, B); else FLCE_H4(float, float, float);
-    }
+  Head4Args a{};
+  a.x_f32 = dt == FLCE_F32;
+  a.D = D;
+  a.ldx = ldx;
+  a.packed = packed;
+  a.ldp = ldp;
+  a.scales = scales;
+  a.s_f32 = dt_s == FLCE_F32;
+  a.zeros = zeros;
+  a.V = V;
+  a.G = (D + group - 1) / group;
+  a.bias = bias;
+  a.y_f32 = dt_y == FLCE_F32;
+  a.ldy = ldy;
+  const int64_t most = a.x_f32 ? 10 : 32;
+  for (int64_t m0 = 0; m0 < M && rc == FLCE_OK; m0 += most) {
+    a.M = static_cast<int>(std::min(most, M - m0));
+    a.cols = a.x_f32 ? 3 * a.M : a.M;
+    a.x = static_cast<const char*>(x) + m0 * ldx * static_cast<int64_t>(dtype_size(dt));
+    a.y = static_cast<char*>(y) + m0 * ldy * static_cast<int64_t>(dtype_size(dt_y));
+    rc = group == 32 ? launch_head4<1>(a, s)
+                     : group == 64 ? launch_head4<2>(a, s) : launch_head4<4>(a, s);
   }
-#undef FLCE_H4
-  return launch_status("head4_rows_kernel launch");
+  return rc;
 }
 
 extern "C" int head4_quantize(const void* W, int dt, int64_t V, int64_t D, int64_t ldw, int group,
