@@ -39,7 +39,6 @@ struct Head4Args {
   const uint8_t* packed;
   int64_t ldp;
   const void* scales;
-  int s_f32;
   const uint8_t* zeros;
   int64_t V, G;
   const void* bias;
@@ -65,30 +64,26 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-
-// c += a b for 16 rows x 16 columns by 16 x 8, bf16 with fp32 sums.
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// c (+)= a b for 16 rows x 16 columns by 16 x 8, bf16 with fp32 sums; `fresh`
+// starts from zero.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], bool fresh, uint32_t a0, uint32_t a1,
+                                         uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  const float z0 = fresh ? 0.0f : c[0], z1 = fresh ? 0.0f : c[1];
+  const float z2 = fresh ? 0.0f : c[2], z3 = fresh ? 0.0f : c[3];
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2), "f"(z3));
 }
 
 // (q - z) 2^-11 of nibbles P and P + 4 as a bf16 pair; minus_z = -(128 + z) 2^-11
 // in both halves.
 template <int P>
 __device__ __forceinline__ uint32_t unpack_pair(uint32_t word, uint32_t minus_z) {
-  const uint32_t v = ((word >> (4 * P)) & 0x000f000fu) | 0x43004300u;
-  uint32_t r;
+  uint32_t v, r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;"  // (a & b) | c
+      : "=r"(v)
+      : "r"(word >> (4 * P)), "r"(0x000f000fu), "r"(0x43004300u));
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x3a003a00u), "r"(minus_z));
   return r;
 }
@@ -140,19 +135,23 @@ __device__ void stage_tokens(const Head4Args& a, int64_t k0, char* xs, int64_t s
   }
 }
 
-// G32: 32-column pieces per group; NT: instructions' widths of 8 token columns.
-template <int G32, int NT, int R, int W, int S>
+// G32: 32-column pieces per group; ST: the scales' type; NT: instructions'
+// widths of 8 token columns.
+template <int G32, typename ST, int NT, int R, int W, int S>
 __global__ void __launch_bounds__(32 * W, 1) head4_kernel(const __grid_constant__ Head4Args a) {
   extern __shared__ __align__(128) char smem[];
   constexpr int kRows = 16 * R;
   constexpr int kSlot = kRows * kStageBytes;
   constexpr int GP = 8 / G32;        // groups of a row in a stage
   constexpr int RR = kRows / 32;     // rows whose scales a lane fetches
+  constexpr int SPW = 4 / sizeof(ST);  // scales per word
+  constexpr int SW = GP / SPW;         // words of a row's scales in a stage
+  constexpr int ZW = (GP + 3) / 4;     // words of its zero points
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(smem) + warp * (S * kSlot);
   char* xs = smem + W * S * kSlot;
-  const uint32_t xs_a = smem_u32(xs);
+  const char* ring_p = smem + warp * (S * kSlot);
   const uint32_t xstride = static_cast<uint32_t>(a.chunk * 2 + kXPad);
 
   const int wk = a.wk, wr = warp / wk, kw = warp - wr * wk;
@@ -165,72 +164,142 @@ __global__ void __launch_bounds__(32 * W, 1) head4_kernel(const __grid_constant_
   const int64_t row_bytes = (a.D + 127) / 128 * 64;
 
   // the warp's stages in order: round by round, within each its columns
-  struct Place {
-    int round, stage;
-  };
   auto first_row = [&](int round) {
     return ((static_cast<int64_t>(round) * per_round + wr) * gridDim.x + blockIdx.x) * kRows;
   };
-  auto advance = [&](Place& p) {
+  // One cursor for the weights, S - 1 stages ahead, and one for the scales, one
+  // stage ahead.  Rows past the last one read it again; a round without rows
+  // reads nothing.
+  struct Cursor {
+    int round, stage;
+    bool real;
+  };
+  const int sub = lane >> 3;                                    // row within four
+  const uint32_t dst0 = ring + sub * kStageBytes + (((lane & 7) ^ ((sub & 1) * 4)) * 16);
+  const int64_t step4 = 4 * a.ldp;
+  const uint8_t* wp = nullptr;  // this lane's 16 bytes of stage 0 in its first row
+  bool wp_last = false;         // the tile holds rows past the last
+  auto enter_weights = [&](Cursor& p) {
+    const int64_t row0 = first_row(p.round);
+    p.real = p.round < rounds && row0 < a.V;
+    wp_last = row0 + kRows > a.V;
+    wp = a.packed + min(row0 + sub, a.V - 1) * a.ldp + (lane & 7) * 16;
+  };
+  auto fetch = [&](Cursor& p, int slot) {
+    if (p.real) {
+      const int at = p.stage * kStageBytes;
+      const bool valid = at + (lane & 7) * 16 < row_bytes;
+      const uint8_t* src = valid ? wp + at : wp - (lane & 7) * 16;
+      const uint32_t dst = dst0 + slot * kSlot;
+      if (!wp_last) {
+#pragma unroll
+        for (int i = 0; i < kRows / 4; ++i) {
+          cp_async16(dst + i * 4 * kStageBytes, src, valid);
+          src += step4;
+        }
+      } else {
+        const int64_t row0 = first_row(p.round);
+#pragma unroll
+        for (int i = 0; i < kRows / 4; ++i) {
+          const int64_t row = min(row0 + sub + 4 * i, a.V - 1);
+          cp_async16(dst + i * 4 * kStageBytes,
+                     a.packed + row * a.ldp + (valid ? at + (lane & 7) * 16 : 0), valid);
+        }
+      }
+    }
+    cp_async_commit();
     p.stage += wk;
     if (p.stage >= stages) {
       p.stage = kw;
       ++p.round;
+      enter_weights(p);
     }
-  };
-  // stages of rows that do not exist are not fetched
-  auto fetch = [&](const Place& p, int slot) {
-    const int64_t row0 = first_row(p.round);
-    if (p.round < rounds && p.stage < stages && row0 < a.V) {
-      const int64_t at = static_cast<int64_t>(p.stage) * kStageBytes + (lane & 7) * 16;
-      const bool valid = at < row_bytes;
-#pragma unroll
-      for (int i = 0; i < kRows / 4; ++i) {
-        const int r = i * 4 + (lane >> 3);
-        const uint8_t* src =
-            a.packed + min(row0 + r, a.V - 1) * a.ldp + (valid ? at : int64_t(0));
-        cp_async16(ring + slot * kSlot + r * kStageBytes + (((lane & 7) ^ ((r & 1) * 4)) * 16),
-                   src, valid);
-      }
-    }
-    cp_async_commit();
   };
   // scales (and zero points) of a stage: lane l fetches rows l, l + 32
-  auto fetch_scales = [&](const Place& p, float (&sc)[RR][GP], uint32_t (&zp)[RR][GP]) {
+  int64_t sp[RR];  // index of the row's first group
+  auto enter_scales = [&](Cursor& p) {
     const int64_t row0 = first_row(p.round);
-    const bool in = p.round < rounds && p.stage < stages && row0 < a.V;
+    p.real = p.round < rounds && row0 < a.V;
+#pragma unroll
+    for (int q = 0; q < RR; ++q) sp[q] = min(row0 + lane + 32 * q, a.V - 1) * a.G;
+  };
+  // Words as loaded (a conversion here would wait for the load), in one access
+  // where rows of groups are aligned to it.
+  const ST* scales = static_cast<const ST*>(a.scales);
+  const bool wide_s = a.G % GP == 0 && reinterpret_cast<uintptr_t>(scales) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0;
+  auto fetch_scales = [&](Cursor& p, uint32_t (&sc)[RR][SW], uint32_t (&zp)[RR][ZW]) {
+    const int g0 = p.stage * GP;
 #pragma unroll
     for (int q = 0; q < RR; ++q) {
-      const int64_t base = min(row0 + lane + 32 * q, a.V - 1) * a.G;
 #pragma unroll
-      for (int k = 0; k < GP; ++k) {
-        const int64_t gi = static_cast<int64_t>(p.stage) * GP + k;
-        sc[q][k] = 0.0f;
-        zp[q][k] = 8u;
-        if (in && gi < a.G) {
-          sc[q][k] = a.s_f32 ? static_cast<const float*>(a.scales)[base + gi]
-                             : Elem<__nv_bfloat16>::load(
-                                   static_cast<const __nv_bfloat16*>(a.scales) + base + gi);
-          sc[q][k] *= 2048.0f;
-          if (a.zeros != nullptr) zp[q][k] = a.zeros[base + gi] & 15u;
+      for (int k = 0; k < SW; ++k) sc[q][k] = 0u;
+#pragma unroll
+      for (int k = 0; k < ZW; ++k) zp[q][k] = 0u;
+      if (!p.real) continue;
+      const ST* from = scales + sp[q] + g0;
+      const uint8_t* zfrom = a.zeros + sp[q] + g0;
+      if (wide_s) {
+        if (g0 < a.G) {
+#pragma unroll
+          for (int k = 0; k < SW; k += 4) {
+            const uint32_t* f = reinterpret_cast<const uint32_t*>(from) + k;
+            if constexpr (SW == 1) {
+              sc[q][0] = f[0];
+            } else if constexpr (SW == 2) {
+              const uint2 v = *reinterpret_cast<const uint2*>(f);
+              sc[q][0] = v.x, sc[q][1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4*>(f);
+              sc[q][k] = v.x, sc[q][k + 1] = v.y, sc[q][k + 2] = v.z, sc[q][k + 3] = v.w;
+            }
+          }
+          if (a.zeros != nullptr) {
+            if constexpr (GP == 2) {
+              zp[q][0] = *reinterpret_cast<const uint16_t*>(zfrom);
+            } else if constexpr (GP == 4) {
+              zp[q][0] = *reinterpret_cast<const uint32_t*>(zfrom);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(zfrom);
+              zp[q][0] = v.x, zp[q][ZW - 1] = v.y;
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < GP; ++k) {
+          if (g0 + k >= a.G) continue;
+          if constexpr (SPW == 1)
+            sc[q][k] = reinterpret_cast<const uint32_t*>(from)[k];
+          else
+            sc[q][k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(from)[k])
+                            << (16 * (k & 1));
+          if (a.zeros != nullptr) zp[q][k / 4] |= static_cast<uint32_t>(zfrom[k]) << (8 * (k & 3));
         }
       }
     }
+    p.stage += wk;
+    if (p.stage >= stages) {
+      p.stage = kw;
+      ++p.round;
+      enter_scales(p);
+    }
   };
 
-  Place ahead{0, kw}, here{0, kw};
+  Cursor weights{0, kw, false}, scale{0, kw, false};
+  enter_weights(weights);
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s) {
-    fetch(ahead, s);
-    advance(ahead);
-  }
-  float sc[RR][GP];
-  uint32_t zp[RR][GP];
-  fetch_scales(here, sc, zp);
+  for (int s = 0; s < S - 1; ++s) fetch(weights, s);
+  uint32_t sc[RR][SW], zp[RR][ZW];
+  enter_scales(scale);
+  fetch_scales(scale, sc, zp);
   if (chunks == 1) {
     stage_tokens(a, 0, xs, xstride);
     __syncthreads();
   }
+  uint32_t xrow[NT];  // this lane's token column (beyond the last: its result is not used)
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xrow[n] = min(n * 8 + g, a.cols - 1) * xstride + t * 16;
   int slot = 0;
   float acc[R][NT][4];
   for (int round = 0; round < rounds; ++round) {
@@ -241,6 +310,7 @@ __global__ void __launch_bounds__(32 * W, 1) head4_kernel(const __grid_constant_
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[r][n][e] = 0.0f;
     const bool real = first_row(round) < a.V;
+    int stage = kw;
     for (int c = 0; c < chunks; ++c) {
       if (chunks > 1) {
         __syncthreads();  // everyone is done with the last chunk
@@ -248,28 +318,24 @@ __global__ void __launch_bounds__(32 * W, 1) head4_kernel(const __grid_constant_
         __syncthreads();
       }
       const int end = min(stages, (c + 1) * chunk_stages);
-      while (here.round == round && here.stage < end) {
-        fetch(ahead, slot + S - 1 < S ? slot + S - 1 : slot - 1);
-        advance(ahead);
-        float next_sc[RR][GP];
-        uint32_t next_zp[RR][GP];
-        Place next = here;
-        advance(next);
-        fetch_scales(next, next_sc, next_zp);
+      for (; stage < end; stage += wk) {
+        fetch(weights, slot + S - 1 < S ? slot + S - 1 : slot - 1);
+        uint32_t next_sc[RR][SW], next_zp[RR][ZW];
+        fetch_scales(scale, next_sc, next_zp);
         cp_async_wait<S - 1>();
         __syncwarp();
         if (real) {
-          const uint32_t x0 =
-              xs_a + (here.stage - c * chunk_stages) * (kStageCols * 2) + g * xstride + t * 16;
-          const uint32_t w0 = ring + slot * kSlot + g * kStageBytes;
+          const uint32_t x0 = (stage - c * chunk_stages) * (kStageCols * 2);
+          const char* w0 = ring_p + slot * kSlot + g * kStageBytes;
+          uint32_t s_lo[R], s_hi[R], z_lo[R], z_hi[R];  // rows g and g + 8 of each tile
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // blocks of 128 columns
             uint4 lo[R], hi[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-              const uint32_t at = w0 + r * 16 * kStageBytes + (((h * 4 + t) ^ ((g & 1) * 4)) * 16);
-              lo[r] = lds128(at);
-              hi[r] = lds128(at + 8 * kStageBytes);
+              const char* at = w0 + r * 16 * kStageBytes + (((h * 4 + t) ^ ((g & 1) * 4)) * 16);
+              lo[r] = *reinterpret_cast<const uint4*>(at);
+              hi[r] = *reinterpret_cast<const uint4*>(at + 8 * kStageBytes);
             }
             float part[R][NT][4];
 #pragma unroll
@@ -278,40 +344,50 @@ __global__ void __launch_bounds__(32 * W, 1) head4_kernel(const __grid_constant_
               uint4 b[NT];
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                b[n] = n * 8 + g < a.cols ? lds128(x0 + n * 8 * xstride + (h * 4 + w) * 64)
-                                          : make_uint4(0, 0, 0, 0);
+                b[n] = *reinterpret_cast<const uint4*>(xs + xrow[n] + x0 + (h * 4 + w) * 64);
 #pragma unroll
               for (int r = 0; r < R; ++r) {
+                const int src = (r & 1) * 16 + g;
                 uint32_t zl = 0xbd88bd88u, zh = 0xbd88bd88u;
                 if (a.zeros != nullptr) {
-                  zl = __shfl_sync(0xffffffffu, zp[r / 2][gi], (r & 1) * 16 + g) * 0x10001u |
-                       0xbd80bd80u;
-                  zh = __shfl_sync(0xffffffffu, zp[r / 2][gi], (r & 1) * 16 + g + 8) * 0x10001u |
-                       0xbd80bd80u;
+                  if (w % G32 == 0 && gi % 4 == 0) {
+                    z_lo[r] = __shfl_sync(0xffffffffu, zp[r / 2][gi / 4], src);
+                    z_hi[r] = __shfl_sync(0xffffffffu, zp[r / 2][gi / 4], src + 8);
+                  }
+                  zl = ((z_lo[r] >> (8 * (gi % 4))) & 15u) * 0x10001u | 0xbd80bd80u;
+                  zh = ((z_hi[r] >> (8 * (gi % 4))) & 15u) * 0x10001u | 0xbd80bd80u;
                 }
                 const uint32_t wl = w == 0 ? lo[r].x : w == 1 ? lo[r].y : w == 2 ? lo[r].z : lo[r].w;
                 const uint32_t wh = w == 0 ? hi[r].x : w == 1 ? hi[r].y : w == 2 ? hi[r].z : hi[r].w;
-                if (w % G32 == 0) {
-#pragma unroll
-                  for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) part[r][n][e] = 0.0f;
-                }
                 {
                   const uint32_t a0 = unpack_pair<0>(wl, zl), a1 = unpack_pair<0>(wh, zh);
                   const uint32_t a2 = unpack_pair<1>(wl, zl), a3 = unpack_pair<1>(wh, zh);
 #pragma unroll
-                  for (int n = 0; n < NT; ++n) mma_bf16(part[r][n], a0, a1, a2, a3, b[n].x, b[n].y);
+                  for (int n = 0; n < NT; ++n)
+                    mma_bf16(part[r][n], w % G32 == 0, a0, a1, a2, a3, b[n].x, b[n].y);
                 }
                 {
                   const uint32_t a0 = unpack_pair<2>(wl, zl), a1 = unpack_pair<2>(wh, zh);
                   const uint32_t a2 = unpack_pair<3>(wl, zl), a3 = unpack_pair<3>(wh, zh);
 #pragma unroll
-                  for (int n = 0; n < NT; ++n) mma_bf16(part[r][n], a0, a1, a2, a3, b[n].z, b[n].w);
+                  for (int n = 0; n < NT; ++n)
+                    mma_bf16(part[r][n], false, a0, a1, a2, a3, b[n].z, b[n].w);
                 }
                 if (w % G32 == G32 - 1) {
-                  const float sl = __shfl_sync(0xffffffffu, sc[r / 2][gi], (r & 1) * 16 + g);
-                  const float sh = __shfl_sync(0xffffffffu, sc[r / 2][gi], (r & 1) * 16 + g + 8);
+                  if (gi % SPW == 0) {
+                    s_lo[r] = __shfl_sync(0xffffffffu, sc[r / 2][gi / SPW], src);
+                    s_hi[r] = __shfl_sync(0xffffffffu, sc[r / 2][gi / SPW], src + 8);
+                  }
+                  float sl, sh;
+                  if constexpr (SPW == 1) {
+                    sl = __uint_as_float(s_lo[r]), sh = __uint_as_float(s_hi[r]);
+                  } else if (gi & 1) {
+                    sl = bf16_hi(s_lo[r]), sh = bf16_hi(s_hi[r]);
+                  } else {
+                    sl = bf16_lo(s_lo[r]), sh = bf16_lo(s_hi[r]);
+                  }
+                  sl *= 2048.0f;
+                  sh *= 2048.0f;
 #pragma unroll
                   for (int n = 0; n < NT; ++n) {
                     acc[r][n][0] += part[r][n][0] * sl;
@@ -326,14 +402,13 @@ __global__ void __launch_bounds__(32 * W, 1) head4_kernel(const __grid_constant_
         }
         __syncwarp();  // the slot may be filled again
         slot = slot + 1 < S ? slot + 1 : 0;
-        here = next;
 #pragma unroll
-        for (int q = 0; q < RR; ++q)
+        for (int q = 0; q < RR; ++q) {
 #pragma unroll
-          for (int k = 0; k < GP; ++k) {
-            sc[q][k] = next_sc[q][k];
-            zp[q][k] = next_zp[q][k];
-          }
+          for (int k = 0; k < SW; ++k) sc[q][k] = next_sc[q][k];
+#pragma unroll
+          for (int k = 0; k < ZW; ++k) zp[q][k] = next_zp[q][k];
+        }
       }
     }
     if (wk > 1) {
@@ -407,7 +482,7 @@ __global__ void __launch_bounds__(32 * W, 1) head4_kernel(const __grid_constant_
 
 constexpr int kSmemMost = 227 * 1024;
 
-template <int G32, int NT, int R, int W, int S>
+template <int G32, typename ST, int NT, int R, int W, int S>
 static int launch_head4_k(Head4Args a, cudaStream_t s) {
   constexpr int kRing = W * S * 16 * R * kStageBytes;
   static std::atomic<uint64_t> raised{0};
@@ -416,7 +491,7 @@ static int launch_head4_k(Head4Args a, cudaStream_t s) {
   if (rc != FLCE_OK) return rc;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(raised.load() & bit)) {
-    rc = cuda_status(cudaFuncSetAttribute(head4_kernel<G32, NT, R, W, S>,
+    rc = cuda_status(cudaFuncSetAttribute(head4_kernel<G32, ST, NT, R, W, S>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost),
                      "cudaFuncSetAttribute(head4_kernel)");
     if (rc != FLCE_OK) return rc;
@@ -432,21 +507,28 @@ static int launch_head4_k(Head4Args a, cudaStream_t s) {
     a.wk *= 2;
   const int64_t smem = kRing + a.cols * (a.chunk * 2 + kXPad);
   const int grid = static_cast<int>(std::min<int64_t>(a.tiles, sms));
-  head4_kernel<G32, NT, R, W, S><<<grid, 32 * W, static_cast<size_t>(smem), s>>>(a);
+  head4_kernel<G32, ST, NT, R, W, S><<<grid, 32 * W, static_cast<size_t>(smem), s>>>(a);
   return launch_status("head4_kernel launch");
 }
 
 // Two tiles to each of 16 warps; from 17 token columns on four to each of 8, so
 // that the tokens read from shared memory serve twice the weights.  A third
 // stage where the tokens leave room for it.
-template <int G32>
+template <int G32, typename ST>
 static int launch_head4(const Head4Args& a, cudaStream_t s) {
-  if (a.cols > 16) return launch_head4_k<G32, 4, 4, 8, 2>(a, s);
-  if (a.cols > 8) return launch_head4_k<G32, 2, 2, 16, 2>(a, s);
+  if (a.cols > 16) return launch_head4_k<G32, ST, 4, 4, 8, 2>(a, s);
+  if (a.cols > 8) return launch_head4_k<G32, ST, 2, 2, 16, 2>(a, s);
   const int64_t stages = (a.D + kStageCols - 1) / kStageCols;
   const int64_t x = a.cols * (stages * kStageCols * 2 + kXPad);
-  if (x <= kSmemMost - 16 * 3 * 32 * kStageBytes) return launch_head4_k<G32, 1, 2, 16, 3>(a, s);
-  return launch_head4_k<G32, 1, 2, 16, 2>(a, s);
+  if (x <= kSmemMost - 16 * 3 * 32 * kStageBytes) return launch_head4_k<G32, ST, 1, 2, 16, 3>(a, s);
+  return launch_head4_k<G32, ST, 1, 2, 16, 2>(a, s);
+}
+
+template <typename ST>
+static int launch_group(int group, const Head4Args& a, cudaStream_t s) {
+  return group == 32   ? launch_head4<1, ST>(a, s)
+         : group == 64 ? launch_head4<2, ST>(a, s)
+                       : launch_head4<4, ST>(a, s);
 }
 
 struct Quant4Args {
@@ -565,7 +647,6 @@ extern "C" int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t
   a.packed = packed;
   a.ldp = ldp;
   a.scales = scales;
-  a.s_f32 = dt_s == FLCE_F32;
   a.zeros = zeros;
   a.V = V;
   a.G = (D + group - 1) / group;
@@ -578,8 +659,10 @@ extern "C" int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t
     a.cols = a.x_f32 ? 3 * a.M : a.M;
     a.x = static_cast<const char*>(x) + m0 * ldx * static_cast<int64_t>(dtype_size(dt));
     a.y = static_cast<char*>(y) + m0 * ldy * static_cast<int64_t>(dtype_size(dt_y));
-    rc = group == 32 ? launch_head4<1>(a, s)
-                     : group == 64 ? launch_head4<2>(a, s) : launch_head4<4>(a, s);
+    if (dt_s == FLCE_BF16)
+      rc = launch_group<__nv_bfloat16>(group, a, s);
+    else
+      rc = launch_group<float>(group, a, s);
   }
   return rc;
 }
