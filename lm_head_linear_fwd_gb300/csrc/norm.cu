@@ -1,22 +1,233 @@
 // Layer norm and RMS norm, forward and backward.
+//
+// Both are bound by the bytes of their rows, so a row is read once and stays in
+// registers: a team of threads holds it, kLane elements to a thread, loads the
+// next row before it works on this one, and sums by shuffles and one shared
+// word per warp.  The square sum is taken around the mean from the registers.
+// The threads' columns are the same for every row: the backward pass adds up its
+// columns of grad_weight and grad_bias in registers (in shared memory for the widest rows) over all rows of a block;
+// one partial sum per block, which norm_bwd_finish_kernel adds in block order.
+//
+// Thread l holds the 16-byte vectors l, l + team, ... of the row, wherever the row
+// lies, and the roundings are written out, so the results do not depend on
+// strides and alignment.  Rows that start
+// inside 16-byte blocks (kWhole = false) are read by whole blocks all the same: a
+// vector is shifted together from two blocks, the second of which a neighbour
+// has brought into the L1 cache, and written the other way round with the
+// neighbour's words.  Bytes of a block outside the row are neither used nor
+// written; a block with one byte of the row lies within mapped memory as a whole.
 #include <algorithm>
+#include <atomic>
 
 #include "rows.cuh"
 
 namespace flce {
 
-constexpr int kNormThreads = 256;
+constexpr int kLane = 16;             // elements of a row per thread
+constexpr int kFwdThreads = 1024;     // most threads of a block
+constexpr int kBwdThreads = 512;      // with the column sums in registers
+constexpr int kBwdThreadsWide = 1024; // with the column sums in shared memory
 
-// Sum over the block; every thread returns the same value.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// How a row is spread: `team` threads to a row (a power of two up to a warp,
+// then whole warps), `teams` rows at a time in a block.
+struct NormPlan {
+  int team, teams;
+  int64_t blocks;
+};
+
+static NormPlan norm_plan(int64_t N, int64_t D, int blocks_of_256) {
+  NormPlan p;
+  const int64_t need = (D + kLane - 1) / kLane;
+  if (need <= 32) {
+    p.team = 4;
+    while (p.team < need) p.team *= 2;
+  } else {
+    p.team = static_cast<int>((need + 31) / 32 * 32);
+  }
+  const int sms = sm_count();
+  // blocks of about 256 threads, smaller ones while there are SMs without a row
+  p.teams = std::max(1, 256 / p.team);
+  while (p.teams > 1 && p.teams * p.team > 32 && (N + p.teams - 1) / p.teams < sms) p.teams /= 2;
+  const int threads = std::max(256, p.team * p.teams);
+  const int64_t most = static_cast<int64_t>(sms) * std::max(1, 256 * blocks_of_256 / threads);
+  p.blocks = std::max<int64_t>(1, std::min((N + p.teams - 1) / p.teams, most));
+  return p;
+}
+
+// Sums of a (and, where asked for, b) over the team; every thread returns the
+// same values.  `red`: one float2 per warp of the team, free again after the
+// next call with another.
+template <bool kTwo>
+__device__ __forceinline__ void team_sum(float& a, float& b, int team, int id, float2* red) {
+  const int width = team < 32 ? team : 32;
+  for (int o = width / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (kTwo) b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if (team <= 32) return;
+  const int lane = threadIdx.x & 31;
+  const int warps = team >> 5, warp = (threadIdx.x - id * team) >> 5;
+  if (lane == 0) red[warp] = make_float2(a, kTwo ? b : 0.0f);
+  named_barrier(1 + id, team);
+  const float2 v = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
+  a = v.x;
+  if (kTwo) b = v.y;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < kNormThreads / 32; ++w) s += red[w];
-  __syncthreads();
-  return s;
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (kTwo) b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+}
+
+// The 16-byte block with byte 16 i of a row that starts `off` bytes into a block.
+__device__ __forceinline__ uint4 row_block(const void* base, int i) {
+  return *(reinterpret_cast<const uint4*>(base) + i);
+}
+
+// kLane elements of a row.
+template <typename T, bool kWhole>
+struct RowRegs {
+  static constexpr int VEC = 16 / sizeof(T), NV = kLane / VEC;
+  uint4 v[NV];       // loaded blocks; after finish(): the row's vectors
+  // starts the loads of a row (none for D = 0)
+  __device__ __forceinline__ void load(const T* p, int D, int team, int l) {
+    const char* base = reinterpret_cast<const char*>(p);
+    if (!kWhole) base -= reinterpret_cast<uintptr_t>(p) & 15;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = k * team + l;
+      v[k] = i * VEC < D ? row_block(base, i) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  // the vectors themselves, zeros past the row's end
+  __device__ __forceinline__ void finish(const T* p, int D, int team, int l) {
+    if (kWhole) return;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    const char* base = reinterpret_cast<const char*>(p) - off;
+    const int end = off + D * static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = k * team + l;
+      uint4 hi = make_uint4(0, 0, 0, 0);
+      if (off != 0 && i * VEC < D && (i + 1) * 16 < end) hi = row_block(base, i + 1);
+      uint32_t w[8] = {v[k].x, v[k].y, v[k].z, v[k].w, hi.x, hi.y, hi.z, hi.w};
+      if (off & 8) {
+#pragma unroll
+        for (int q = 0; q < 6; ++q) w[q] = w[q + 2];
+      }
+      if (off & 4) {
+#pragma unroll
+        for (int q = 0; q < 5; ++q) w[q] = w[q + 1];
+      }
+      if (sizeof(T) == 2 && (off & 2)) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = __funnelshift_r(w[q], w[q + 1], 16);
+      }
+      const int left = D - i * VEC;
+      if (left < VEC) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (sizeof(T) == 4) {
+            if (q >= left) w[q] = 0u;
+          } else {
+            if (2 * q >= left) w[q] = 0u;
+            if (2 * q + 1 >= left) w[q] &= 0xffffu;
+          }
+        }
+      }
+      v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void unpack(int k, float (&x)[VEC]) const {
+    Elem<T>::unpack(v[k], x);
+  }
+};
+
+// Writes the vector at columns j.. of a row (one per lane, all lanes of the warp
+// take part).  A row inside a block: each lane writes the block that begins with
+// its left neighbour's last elements, where it has such a neighbour and the block
+// is full; what no such block covers goes element by element.
+template <typename T, bool kWhole>
+__device__ __forceinline__ void store_vector(T* row, int j, int D, int team, int l,
+                                             const float (&x)[16 / sizeof(T)]) {
+  constexpr int VEC = 16 / sizeof(T);
+  const uint4 own = Elem<T>::pack(x);
+  if (kWhole) {
+    if (j < D) *reinterpret_cast<uint4*>(row + j) = own;
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+  const int o = off / static_cast<int>(sizeof(T));
+  const int left = D - j;  // this lane's elements (VEC or fewer, none when <= 0)
+  uint32_t w[8];
+  w[0] = __shfl_up_sync(0xffffffffu, own.x, 1);
+  w[1] = __shfl_up_sync(0xffffffffu, own.y, 1);
+  w[2] = __shfl_up_sync(0xffffffffu, own.z, 1);
+  w[3] = __shfl_up_sync(0xffffffffu, own.w, 1);
+  w[4] = own.x, w[5] = own.y, w[6] = own.z, w[7] = own.w;
+  const bool full = (o == 0 || (lane > 0 && l > 0)) && left >= VEC - o;
+  const bool next_full = __shfl_down_sync(0xffffffffu, full, 1) && lane < 31 && l < team - 1;
+  if (left <= 0) return;
+  if (full) {
+    // the last off bytes of the neighbour's vector, then the first of this one
+    uint32_t b[5];  // words 4 - ceil(off / 4) .. of w
+    const int from = 16 - off;  // byte of w where the block begins
+    uint32_t t[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t[q] = w[q];
+    if (from & 16) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) t[q] = t[q + 4];
+    }
+    if (from & 8) {
+#pragma unroll
+      for (int q = 0; q < 6; ++q) t[q] = t[q + 2];
+    }
+    if (from & 4) {
+#pragma unroll
+      for (int q = 0; q < 7; ++q) t[q] = t[q + 1];
+    }
+#pragma unroll
+    for (int q = 0; q < 5; ++q) b[q] = t[q];
+    if (sizeof(T) == 2 && (from & 2)) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) b[q] = __funnelshift_r(b[q], b[q + 1], 16);
+    }
+    *reinterpret_cast<uint4*>(reinterpret_cast<char*>(row + j) - off) =
+        make_uint4(b[0], b[1], b[2], b[3]);
+  }
+  if (!full || !next_full) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const bool covered = e < VEC - o ? full : next_full;
+      if (!covered && e < left) Elem<T>::store(row + j + e, x[e]);
+    }
+  }
+}
+
+// VEC elements of a weight vector from column j on (read again for every row: they
+// stay in the L1 cache, and registers are what bounds the rows in flight).
+template <int VEC, bool kWhole>
+__device__ __forceinline__ void weight_vec(const void* p, int f32, int j, int D, float other,
+                                           float (&x)[VEC]) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = other;
+  } else if (kWhole || (j + VEC <= D && (reinterpret_cast<uintptr_t>(p) & 15) == 0)) {
+    if (f32)
+      load_as<float, VEC>(static_cast<const float*>(p) + j, x);
+    else
+      load_as<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(p) + j, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      x[e] = other;
+      if (j + e < D)
+        x[e] = f32 ? static_cast<const float*>(p)[j + e]
+                   : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(p) + j + e);
+    }
+  }
 }
 
 struct NormArgs {
@@ -24,43 +235,87 @@ struct NormArgs {
   int64_t N, D, ldx;
   const void* weight;
   const void* bias;
+  int w_f32;
   float eps;
   void* y;
   int64_t ldy;
   float* mean;
   float* rstd;
+  int team, teams;
 };
 
-template <typename T, typename U, bool kCenter>
-__global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormArgs a) {
-  __shared__ float red[kNormThreads / 32];
-  const U* w = static_cast<const U*>(a.weight);
-  const U* b = static_cast<const U*>(a.bias);
-  for (int64_t i = blockIdx.x; i < a.N; i += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + i * a.ldx;
-    T* y = static_cast<T*>(a.y) + i * a.ldy;
-    float mean = 0.0f;
+template <typename T, bool kWhole, bool kCenter>
+__global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(NormArgs a) {
+  __shared__ float2 red_all[2][kFwdThreads / 32];
+  using Row = RowRegs<T, kWhole>;
+  constexpr int VEC = Row::VEC, NV = Row::NV;
+  const int team = a.team, id = threadIdx.x / team, l = threadIdx.x - id * team;
+  float2* red0 = red_all[0] + (team > 32 ? id * (team >> 5) : 0);
+  float2* red1 = red_all[1] + (team > 32 ? id * (team >> 5) : 0);
+  // teams of one warp go on together
+  const int lead = team < 32 ? (threadIdx.x & ~31) / team : id;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * a.teams;
+  int64_t first = static_cast<int64_t>(blockIdx.x) * a.teams + lead;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + id;
+  const int D = static_cast<int>(a.D);
+  const T* x = static_cast<const T*>(a.x);
+  Row next;
+  next.load(x + (row < a.N ? row : 0) * a.ldx, row < a.N ? D : 0, team, l);
+  const float n = static_cast<float>(D);
+  for (; first < a.N; first += step, row += step) {
+    Row cur = next;
+    const bool in_row = row < a.N;
+    cur.finish(x + (in_row ? row : 0) * a.ldx, in_row ? D : 0, team, l);
+    const int64_t ahead = row + step;
+    next.load(x + (ahead < a.N ? ahead : 0) * a.ldx, ahead < a.N ? D : 0, team, l);
+    float mean = 0.0f, none = 0.0f;
     if (kCenter) {
-      float s = 0.0f;
-      for (int64_t j = threadIdx.x; j < a.D; j += kNormThreads) s += Elem<T>::load(x + j);
-      mean = block_sum(s, red) / static_cast<float>(a.D);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float f[VEC];
+        cur.unpack(k, f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) mean += f[e];
+      }
+      team_sum<false>(mean, none, team, id, red0);
+      mean /= n;
     }
     float q = 0.0f;
-    for (int64_t j = threadIdx.x; j < a.D; j += kNormThreads) {
-      const float d = Elem<T>::load(x + j) - mean;
-      q += d * d;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float f[VEC];
+      cur.unpack(k, f);
+      const int j = (k * team + l) * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float d = f[e] - mean;
+        if ((kWhole ? j : j + e) < D) q = __fmaf_rn(d, d, q);
+      }
     }
-    const float rstd = 1.0f / sqrtf(block_sum(q, red) / static_cast<float>(a.D) + a.eps);
-    for (int64_t j = threadIdx.x; j < a.D; j += kNormThreads) {
-      float v = (Elem<T>::load(x + j) - mean) * rstd;
-      if (w != nullptr) v *= Elem<U>::load(w + j);
-      if (b != nullptr) v += Elem<U>::load(b + j);
-      Elem<T>::store(y + j, v);
+    team_sum<false>(q, none, team, id, red1);
+    const float rstd = 1.0f / sqrtf(q / n + a.eps);
+    T* yr = static_cast<T*>(a.y) + (in_row ? row : 0) * a.ldy;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int j = (k * team + l) * VEC;
+      float f[VEC], w[VEC], b[VEC];
+      if (j < D) {
+        weight_vec<VEC, kWhole>(a.weight, a.w_f32, j, D, 1.0f, w);
+        if (kCenter) weight_vec<VEC, kWhole>(a.bias, a.w_f32, j, D, 0.0f, b);
+        cur.unpack(k, f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float h = __fmul_rn(f[e] - mean, rstd);
+          f[e] = kCenter ? __fmaf_rn(h, w[e], b[e]) : __fmul_rn(h, w[e]);
+        }
+      }
+      store_vector<T, kWhole>(yr, j, in_row ? D : 0, team, l, f);
     }
-    if (threadIdx.x == 0) {
-      if (kCenter && a.mean != nullptr) a.mean[i] = mean;
-      if (a.rstd != nullptr) a.rstd[i] = rstd;
+    if (l == 0 && in_row) {
+      if (kCenter && a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
+    if (!kCenter && team > 32) named_barrier(1 + id, team);  // red1 is free again
   }
 }
 
@@ -70,6 +325,7 @@ struct NormBwdArgs {
   const void* dy;
   int64_t lddy;
   const void* weight;
+  int w_f32;
   const float* mean;
   const float* rstd;
   void* dx;
@@ -77,42 +333,218 @@ struct NormBwdArgs {
   float* dw;
   float* db;
   int accumulate;
-  float* part;
-  int slices;
+  float* part;  // [slices][2][D]: the blocks' column sums
+  int64_t slices;
+  int team, teams;
 };
 
-template <typename T, typename U, bool kCenter>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_rows_kernel(NormBwdArgs a) {
-  __shared__ float red[kNormThreads / 32];
-  const U* w = static_cast<const U*>(a.weight);
+// kWide: the column sums in shared memory, one row at a time in a block.
+template <typename T, bool kWhole, bool kCenter, bool kWide>
+__global__ void __launch_bounds__(kWide ? kBwdThreadsWide : kBwdThreads)
+    norm_bwd_kernel(NormBwdArgs a) {
+  extern __shared__ float sums[];  // teams * D (kWide: D) for grad_weight, as many for grad_bias
+  __shared__ float2 red_all[2][kBwdThreadsWide / 32];
+  using Row = RowRegs<T, kWhole>;
+  constexpr int VEC = Row::VEC, NV = Row::NV;
+  const int team = a.team, id = threadIdx.x / team, l = threadIdx.x - id * team;
+  const int lead = team < 32 ? (threadIdx.x & ~31) / team : id;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * a.teams;
+  int64_t first = static_cast<int64_t>(blockIdx.x) * a.teams + lead;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + id;
+  const int D = static_cast<int>(a.D);
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  Row nx, ng;
+  float nmean = 0.0f, nrstd = 0.0f;
+  auto prefetch = [&](int64_t r) {
+    const bool in = r < a.N;
+    const int64_t at = in ? r : 0;
+    nx.load(x + at * a.ldx, in ? D : 0, team, l);
+    ng.load(dy + at * a.lddy, in ? D : 0, team, l);
+    nrstd = in ? a.rstd[at] : 0.0f;
+    if (kCenter) nmean = in ? a.mean[at] : 0.0f;
+  };
+  if (!kWide) prefetch(row);
+  float dw[kLane] = {}, db[kLane] = {};
+  if (kWide) {
+    for (int j = threadIdx.x; j < (kCenter ? 2 : 1) * D; j += blockDim.x) sums[j] = 0.0f;
+    __syncthreads();
+  }
+  const float n = static_cast<float>(D);
+  int parity = 0;
+  for (; first < a.N; first += step, row += step) {
+    if (kWide) prefetch(row);  // no registers for a second row
+    Row cx = nx, cg = ng;
+    const float mean = nmean, rstd = nrstd;
+    const bool in_row = row < a.N;
+    cx.finish(x + (in_row ? row : 0) * a.ldx, in_row ? D : 0, team, l);
+    cg.finish(dy + (in_row ? row : 0) * a.lddy, in_row ? D : 0, team, l);
+    if (!kWide) prefetch(row + step);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float f[VEC], g[VEC];
+      cx.unpack(k, f);
+      cg.unpack(k, g);
+      const int j = (k * team + l) * VEC;
+      if (j >= D) continue;
+      float w[VEC];
+      weight_vec<VEC, kWhole>(a.weight, a.w_f32, j, D, 1.0f, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int i = k * VEC + e;
+        // past the row's end g is 0, and so is all below
+        const float h = __fmul_rn(f[e] - mean, rstd);
+        const float u = __fmul_rn(g[e], w[e]);
+        if (kCenter) s1 = __fadd_rn(s1, u);
+        s2 = __fmaf_rn(u, h, s2);
+        if (kWide) {
+          if (kWhole || j + e < D) {
+            sums[j + e] = __fmaf_rn(g[e], h, sums[j + e]);
+            if (kCenter) sums[D + j + e] = __fadd_rn(sums[D + j + e], g[e]);
+          }
+        } else {
+          dw[i] = __fmaf_rn(g[e], h, dw[i]);
+          if (kCenter) db[i] = __fadd_rn(db[i], g[e]);
+        }
+      }
+    }
+    team_sum<kCenter>(s2, s1, team, id, red_all[parity] + (team > 32 ? id * (team >> 5) : 0));
+    parity ^= 1;
+    if (a.dx == nullptr) continue;
+    const float c1 = s1 / n, c2 = s2 / n;
+    T* dx = static_cast<T*>(a.dx) + (in_row ? row : 0) * a.lddx;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int j = (k * team + l) * VEC;
+      float out[VEC];
+      if (j < D) {
+        float f[VEC], g[VEC], w[VEC];
+        cx.unpack(k, f);
+        cg.unpack(k, g);
+        weight_vec<VEC, kWhole>(a.weight, a.w_f32, j, D, 1.0f, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float h = __fmul_rn(f[e] - mean, rstd);
+          const float u = __fmul_rn(g[e], w[e]);
+          out[e] = __fmul_rn(rstd, __fmaf_rn(-h, c2, u - c1));
+        }
+      }
+      store_vector<T, kWhole>(dx, j, in_row ? D : 0, team, l, out);
+    }
+  }
+  if (a.part == nullptr) return;
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
+  if (!kWide) {
+    // the teams' sums side by side, then in team order
+    float* to = a.teams == 1 ? part : sums + id * D;
+    const int64_t bias_at = static_cast<int64_t>(a.teams) * D;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int j = (k * team + l) * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        if (j + e >= D) continue;
+        to[j + e] = dw[k * VEC + e];
+        if (kCenter) to[bias_at + j + e] = db[k * VEC + e];
+      }
+    }
+    if (a.teams == 1) return;
+  }
+  __syncthreads();
+  const int parts = kWide ? 1 : a.teams;
+  for (int64_t j = threadIdx.x; j < (kCenter ? 2 : 1) * a.D; j += blockDim.x) {
+    const int64_t which = j / a.D, c = j - which * a.D;
+    float s = 0.0f;
+    for (int t = 0; t < parts; ++t) s += sums[(which * parts + t) * a.D + c];
+    part[j] = s;
+  }
+}
+
+// ------------------------------------------------------------ rows too wide to hold
+
+constexpr int kLongThreads = 256;
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int w = 0; w < kLongThreads / 32; ++w) s += red[w];
+  __syncthreads();
+  return s;
+}
+
+__device__ __forceinline__ float weight_at(const void* p, int f32, int64_t j, float other) {
+  if (p == nullptr) return other;
+  return f32 ? static_cast<const float*>(p)[j]
+             : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(p) + j);
+}
+
+// One block per row, the row read again for each pass.
+template <typename T, bool kCenter>
+__global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(NormArgs a) {
+  __shared__ float red[kLongThreads / 32];
+  for (int64_t i = blockIdx.x; i < a.N; i += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + i * a.ldx;
+    T* y = static_cast<T*>(a.y) + i * a.ldy;
+    float mean = 0.0f;
+    if (kCenter) {
+      float s = 0.0f;
+      for (int64_t j = threadIdx.x; j < a.D; j += kLongThreads) s += Elem<T>::load(x + j);
+      mean = block_sum(s, red) / static_cast<float>(a.D);
+    }
+    float q = 0.0f;
+    for (int64_t j = threadIdx.x; j < a.D; j += kLongThreads) {
+      const float d = Elem<T>::load(x + j) - mean;
+      q += d * d;
+    }
+    const float rstd = 1.0f / sqrtf(block_sum(q, red) / static_cast<float>(a.D) + a.eps);
+    for (int64_t j = threadIdx.x; j < a.D; j += kLongThreads) {
+      float v = (Elem<T>::load(x + j) - mean) * rstd * weight_at(a.weight, a.w_f32, j, 1.0f);
+      if (kCenter) v += weight_at(a.bias, a.w_f32, j, 0.0f);
+      Elem<T>::store(y + j, v);
+    }
+    if (threadIdx.x == 0) {
+      if (kCenter && a.mean != nullptr) a.mean[i] = mean;
+      if (a.rstd != nullptr) a.rstd[i] = rstd;
+    }
+  }
+}
+
+template <typename T, bool kCenter>
+__global__ void __launch_bounds__(kLongThreads) norm_bwd_long_kernel(NormBwdArgs a) {
+  __shared__ float red[kLongThreads / 32];
   for (int64_t i = blockIdx.x; i < a.N; i += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + i * a.ldx;
     const T* dy = static_cast<const T*>(a.dy) + i * a.lddy;
     T* dx = static_cast<T*>(a.dx) + i * a.lddx;
     const float mean = kCenter ? a.mean[i] : 0.0f, rstd = a.rstd[i];
     float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t j = threadIdx.x; j < a.D; j += kNormThreads) {
-      const float u = Elem<T>::load(dy + j) * (w != nullptr ? Elem<U>::load(w + j) : 1.0f);
+    for (int64_t j = threadIdx.x; j < a.D; j += kLongThreads) {
+      const float u = Elem<T>::load(dy + j) * weight_at(a.weight, a.w_f32, j, 1.0f);
       s1 += u;
       s2 += u * ((Elem<T>::load(x + j) - mean) * rstd);
     }
     const float c1 = kCenter ? block_sum(s1, red) / static_cast<float>(a.D) : 0.0f;
     const float c2 = block_sum(s2, red) / static_cast<float>(a.D);
-    for (int64_t j = threadIdx.x; j < a.D; j += kNormThreads) {
-      const float u = Elem<T>::load(dy + j) * (w != nullptr ? Elem<U>::load(w + j) : 1.0f);
+    for (int64_t j = threadIdx.x; j < a.D; j += kLongThreads) {
+      const float u = Elem<T>::load(dy + j) * weight_at(a.weight, a.w_f32, j, 1.0f);
       const float h = (Elem<T>::load(x + j) - mean) * rstd;
       Elem<T>::store(dx + j, rstd * (u - c1 - h * c2));
     }
   }
 }
 
-// Column sums of one slice of the rows: 256 columns per block.
+// Column sums of one slice of the rows, 256 columns per block; before
+// norm_bwd_long_kernel, which may overwrite dy.
 template <typename T, bool kCenter>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_cols_kernel(NormBwdArgs a) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
+__global__ void __launch_bounds__(kLongThreads) norm_bwd_long_cols_kernel(NormBwdArgs a) {
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * kLongThreads + threadIdx.x;
   if (j >= a.D) return;
   const int64_t per = (a.N + a.slices - 1) / a.slices;
-  const int64_t i0 = blockIdx.y * per, i1 = i0 + per < a.N ? i0 + per : a.N;
+  const int64_t i0 = min(a.N, blockIdx.y * per), i1 = min(a.N, i0 + per);
   float dw = 0.0f, db = 0.0f;
   for (int64_t i = i0; i < i1; ++i) {
     const float g = Elem<T>::load(static_cast<const T*>(a.dy) + i * a.lddy + j);
@@ -121,19 +553,61 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_cols_kernel(NormBwdArgs
     db += g;
   }
   a.part[(2 * static_cast<int64_t>(blockIdx.y)) * a.D + j] = dw;
-  a.part[(2 * static_cast<int64_t>(blockIdx.y) + 1) * a.D + j] = db;
+  if (kCenter) a.part[(2 * static_cast<int64_t>(blockIdx.y) + 1) * a.D + j] = db;
 }
 
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_finish_kernel(NormBwdArgs a) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
-  if (j >= a.D) return;
-  float dw = 0.0f, db = 0.0f;
-  for (int k = 0; k < a.slices; ++k) {
-    dw += a.part[(2 * static_cast<int64_t>(k)) * a.D + j];
-    db += a.part[(2 * static_cast<int64_t>(k) + 1) * a.D + j];
+// ---------------------------------------------------------------- column sums
+
+// 32 columns per block: 32 warps add up every 32nd slice, then the warps' sums
+// in warp order.  blockIdx.y: grad_weight, grad_bias.
+__global__ void __launch_bounds__(1024) norm_bwd_finish_kernel(NormBwdArgs a) {
+  __shared__ float red[32][33];
+  float* out = blockIdx.y == 0 ? a.dw : a.db;
+  if (out == nullptr) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float s = 0.0f;
+  if (j < a.D) {
+#pragma unroll 8
+    for (int64_t k = warp; k < a.slices; k += 32) s += a.part[(2 * k + blockIdx.y) * a.D + j];
   }
-  if (a.dw != nullptr) a.dw[j] = a.accumulate ? a.dw[j] + dw : dw;
-  if (a.db != nullptr) a.db[j] = a.accumulate ? a.db[j] + db : db;
+  red[warp][lane] = s;
+  __syncthreads();
+  // warp w: the 32 sums of column w
+  s = red[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane == 0 && c < a.D) out[c] = a.accumulate ? out[c] + s : s;
+}
+
+// ------------------------------------------------------------------------ host
+
+// Whether the rows of a matrix start on 16-byte boundaries.
+static bool whole(int dt, const void* p, int64_t ld) {
+  return aligned(p, 16) && ld % (dt == FLCE_BF16 ? 8 : 4) == 0;
+}
+
+constexpr int kFwdBlocks = 4;  // blocks of 256 threads to an SM
+constexpr int kBwdBlocks = 2;
+
+template <typename T, bool kCenter>
+static int launch_norm_fwd(NormArgs a, int dt, cudaStream_t s) {
+  if (a.D > int64_t(kFwdThreads) * kLane) {
+    const int grid = static_cast<int>(std::min<int64_t>(a.N, sm_count() * 8));
+    norm_fwd_long_kernel<T, kCenter><<<grid, kLongThreads, 0, s>>>(a);
+    return launch_status("norm_fwd_long_kernel launch");
+  }
+  const NormPlan p = norm_plan(a.N, a.D, kFwdBlocks);
+  a.team = p.team;
+  a.teams = p.teams;
+  const unsigned grid = static_cast<unsigned>(p.blocks);
+  if (whole(dt, a.x, a.ldx) && whole(dt, a.y, a.ldy) && whole(dt, a.weight, a.D) &&
+      aligned(a.bias, 16))
+    norm_fwd_kernel<T, true, kCenter><<<grid, p.team * p.teams, 0, s>>>(a);
+  else
+    norm_fwd_kernel<T, false, kCenter><<<grid, p.team * p.teams, 0, s>>>(a);
+  return launch_status("norm_fwd_kernel launch");
 }
 
 template <bool kCenter>
@@ -152,18 +626,82 @@ static int norm_fwd(NormArgs a, int dt, int wdt, flce_stream_t stream) {
                            span_bytes(a.N, a.D, a.ldy, es)))
     return FLCE_EINVAL;
   if (a.N == 0) return FLCE_OK;
+  a.w_f32 = wdt == FLCE_F32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int grid = static_cast<int>(std::min<int64_t>(a.N, sm_count() * 8));
-  using B = __nv_bfloat16;
-  if (dt == FLCE_BF16 && wdt == FLCE_BF16)
-    norm_fwd_kernel<B, B, kCenter><<<grid, kNormThreads, 0, s>>>(a);
-  else if (dt == FLCE_BF16)
-    norm_fwd_kernel<B, float, kCenter><<<grid, kNormThreads, 0, s>>>(a);
-  else if (wdt == FLCE_BF16)
-    norm_fwd_kernel<float, B, kCenter><<<grid, kNormThreads, 0, s>>>(a);
-  else
-    norm_fwd_kernel<float, float, kCenter><<<grid, kNormThreads, 0, s>>>(a);
-  return launch_status("norm_fwd_kernel launch");
+  return dt == FLCE_BF16 ? launch_norm_fwd<__nv_bfloat16, kCenter>(a, dt, s)
+                         : launch_norm_fwd<float, kCenter>(a, dt, s);
+}
+
+// Column sums in registers, in shared memory, or by kernels of their own.
+static bool bwd_narrow(int64_t D) { return D <= int64_t(kBwdThreads) * kLane; }
+static bool bwd_held(int64_t D) { return D <= int64_t(kBwdThreadsWide) * kLane; }
+
+static int64_t bwd_slices(int64_t N, int64_t D) {
+  if (bwd_held(D)) return norm_plan(N, D, kBwdBlocks).blocks;
+  return std::min<int64_t>(64, N);
+}
+
+template <typename K>
+static int raise_smem(K kern, int bytes, std::atomic<uint64_t>& raised) {
+  int dev = 0;
+  int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc != FLCE_OK) return rc;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(raised.load() & bit)) {
+    rc = cuda_status(
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+        "cudaFuncSetAttribute(norm_bwd_kernel)");
+    if (rc == FLCE_OK) raised.fetch_or(bit);
+  }
+  return rc;
+}
+
+template <typename T, bool kWhole, bool kCenter>
+static int launch_norm_bwd_held(NormBwdArgs a, cudaStream_t s) {
+  const NormPlan p = norm_plan(a.N, a.D, kBwdBlocks);
+  a.team = p.team;
+  a.teams = p.teams;
+  const unsigned grid = static_cast<unsigned>(p.blocks);
+  const int threads = p.team * p.teams;
+  const size_t per = static_cast<size_t>(a.D) * sizeof(float) * (kCenter ? 2 : 1);
+  if (bwd_narrow(a.D)) {
+    const size_t smem = p.teams > 1 ? p.teams * per : 0;
+    norm_bwd_kernel<T, kWhole, kCenter, false><<<grid, threads, smem, s>>>(a);
+  } else {
+    static std::atomic<uint64_t> raised{0};
+    const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, true>,
+                              2 * kBwdThreadsWide * kLane * static_cast<int>(sizeof(float)),
+                              raised);
+    if (rc != FLCE_OK) return rc;
+    norm_bwd_kernel<T, kWhole, kCenter, true><<<grid, threads, per, s>>>(a);
+  }
+  return launch_status("norm_bwd_kernel launch");
+}
+
+template <typename T, bool kCenter>
+static int launch_norm_bwd(NormBwdArgs a, int dt, cudaStream_t s) {
+  if (a.N > 0 && bwd_held(a.D)) {
+    const bool w = whole(dt, a.x, a.ldx) && whole(dt, a.dy, a.lddy) &&
+                   whole(dt, a.dx, a.dx != nullptr ? a.lddx : 0) && whole(dt, a.weight, a.D);
+    const int rc = w ? launch_norm_bwd_held<T, true, kCenter>(a, s)
+                     : launch_norm_bwd_held<T, false, kCenter>(a, s);
+    if (rc != FLCE_OK) return rc;
+  } else if (a.N > 0) {
+    if (a.part != nullptr) {
+      const dim3 g(static_cast<unsigned>((a.D + kLongThreads - 1) / kLongThreads),
+                   static_cast<unsigned>(a.slices));
+      norm_bwd_long_cols_kernel<T, kCenter><<<g, kLongThreads, 0, s>>>(a);
+    }
+    if (a.dx != nullptr) {
+      const int grid = static_cast<int>(std::min<int64_t>(a.N, sm_count() * 8));
+      norm_bwd_long_kernel<T, kCenter><<<grid, kLongThreads, 0, s>>>(a);
+    }
+  }
+  if (a.dw != nullptr || a.db != nullptr) {
+    const dim3 g(static_cast<unsigned>((a.D + 31) / 32), a.db != nullptr ? 2 : 1);
+    norm_bwd_finish_kernel<<<g, 1024, 0, s>>>(a);
+  }
+  return launch_status("norm_bwd launch");
 }
 
 template <bool kCenter>
@@ -194,33 +732,12 @@ static int norm_bwd(NormBwdArgs a, int dt, int wdt, void* ws, size_t ws_bytes,
     if (need > 0 && (ws == nullptr || ws_bytes < need)) return FLCE_EWORKSPACE;
     if (!aligned(ws, 16)) return FLCE_EALIGN;
   }
+  a.part = cols ? static_cast<float*>(ws) : nullptr;
+  a.slices = a.N > 0 ? bwd_slices(a.N, a.D) : 0;
+  a.w_f32 = wdt == FLCE_F32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  using B = __nv_bfloat16;
-  a.part = static_cast<float*>(ws);
-  a.slices = static_cast<int>(std::min<int64_t>(64, a.N));
-  if (cols) {
-    const unsigned nb = static_cast<unsigned>((a.D + kNormThreads - 1) / kNormThreads);
-    if (a.slices > 0) {
-      const dim3 g(nb, a.slices);
-      if (dt == FLCE_BF16)
-        norm_bwd_cols_kernel<B, kCenter><<<g, kNormThreads, 0, s>>>(a);
-      else
-        norm_bwd_cols_kernel<float, kCenter><<<g, kNormThreads, 0, s>>>(a);
-    }
-    norm_bwd_finish_kernel<<<nb, kNormThreads, 0, s>>>(a);
-  }
-  if (a.dx != nullptr && a.N > 0) {
-    const int grid = static_cast<int>(std::min<int64_t>(a.N, sm_count() * 8));
-    if (dt == FLCE_BF16 && wdt == FLCE_BF16)
-      norm_bwd_rows_kernel<B, B, kCenter><<<grid, kNormThreads, 0, s>>>(a);
-    else if (dt == FLCE_BF16)
-      norm_bwd_rows_kernel<B, float, kCenter><<<grid, kNormThreads, 0, s>>>(a);
-    else if (wdt == FLCE_BF16)
-      norm_bwd_rows_kernel<float, B, kCenter><<<grid, kNormThreads, 0, s>>>(a);
-    else
-      norm_bwd_rows_kernel<float, float, kCenter><<<grid, kNormThreads, 0, s>>>(a);
-  }
-  return launch_status("norm_bwd launch");
+  return dt == FLCE_BF16 ? launch_norm_bwd<__nv_bfloat16, kCenter>(a, dt, s)
+                         : launch_norm_bwd<float, kCenter>(a, dt, s);
 }
 
 }  // namespace flce
@@ -230,19 +747,24 @@ using namespace flce;
 extern "C" int layer_norm_fwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
                               const void* weight, const void* bias, int wdt, float eps, void* y,
                               int64_t ldy, float* mean, float* rstd, flce_stream_t stream) {
-  return norm_fwd<true>({x, N, D, ldx, weight, bias, eps, y, ldy, mean, rstd}, dt, wdt, stream);
+  NormArgs a{};
+  a.x = x, a.N = N, a.D = D, a.ldx = ldx, a.weight = weight, a.bias = bias, a.eps = eps;
+  a.y = y, a.ldy = ldy, a.mean = mean, a.rstd = rstd;
+  return norm_fwd<true>(a, dt, wdt, stream);
 }
 
 extern "C" int rms_norm_fwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
                             const void* weight, int wdt, float eps, void* y, int64_t ldy,
                             float* rstd, flce_stream_t stream) {
-  return norm_fwd<false>({x, N, D, ldx, weight, nullptr, eps, y, ldy, nullptr, rstd}, dt, wdt,
-                         stream);
+  NormArgs a{};
+  a.x = x, a.N = N, a.D = D, a.ldx = ldx, a.weight = weight, a.eps = eps;
+  a.y = y, a.ldy = ldy, a.rstd = rstd;
+  return norm_fwd<false>(a, dt, wdt, stream);
 }
 
 extern "C" size_t norm_bwd_workspace_bytes(int64_t N, int64_t D) {
   if (N < 1 || D < 1) return 0;
-  return 64 * 2 * round_up(static_cast<size_t>(D) * 4, 256);
+  return round_up(static_cast<size_t>(bwd_slices(N, D)) * 2 * static_cast<size_t>(D) * 4, 256);
 }
 
 extern "C" int layer_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
@@ -250,16 +772,19 @@ extern "C" int layer_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64
                               const float* mean, const float* rstd, void* grad_x, int64_t ldgx,
                               float* grad_weight, float* grad_bias, int accumulate, void* ws,
                               size_t ws_bytes, flce_stream_t stream) {
-  return norm_bwd<true>({x, N, D, ldx, grad_y, ldgy, weight, mean, rstd, grad_x, ldgx,
-                         grad_weight, grad_bias, accumulate, nullptr, 0},
-                        dt, wdt, ws, ws_bytes, stream);
+  NormBwdArgs a{};
+  a.x = x, a.N = N, a.D = D, a.ldx = ldx, a.dy = grad_y, a.lddy = ldgy, a.weight = weight;
+  a.mean = mean, a.rstd = rstd, a.dx = grad_x, a.lddx = ldgx, a.dw = grad_weight;
+  a.db = grad_bias, a.accumulate = accumulate;
+  return norm_bwd<true>(a, dt, wdt, ws, ws_bytes, stream);
 }
 
 extern "C" int rms_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
                             const void* grad_y, int64_t ldgy, const void* weight, int wdt,
                             const float* rstd, void* grad_x, int64_t ldgx, float* grad_weight,
                             int accumulate, void* ws, size_t ws_bytes, flce_stream_t stream) {
-  return norm_bwd<false>({x, N, D, ldx, grad_y, ldgy, weight, nullptr, rstd, grad_x, ldgx,
-                          grad_weight, nullptr, accumulate, nullptr, 0},
-                         dt, wdt, ws, ws_bytes, stream);
+  NormBwdArgs a{};
+  a.x = x, a.N = N, a.D = D, a.ldx = ldx, a.dy = grad_y, a.lddy = ldgy, a.weight = weight;
+  a.rstd = rstd, a.dx = grad_x, a.lddx = ldgx, a.dw = grad_weight, a.accumulate = accumulate;
+  return norm_bwd<false>(a, dt, wdt, ws, ws_bytes, stream);
 }

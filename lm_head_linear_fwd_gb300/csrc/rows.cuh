@@ -28,4 +28,108 @@ inline int check_matrix(const void* p, int dt, int64_t rows, int64_t cols, int64
   return FLCE_OK;
 }
 
+// VEC consecutive elements of T in fp32, loaded and stored as one access of
+// VEC * sizeof(T) bytes (2 to 16).
+template <typename T, int VEC>
+struct Vec {
+  static_assert(VEC * sizeof(T) <= 16, "one access");
+  float x[VEC];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == Elem<T>::kPerVec) {
+      Elem<T>::unpack(*reinterpret_cast<const uint4*>(p), x);
+    } else if constexpr (VEC == 2 && sizeof(T) == 2) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+      x[0] = bf16_lo(w);
+      x[1] = bf16_hi(w);
+    } else {
+      static_assert(VEC == 1, "16 or 4 bytes, or one element");
+      x[0] = Elem<T>::load(p);
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (VEC == Elem<T>::kPerVec) {
+      *reinterpret_cast<uint4*>(p) = Elem<T>::pack(x);
+    } else if constexpr (VEC == 2 && sizeof(T) == 2) {
+      *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x[0], x[1]);
+    } else {
+      static_assert(VEC == 1, "16 or 4 bytes, or one element");
+      Elem<T>::store(p, x[0]);
+    }
+  }
+};
+
+// VEC elements of T as they lie in memory, to be unpacked when used (half the
+// registers of Vec for bf16).
+template <typename T, int VEC>
+struct RawVec {
+  static constexpr int kWords = VEC * sizeof(T) >= 4 ? VEC * sizeof(T) / 4 : 1;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (VEC * sizeof(T) == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      static_assert(VEC * sizeof(T) == 2, "16, 4 or 2 bytes");
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = 0u;
+  }
+  __device__ __forceinline__ void unpack(float (&x)[VEC]) const {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if constexpr (sizeof(T) == 4)
+        x[e] = __uint_as_float(w[e]);
+      else
+        x[e] = (e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+    }
+  }
+};
+
+// VEC values of type G as fp32, in accesses of at most 16 bytes (the address is
+// aligned to them).
+template <typename G, int VEC>
+__device__ __forceinline__ void load_as(const G* p, float (&x)[VEC]) {
+  constexpr int W = VEC < Elem<G>::kPerVec ? VEC : Elem<G>::kPerVec;
+#pragma unroll
+  for (int k = 0; k < VEC; k += W) {
+    if constexpr (W == 4 && sizeof(G) == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + k);
+      x[k] = bf16_lo(v.x);
+      x[k + 1] = bf16_hi(v.x);
+      x[k + 2] = bf16_lo(v.y);
+      x[k + 3] = bf16_hi(v.y);
+    } else {
+      Vec<G, W> v;
+      v.load(p + k);
+#pragma unroll
+      for (int e = 0; e < W; ++e) x[k + e] = v.x[e];
+    }
+  }
+}
+
+// VEC fp32 values stored as type G in accesses of at most 16 bytes.
+template <typename G, int VEC>
+__device__ __forceinline__ void store_as(G* p, const float (&x)[VEC]) {
+  constexpr int W = VEC < Elem<G>::kPerVec ? VEC : Elem<G>::kPerVec;
+#pragma unroll
+  for (int k = 0; k < VEC; k += W) {
+    if constexpr (W == 2 && sizeof(G) == 4) {
+      *reinterpret_cast<float2*>(p + k) = make_float2(x[k], x[k + 1]);
+    } else if constexpr (W == 4 && sizeof(G) == 2) {
+      *reinterpret_cast<uint2*>(p + k) =
+          make_uint2(pack_bf16x2(x[k], x[k + 1]), pack_bf16x2(x[k + 2], x[k + 3]));
+    } else {
+      Vec<G, W> v;
+#pragma unroll
+      for (int e = 0; e < W; ++e) v.x[e] = x[k + e];
+      v.store(p + k);
+    }
+  }
+}
+
 }  // namespace flce
