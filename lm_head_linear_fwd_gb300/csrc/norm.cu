@@ -23,10 +23,11 @@
 
 namespace flce {
 
-constexpr int kLane = 16;             // elements of a row per thread
-constexpr int kFwdThreads = 1024;     // most threads of a block
-constexpr int kBwdThreads = 512;      // with the column sums in registers
-constexpr int kBwdThreadsWide = 1024; // with the column sums in shared memory
+constexpr int kFwdLane = 32;           // elements of a row per thread
+constexpr int kBwdLane = 16;           // the column sums take twice as many again
+constexpr int kFwdThreads = 512;       // most threads of a block
+constexpr int kBwdThreads = 512;       // with the column sums in registers
+constexpr int kBwdThreadsWide = 1024;  // with the column sums in shared memory
 
 // How a row is spread: `team` threads to a row (a power of two up to a warp,
 // then whole warps), `teams` rows at a time in a block.
@@ -35,11 +36,11 @@ struct NormPlan {
   int64_t blocks;
 };
 
-static NormPlan norm_plan(int64_t N, int64_t D, int blocks_of_256) {
+static NormPlan norm_plan(int64_t N, int64_t D, int lane, int blocks_of_256) {
   NormPlan p;
-  const int64_t need = (D + kLane - 1) / kLane;
+  const int64_t need = (D + lane - 1) / lane;
   if (need <= 32) {
-    p.team = 4;
+    p.team = 1;
     while (p.team < need) p.team *= 2;
   } else {
     p.team = static_cast<int>((need + 31) / 32 * 32);
@@ -85,18 +86,22 @@ __device__ __forceinline__ uint4 row_block(const void* base, int i) {
 }
 
 // kLane elements of a row.
-template <typename T, bool kWhole>
+template <typename T, bool kWhole, int kLane>
 struct RowRegs {
   static constexpr int VEC = 16 / sizeof(T), NV = kLane / VEC;
   uint4 v[NV];       // loaded blocks; after finish(): the row's vectors
-  // starts the loads of a row (none for D = 0)
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = make_uint4(0, 0, 0, 0);
+  }
+  // starts the loads of a row
   __device__ __forceinline__ void load(const T* p, int D, int team, int l) {
     const char* base = reinterpret_cast<const char*>(p);
     if (!kWhole) base -= reinterpret_cast<uintptr_t>(p) & 15;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = k * team + l;
-      v[k] = i * VEC < D ? row_block(base, i) : make_uint4(0, 0, 0, 0);
+      if (i * VEC < D) v[k] = row_block(base, i);
     }
   }
   // the vectors themselves, zeros past the row's end
@@ -138,8 +143,12 @@ struct RowRegs {
       v[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  __device__ __forceinline__ void unpack(int k, float (&x)[VEC]) const {
-    Elem<T>::unpack(v[k], x);
+  // vector k as pairs (for the packed fp32 instructions)
+  __device__ __forceinline__ void unpack(int k, float2 (&x)[VEC / 2]) const {
+    float f[VEC];
+    Elem<T>::unpack(v[k], f);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) x[e] = make_float2(f[2 * e], f[2 * e + 1]);
   }
 };
 
@@ -149,8 +158,11 @@ struct RowRegs {
 // is full; what no such block covers goes element by element.
 template <typename T, bool kWhole>
 __device__ __forceinline__ void store_vector(T* row, int j, int D, int team, int l,
-                                             const float (&x)[16 / sizeof(T)]) {
+                                             const float2 (&pairs)[8 / sizeof(T)]) {
   constexpr int VEC = 16 / sizeof(T);
+  float x[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC / 2; ++e) x[2 * e] = pairs[e].x, x[2 * e + 1] = pairs[e].y;
   const uint4 own = Elem<T>::pack(x);
   if (kWhole) {
     if (j < D) *reinterpret_cast<uint4*>(row + j) = own;
@@ -206,29 +218,40 @@ __device__ __forceinline__ void store_vector(T* row, int j, int D, int team, int
   }
 }
 
-// VEC elements of a weight vector from column j on (read again for every row: they
-// stay in the L1 cache, and registers are what bounds the rows in flight).
-template <int VEC, bool kWhole>
-__device__ __forceinline__ void weight_vec(const void* p, int f32, int j, int D, float other,
-                                           float (&x)[VEC]) {
-  if (p == nullptr) {
+// A weight vector in shared memory as fp32: of each row vector's VEC weights
+// four together, the quarters of all vectors first, so that 16-byte reads of
+// neighbouring threads lie next to each other.  Zeros past the end.
+template <int VEC>
+__device__ __forceinline__ void stage_weights(float4* to, const void* p, int f32, float other,
+                                              int D) {
+  const int nvec = (D + VEC - 1) / VEC;
+  for (int q = threadIdx.x; q < nvec * (VEC / 4); q += blockDim.x) {
+    const int j = q % nvec * VEC + q / nvec * 4;
+    float v[4];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = other;
-  } else if (kWhole || (j + VEC <= D && (reinterpret_cast<uintptr_t>(p) & 15) == 0)) {
-    if (f32)
-      load_as<float, VEC>(static_cast<const float*>(p) + j, x);
-    else
-      load_as<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(p) + j, x);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      x[e] = other;
-      if (j + e < D)
-        x[e] = f32 ? static_cast<const float*>(p)[j + e]
+    for (int e = 0; e < 4; ++e) {
+      v[e] = j + e < D ? other : 0.0f;
+      if (p != nullptr && j + e < D)
+        v[e] = f32 ? static_cast<const float*>(p)[j + e]
                    : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(p) + j + e);
     }
+    to[q] = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
+
+// The weights of vector i.
+template <int VEC>
+__device__ __forceinline__ void weight_vec(const float4* w, int nvec, int i,
+                                           float2 (&pairs)[VEC / 2]) {
+#pragma unroll
+  for (int q = 0; q < VEC / 4; ++q) {
+    const float4 v = w[q * nvec + i];
+    pairs[2 * q] = make_float2(v.x, v.y);
+    pairs[2 * q + 1] = make_float2(v.z, v.w);
+  }
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 struct NormArgs {
   const void* x;
@@ -246,9 +269,10 @@ struct NormArgs {
 
 template <typename T, bool kWhole, bool kCenter>
 __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(NormArgs a) {
+  extern __shared__ float4 weights[];  // weight, then bias
   __shared__ float2 red_all[2][kFwdThreads / 32];
-  using Row = RowRegs<T, kWhole>;
-  constexpr int VEC = Row::VEC, NV = Row::NV;
+  using Row = RowRegs<T, kWhole, kFwdLane>;
+  constexpr int VEC = Row::VEC, NV = Row::NV, P = VEC / 2;
   const int team = a.team, id = threadIdx.x / team, l = threadIdx.x - id * team;
   float2* red0 = red_all[0] + (team > 32 ? id * (team >> 5) : 0);
   float2* red1 = red_all[1] + (team > 32 ? id * (team >> 5) : 0);
@@ -259,61 +283,78 @@ __global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(NormArgs a) {
   int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + id;
   const int D = static_cast<int>(a.D);
   const T* x = static_cast<const T*>(a.x);
+  const T* xr = x + (row < a.N ? row : 0) * a.ldx;
+  T* yr = static_cast<T*>(a.y) + (row < a.N ? row : 0) * a.ldy;
   Row next;
-  next.load(x + (row < a.N ? row : 0) * a.ldx, row < a.N ? D : 0, team, l);
+  next.clear();
+  if (row < a.N) next.load(xr, D, team, l);
+  const int nvec = (D + VEC - 1) / VEC;
+  const float4* bias = weights + nvec * (VEC / 4);
+  stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
+  if (kCenter) stage_weights<VEC>(weights + nvec * (VEC / 4), a.bias, a.w_f32, 0.0f, D);
+  __syncthreads();
   const float n = static_cast<float>(D);
-  for (; first < a.N; first += step, row += step) {
-    Row cur = next;
+  for (; first < a.N; first += step) {
     const bool in_row = row < a.N;
-    cur.finish(x + (in_row ? row : 0) * a.ldx, in_row ? D : 0, team, l);
-    const int64_t ahead = row + step;
-    next.load(x + (ahead < a.N ? ahead : 0) * a.ldx, ahead < a.N ? D : 0, team, l);
+    if (in_row) next.finish(xr, D, team, l);
+    float2 f[NV][P];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) next.unpack(k, f[k]);
+    const int64_t here = row;
+    row += step;
+    if (row < a.N) {
+      xr += step * a.ldx;
+      next.load(xr, D, team, l);
+    }
     float mean = 0.0f, none = 0.0f;
     if (kCenter) {
+      float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        float f[VEC];
-        cur.unpack(k, f);
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) mean += f[e];
-      }
+        for (int e = 0; e < P; ++e) s = __fadd2_rn(s, f[k][e]);
+      mean = __fadd_rn(s.x, s.y);
       team_sum<false>(mean, none, team, id, red0);
       mean /= n;
     }
-    float q = 0.0f;
+    float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float f[VEC];
-      cur.unpack(k, f);
       const int j = (k * team + l) * VEC;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = f[e] - mean;
-        if ((kWhole ? j : j + e) < D) q = __fmaf_rn(d, d, q);
+      for (int e = 0; e < P; ++e) {
+        if (kCenter) f[k][e] = __fadd2_rn(f[k][e], both(-mean));
+        // past the row's end the elements are 0, less the mean: left out
+        float2 d = f[k][e];
+        if (!kWhole && kCenter) {
+          if (j + 2 * e >= D) d.x = 0.0f;
+          if (j + 2 * e + 1 >= D) d.y = 0.0f;
+        }
+        if (!kWhole || j < D) q = __ffma2_rn(d, d, q);
       }
     }
-    team_sum<false>(q, none, team, id, red1);
-    const float rstd = 1.0f / sqrtf(q / n + a.eps);
-    T* yr = static_cast<T*>(a.y) + (in_row ? row : 0) * a.ldy;
+    float qs = __fadd_rn(q.x, q.y);
+    team_sum<false>(qs, none, team, id, red1);
+    const float rstd = 1.0f / sqrtf(qs / n + a.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int j = (k * team + l) * VEC;
-      float f[VEC], w[VEC], b[VEC];
       if (j < D) {
-        weight_vec<VEC, kWhole>(a.weight, a.w_f32, j, D, 1.0f, w);
-        if (kCenter) weight_vec<VEC, kWhole>(a.bias, a.w_f32, j, D, 0.0f, b);
-        cur.unpack(k, f);
+        float2 w[P], b[P];
+        weight_vec<VEC>(weights, nvec, k * team + l, w);
+        if (kCenter) weight_vec<VEC>(bias, nvec, k * team + l, b);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float h = __fmul_rn(f[e] - mean, rstd);
-          f[e] = kCenter ? __fmaf_rn(h, w[e], b[e]) : __fmul_rn(h, w[e]);
+        for (int e = 0; e < P; ++e) {
+          const float2 h = __fmul2_rn(f[k][e], both(rstd));
+          f[k][e] = kCenter ? __ffma2_rn(h, w[e], b[e]) : __fmul2_rn(h, w[e]);
         }
       }
-      store_vector<T, kWhole>(yr, j, in_row ? D : 0, team, l, f);
+      store_vector<T, kWhole>(yr, j, in_row ? D : 0, team, l, f[k]);
     }
+    if (row < a.N) yr += step * a.ldy;
     if (l == 0 && in_row) {
-      if (kCenter && a.mean != nullptr) a.mean[row] = mean;
-      if (a.rstd != nullptr) a.rstd[row] = rstd;
+      if (kCenter && a.mean != nullptr) a.mean[here] = mean;
+      if (a.rstd != nullptr) a.rstd[here] = rstd;
     }
     if (!kCenter && team > 32) named_barrier(1 + id, team);  // red1 is free again
   }
@@ -342,96 +383,112 @@ struct NormBwdArgs {
 template <typename T, bool kWhole, bool kCenter, bool kWide>
 __global__ void __launch_bounds__(kWide ? kBwdThreadsWide : kBwdThreads)
     norm_bwd_kernel(NormBwdArgs a) {
-  extern __shared__ float sums[];  // teams * D (kWide: D) for grad_weight, as many for grad_bias
+  // weight; column sums: teams * D (kWide: D) for grad_weight, as many for grad_bias
+  extern __shared__ float4 weights[];
   __shared__ float2 red_all[2][kBwdThreadsWide / 32];
-  using Row = RowRegs<T, kWhole>;
-  constexpr int VEC = Row::VEC, NV = Row::NV;
+  using Row = RowRegs<T, kWhole, kBwdLane>;
+  constexpr int VEC = Row::VEC, NV = Row::NV, P = VEC / 2;
   const int team = a.team, id = threadIdx.x / team, l = threadIdx.x - id * team;
   const int lead = team < 32 ? (threadIdx.x & ~31) / team : id;
   const int64_t step = static_cast<int64_t>(gridDim.x) * a.teams;
   int64_t first = static_cast<int64_t>(blockIdx.x) * a.teams + lead;
   int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + id;
   const int D = static_cast<int>(a.D);
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
+  const T* xr = static_cast<const T*>(a.x) + (row < a.N ? row : 0) * a.ldx;
+  const T* gr = static_cast<const T*>(a.dy) + (row < a.N ? row : 0) * a.lddy;
+  T* dxr = static_cast<T*>(a.dx) + (row < a.N ? row : 0) * a.lddx;
+  const int nvec = (D + VEC - 1) / VEC;
+  float* sums = reinterpret_cast<float*>(weights + nvec * (VEC / 4));
   Row nx, ng;
   float nmean = 0.0f, nrstd = 0.0f;
-  auto prefetch = [&](int64_t r) {
-    const bool in = r < a.N;
-    const int64_t at = in ? r : 0;
-    nx.load(x + at * a.ldx, in ? D : 0, team, l);
-    ng.load(dy + at * a.lddy, in ? D : 0, team, l);
-    nrstd = in ? a.rstd[at] : 0.0f;
-    if (kCenter) nmean = in ? a.mean[at] : 0.0f;
+  nx.clear();
+  ng.clear();
+  auto prefetch = [&]() {
+    if (row >= a.N) return;
+    nx.load(xr, D, team, l);
+    ng.load(gr, D, team, l);
+    nrstd = a.rstd[row];
+    if (kCenter) nmean = a.mean[row];
   };
-  if (!kWide) prefetch(row);
-  float dw[kLane] = {}, db[kLane] = {};
+  if (!kWide) prefetch();
+  stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
+  float2 dw[NV][P] = {}, db[NV][P] = {};
   if (kWide) {
     for (int j = threadIdx.x; j < (kCenter ? 2 : 1) * D; j += blockDim.x) sums[j] = 0.0f;
-    __syncthreads();
   }
+  __syncthreads();
   const float n = static_cast<float>(D);
   int parity = 0;
-  for (; first < a.N; first += step, row += step) {
-    if (kWide) prefetch(row);  // no registers for a second row
-    Row cx = nx, cg = ng;
-    const float mean = nmean, rstd = nrstd;
+  for (; first < a.N; first += step) {
+    if (kWide) prefetch();  // no registers for a second row
     const bool in_row = row < a.N;
-    cx.finish(x + (in_row ? row : 0) * a.ldx, in_row ? D : 0, team, l);
-    cg.finish(dy + (in_row ? row : 0) * a.lddy, in_row ? D : 0, team, l);
-    if (!kWide) prefetch(row + step);
-    float s1 = 0.0f, s2 = 0.0f;
+    const float mean = nmean, rstd = nrstd;
+    if (in_row) {
+      nx.finish(xr, D, team, l);
+      ng.finish(gr, D, team, l);
+    } else {
+      ng.clear();  // adds nothing to the column sums
+    }
+    float2 h[NV][P], u[NV][P];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float f[VEC], g[VEC];
-      cx.unpack(k, f);
-      cg.unpack(k, g);
+      nx.unpack(k, h[k]);
+      ng.unpack(k, u[k]);
+    }
+    row += step;
+    if (row < a.N) xr += step * a.ldx, gr += step * a.lddy;
+    if (!kWide) prefetch();
+    float2 s1 = make_float2(0.0f, 0.0f), s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
       const int j = (k * team + l) * VEC;
       if (j >= D) continue;
-      float w[VEC];
-      weight_vec<VEC, kWhole>(a.weight, a.w_f32, j, D, 1.0f, w);
+      float2 w[P];
+      weight_vec<VEC>(weights, nvec, k * team + l, w);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int i = k * VEC + e;
-        // past the row's end g is 0, and so is all below
-        const float h = __fmul_rn(f[e] - mean, rstd);
-        const float u = __fmul_rn(g[e], w[e]);
-        if (kCenter) s1 = __fadd_rn(s1, u);
-        s2 = __fmaf_rn(u, h, s2);
+      for (int e = 0; e < P; ++e) {
+        // past the row's end the incoming gradient is 0, and so are all sums
+        if (kCenter) h[k][e] = __fadd2_rn(h[k][e], both(-mean));
+        h[k][e] = __fmul2_rn(h[k][e], both(rstd));
+        const float2 g = u[k][e];
+        u[k][e] = __fmul2_rn(g, w[e]);
+        if (kCenter) s1 = __fadd2_rn(s1, u[k][e]);
+        s2 = __ffma2_rn(u[k][e], h[k][e], s2);
         if (kWide) {
-          if (kWhole || j + e < D) {
-            sums[j + e] = __fmaf_rn(g[e], h, sums[j + e]);
-            if (kCenter) sums[D + j + e] = __fadd_rn(sums[D + j + e], g[e]);
+          const int at = j + 2 * e;
+          if (kWhole || at < D) {
+            sums[at] = __fmaf_rn(g.x, h[k][e].x, sums[at]);
+            if (kCenter) sums[D + at] = __fadd_rn(sums[D + at], g.x);
+          }
+          if (kWhole || at + 1 < D) {
+            sums[at + 1] = __fmaf_rn(g.y, h[k][e].y, sums[at + 1]);
+            if (kCenter) sums[D + at + 1] = __fadd_rn(sums[D + at + 1], g.y);
           }
         } else {
-          dw[i] = __fmaf_rn(g[e], h, dw[i]);
-          if (kCenter) db[i] = __fadd_rn(db[i], g[e]);
+          dw[k][e] = __ffma2_rn(g, h[k][e], dw[k][e]);
+          if (kCenter) db[k][e] = __fadd2_rn(db[k][e], g);
         }
       }
     }
-    team_sum<kCenter>(s2, s1, team, id, red_all[parity] + (team > 32 ? id * (team >> 5) : 0));
+    float c1 = __fadd_rn(s1.x, s1.y), c2 = __fadd_rn(s2.x, s2.y);
+    team_sum<kCenter>(c2, c1, team, id, red_all[parity] + (team > 32 ? id * (team >> 5) : 0));
     parity ^= 1;
     if (a.dx == nullptr) continue;
-    const float c1 = s1 / n, c2 = s2 / n;
-    T* dx = static_cast<T*>(a.dx) + (in_row ? row : 0) * a.lddx;
+    c1 /= n;
+    c2 /= n;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int j = (k * team + l) * VEC;
-      float out[VEC];
-      if (j < D) {
-        float f[VEC], g[VEC], w[VEC];
-        cx.unpack(k, f);
-        cg.unpack(k, g);
-        weight_vec<VEC, kWhole>(a.weight, a.w_f32, j, D, 1.0f, w);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float h = __fmul_rn(f[e] - mean, rstd);
-          const float u = __fmul_rn(g[e], w[e]);
-          out[e] = __fmul_rn(rstd, __fmaf_rn(-h, c2, u - c1));
-        }
+      for (int e = 0; e < P; ++e) {
+        float2 t = u[k][e];
+        if (kCenter) t = __fadd2_rn(t, both(-c1));
+        t = __ffma2_rn(h[k][e], both(-c2), t);
+        u[k][e] = __fmul2_rn(t, both(rstd));
       }
-      store_vector<T, kWhole>(dx, j, in_row ? D : 0, team, l, out);
+      store_vector<T, kWhole>(dxr, j, in_row ? D : 0, team, l, u[k]);
     }
+    if (row < a.N) dxr += step * a.lddx;
   }
   if (a.part == nullptr) return;
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
@@ -445,8 +502,8 @@ __global__ void __launch_bounds__(kWide ? kBwdThreadsWide : kBwdThreads)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         if (j + e >= D) continue;
-        to[j + e] = dw[k * VEC + e];
-        if (kCenter) to[bias_at + j + e] = db[k * VEC + e];
+        to[j + e] = (e & 1) ? dw[k][e / 2].y : dw[k][e / 2].x;
+        if (kCenter) to[bias_at + j + e] = (e & 1) ? db[k][e / 2].y : db[k][e / 2].x;
       }
     }
     if (a.teams == 1) return;
@@ -588,25 +645,53 @@ static bool whole(int dt, const void* p, int64_t ld) {
   return aligned(p, 16) && ld % (dt == FLCE_BF16 ? 8 : 4) == 0;
 }
 
-constexpr int kFwdBlocks = 4;  // blocks of 256 threads to an SM
+constexpr int kFwdBlocks = 2;  // blocks of 256 threads to an SM
 constexpr int kBwdBlocks = 2;
+
+// A weight vector in shared memory, to whole row vectors.
+static size_t weight_bytes(int64_t D) { return round_up(static_cast<size_t>(D), 8) * 4; }
+
+constexpr int kSmemMost = 224 * 1024;
+
+// Allows a kernel kSmemMost bytes of shared memory, once per device.
+template <typename K>
+static int raise_smem(K kern, std::atomic<uint64_t>& raised) {
+  int dev = 0;
+  int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc != FLCE_OK) return rc;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(raised.load() & bit)) {
+    rc = cuda_status(
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost),
+        "cudaFuncSetAttribute(norm kernel)");
+    if (rc == FLCE_OK) raised.fetch_or(bit);
+  }
+  return rc;
+}
 
 template <typename T, bool kCenter>
 static int launch_norm_fwd(NormArgs a, int dt, cudaStream_t s) {
-  if (a.D > int64_t(kFwdThreads) * kLane) {
+  if (a.D > int64_t(kFwdThreads) * kFwdLane) {
     const int grid = static_cast<int>(std::min<int64_t>(a.N, sm_count() * 8));
     norm_fwd_long_kernel<T, kCenter><<<grid, kLongThreads, 0, s>>>(a);
     return launch_status("norm_fwd_long_kernel launch");
   }
-  const NormPlan p = norm_plan(a.N, a.D, kFwdBlocks);
+  const NormPlan p = norm_plan(a.N, a.D, kFwdLane, kFwdBlocks);
   a.team = p.team;
   a.teams = p.teams;
   const unsigned grid = static_cast<unsigned>(p.blocks);
-  if (whole(dt, a.x, a.ldx) && whole(dt, a.y, a.ldy) && whole(dt, a.weight, a.D) &&
-      aligned(a.bias, 16))
-    norm_fwd_kernel<T, true, kCenter><<<grid, p.team * p.teams, 0, s>>>(a);
-  else
-    norm_fwd_kernel<T, false, kCenter><<<grid, p.team * p.teams, 0, s>>>(a);
+  const size_t smem = weight_bytes(a.D) * (kCenter ? 2 : 1);
+  if (whole(dt, a.x, a.ldx) && whole(dt, a.y, a.ldy) && whole(dt, nullptr, a.D)) {
+    static std::atomic<uint64_t> raised{0};
+    const int rc = raise_smem(norm_fwd_kernel<T, true, kCenter>, raised);
+    if (rc != FLCE_OK) return rc;
+    norm_fwd_kernel<T, true, kCenter><<<grid, p.team * p.teams, smem, s>>>(a);
+  } else {
+    static std::atomic<uint64_t> raised{0};
+    const int rc = raise_smem(norm_fwd_kernel<T, false, kCenter>, raised);
+    if (rc != FLCE_OK) return rc;
+    norm_fwd_kernel<T, false, kCenter><<<grid, p.team * p.teams, smem, s>>>(a);
+  }
   return launch_status("norm_fwd_kernel launch");
 }
 
@@ -633,47 +718,34 @@ static int norm_fwd(NormArgs a, int dt, int wdt, flce_stream_t stream) {
 }
 
 // Column sums in registers, in shared memory, or by kernels of their own.
-static bool bwd_narrow(int64_t D) { return D <= int64_t(kBwdThreads) * kLane; }
-static bool bwd_held(int64_t D) { return D <= int64_t(kBwdThreadsWide) * kLane; }
+static bool bwd_narrow(int64_t D) { return D <= int64_t(kBwdThreads) * kBwdLane; }
+static bool bwd_held(int64_t D) { return D <= int64_t(kBwdThreadsWide) * kBwdLane; }
 
 static int64_t bwd_slices(int64_t N, int64_t D) {
-  if (bwd_held(D)) return norm_plan(N, D, kBwdBlocks).blocks;
+  if (bwd_held(D)) return norm_plan(N, D, kBwdLane, kBwdBlocks).blocks;
   return std::min<int64_t>(64, N);
-}
-
-template <typename K>
-static int raise_smem(K kern, int bytes, std::atomic<uint64_t>& raised) {
-  int dev = 0;
-  int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
-  if (rc != FLCE_OK) return rc;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(raised.load() & bit)) {
-    rc = cuda_status(
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
-        "cudaFuncSetAttribute(norm_bwd_kernel)");
-    if (rc == FLCE_OK) raised.fetch_or(bit);
-  }
-  return rc;
 }
 
 template <typename T, bool kWhole, bool kCenter>
 static int launch_norm_bwd_held(NormBwdArgs a, cudaStream_t s) {
-  const NormPlan p = norm_plan(a.N, a.D, kBwdBlocks);
+  const NormPlan p = norm_plan(a.N, a.D, kBwdLane, kBwdBlocks);
   a.team = p.team;
   a.teams = p.teams;
   const unsigned grid = static_cast<unsigned>(p.blocks);
   const int threads = p.team * p.teams;
   const size_t per = static_cast<size_t>(a.D) * sizeof(float) * (kCenter ? 2 : 1);
+  const size_t w = weight_bytes(a.D);
   if (bwd_narrow(a.D)) {
-    const size_t smem = p.teams > 1 ? p.teams * per : 0;
+    static std::atomic<uint64_t> raised{0};
+    const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, false>, raised);
+    if (rc != FLCE_OK) return rc;
+    const size_t smem = w + (p.teams > 1 ? p.teams * per : 0);
     norm_bwd_kernel<T, kWhole, kCenter, false><<<grid, threads, smem, s>>>(a);
   } else {
     static std::atomic<uint64_t> raised{0};
-    const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, true>,
-                              2 * kBwdThreadsWide * kLane * static_cast<int>(sizeof(float)),
-                              raised);
+    const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, true>, raised);
     if (rc != FLCE_OK) return rc;
-    norm_bwd_kernel<T, kWhole, kCenter, true><<<grid, threads, per, s>>>(a);
+    norm_bwd_kernel<T, kWhole, kCenter, true><<<grid, threads, w + per, s>>>(a);
   }
   return launch_status("norm_bwd_kernel launch");
 }
@@ -682,7 +754,7 @@ template <typename T, bool kCenter>
 static int launch_norm_bwd(NormBwdArgs a, int dt, cudaStream_t s) {
   if (a.N > 0 && bwd_held(a.D)) {
     const bool w = whole(dt, a.x, a.ldx) && whole(dt, a.dy, a.lddy) &&
-                   whole(dt, a.dx, a.dx != nullptr ? a.lddx : 0) && whole(dt, a.weight, a.D);
+                   whole(dt, a.dx, a.dx != nullptr ? a.lddx : 0) && whole(dt, nullptr, a.D);
     const int rc = w ? launch_norm_bwd_held<T, true, kCenter>(a, s)
                      : launch_norm_bwd_held<T, false, kCenter>(a, s);
     if (rc != FLCE_OK) return rc;
