@@ -1,21 +1,23 @@
 // Layer norm and RMS norm, forward and backward.
 //
 // Both are bound by the bytes of their rows, so a row is read once and stays in
-// registers: a team of threads holds it, kLane elements to a thread, loads the
-// next row before it works on this one, and sums by shuffles and one shared
-// word per warp.  The square sum is taken around the mean from the registers.
-// The threads' columns are the same for every row: the backward pass adds up its
-// columns of grad_weight and grad_bias in registers (in shared memory for the widest rows) over all rows of a block;
-// one partial sum per block, which norm_bwd_finish_kernel adds in block order.
+// registers: a team of threads holds it, a few 16-byte vectors to a thread, and
+// sums by shuffles and one shared word per warp.  The square sum is taken around
+// the mean from the registers.  What the memory needs is bytes in flight: each
+// thread copies its own vectors of the next rows to shared memory (cp.async, no
+// barrier: it reads back what it copied), which costs no registers.  A thread's
+// columns are the same for every row: the backward pass adds up its columns of
+// grad_weight and grad_bias in registers over all rows of a block; one partial
+// sum per block, which norm_bwd_finish_kernel adds in block order.
 //
-// Each warp holds a run of 16-byte vectors of the row, wherever the row lies, and
-// the roundings are written out, so the results do not depend on strides and
+// Vector k of thread l of a team is k * team + l, wherever the row lies, and the
+// roundings are written out, so the results do not depend on strides and
 // alignment.  Rows that start inside 16-byte blocks (kWhole = false) are read by
-// whole blocks all the same: a vector is shifted together from two blocks, the
-// second of which a neighbour has brought into the L1 cache, and written the
-// other way round with the neighbour's words; only the ends of a warp's run go
-// element by element.  Bytes of a block outside the row are neither used nor
-// written; a block with one byte of the row lies within mapped memory as a whole.
+// whole blocks all the same: a vector is shifted together from its own block and
+// its right neighbour's, and written the other way round with the left
+// neighbour's words; only the ends of a warp's vectors go element by element.
+// Bytes of a block outside the row are neither used nor written; a block with one
+// byte of the row lies within mapped memory as a whole.
 #include <algorithm>
 #include <atomic>
 
@@ -23,15 +25,15 @@
 
 namespace flce {
 
-constexpr int kLane = 16;              // elements of a row per thread
-constexpr int kLaneLong = 32;          // in the forward of rows too long for that
-// Most threads of a block, and of an SM: what the registers allow.
+// Elements of a row per thread (in the forward, where two rows at a time or one
+// fit the registers).
+constexpr int kFwdLane = 16, kFwdLaneLong = 32, kBwdLane = 16;
+constexpr int kBlock = 256;      // threads of a block, where a team is not larger
+// Most threads of a block, and of an SM: what registers and shared memory allow.
 template <typename T>
 constexpr int kFwdThreads = sizeof(T) == 2 ? 640 : 512;
-constexpr int kFwdBlock = 256;
-constexpr int kBwdThreads = 512;       // with the column sums in registers
-constexpr int kBwdBlock = 256;
-constexpr int kBwdThreadsWide = 1024;  // with the column sums in shared memory
+constexpr int kBwdThreads = 512;
+constexpr int kSmemMost = 224 * 1024;
 
 // How a row is spread: `team` threads to a row (a power of two up to a warp,
 // then whole warps), `teams` rows at a time in a block.
@@ -40,7 +42,7 @@ struct NormPlan {
   int64_t blocks;
 };
 
-static NormPlan norm_plan(int64_t N, int64_t D, int lane, int block, int sm_threads) {
+static NormPlan norm_plan(int64_t N, int64_t D, int lane, int sm_threads) {
   NormPlan p;
   const int64_t need = (D + lane - 1) / lane;
   if (need <= 32) {
@@ -50,8 +52,8 @@ static NormPlan norm_plan(int64_t N, int64_t D, int lane, int block, int sm_thre
     p.team = static_cast<int>((need + 31) / 32 * 32);
   }
   const int sms = sm_count();
-  // blocks of about `block` threads, smaller ones while there are SMs without a row
-  p.teams = std::max(1, block / p.team);
+  // blocks of about kBlock threads, smaller ones while there are SMs without a row
+  p.teams = std::max(1, kBlock / p.team);
   while (p.teams > 1 && p.teams * p.team > 32 && (N + p.teams - 1) / p.teams < sms) p.teams /= 2;
   const int64_t most =
       static_cast<int64_t>(sms) * std::max(1, sm_threads / std::max(64, p.team * p.teams));
@@ -59,49 +61,92 @@ static NormPlan norm_plan(int64_t N, int64_t D, int lane, int block, int sm_thre
   return p;
 }
 
-// Sums of a and of b over the team; every thread returns the same values.
-// `red`: one float2 per warp of the team (an even number of places), free again
-// after the next call with another.
-__device__ __forceinline__ void team_sum(float& a, float& b, int team, int id, float2* red) {
-  if (team < 32) {
-    for (int o = team / 2; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    return;
-  }
-  // the lower half of the warp adds up a, the upper half b
-  const int lane = threadIdx.x & 31;
-  const bool upper = lane >= 16;
-  float s = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+// The threads that hold a row, and this thread's place among them.
+struct Team {
+  int size, id, l;     // threads; which team of the block; which thread of it
+  int mine;            // how many of the thread's vectors begin within the row
+  bool first, last;    // no left, no right neighbour within the warp
+  float2* red[2];      // a pair of sums for each warp, places to a multiple of eight
+  int warp;
+  __device__ __forceinline__ Team(int size, int nvec, float2* pairs, int kind)
+      : size(size), id(threadIdx.x / size), l(threadIdx.x - id * size) {
+    mine = (nvec - l + size - 1) / size;
+    first = l == 0 || (threadIdx.x & 31) == 0;
+    last = l == size - 1 || (threadIdx.x & 31) == 31;
+    warp = l >> 5;
+    const int warps = size >> 5, places = (warps + 7) / 8 * 8;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (team == 32) {
-    const float other = __shfl_xor_sync(0xffffffffu, s, 16);
-    a = upper ? other : s;
-    b = upper ? s : other;
-    return;
+    for (int q = 0; q < 2; ++q) {
+      red[q] = pairs + q * kind + (size > 32 ? id * places : 0);
+      if (size > 32)
+        for (int w = warps + l; w < places; w += size) red[q][w] = make_float2(0.0f, 0.0f);
+    }
   }
-  const int warps = team >> 5, warp = (threadIdx.x - id * team) >> 5;
-  if ((lane & 15) == 0) reinterpret_cast<float*>(red)[2 * warp + (upper ? 1 : 0)] = s;
-  named_barrier(1 + id, team);
-  float2 t = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-  for (int w = 0; w < warps; w += 2) {
-    const float4 v = *reinterpret_cast<const float4*>(red + w);
-    t = __fadd2_rn(t, make_float2(v.x, v.y));
-    if (w + 1 < warps) t = __fadd2_rn(t, make_float2(v.z, v.w));
+  // Vector k of the thread is vector at(k) of the row: the team's vectors of one k
+  // lie next to each other (against runs of vectors per warp: 215 and 291 us for
+  // the layer norm of 65536 x 5120 bf16).
+  __device__ __forceinline__ int at(int k) const { return k * size + l; }
+
+  // Sums of a and of b over the team; every thread returns the same.  Two calls
+  // in a row use different q.
+  __device__ __forceinline__ void sum(float& a, float& b, int q) const {
+    if (size < 32) {
+      for (int o = size / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+      return;
+    }
+    // the lower half of the warp adds up a, the upper half b
+    const bool upper = (threadIdx.x & 16) != 0;
+    float s = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (size == 32) {
+      const float other = __shfl_xor_sync(0xffffffffu, s, 16);
+      a = upper ? other : s;
+      b = upper ? s : other;
+      return;
+    }
+    float2* r = red[q];
+    if ((threadIdx.x & 15) == 0) reinterpret_cast<float*>(r + warp)[upper ? 1 : 0] = s;
+    named_barrier(1 + id, size);
+    float2 t = make_float2(0.0f, 0.0f);
+    for (int w = 0; w < size; w += 256, r += 8) {
+#pragma unroll
+      for (int k = 0; k < 8; k += 2) {
+        const float4 v = *reinterpret_cast<const float4*>(r + k);
+        t = __fadd2_rn(t, make_float2(v.x, v.y));
+        t = __fadd2_rn(t, make_float2(v.z, v.w));
+      }
+    }
+    a = t.x;
+    b = t.y;
   }
-  a = t.x;
-  b = t.y;
+};
+
+// Places of all teams of a block: teams of two warps or more take eight each.
+template <int kThreads>
+constexpr int kRedPlaces = kThreads / 64 * 8 + 8;
+
+// How many of the rows first, first + step, ... there are.
+__device__ __forceinline__ int rows_from(int64_t first, int64_t step, int64_t N) {
+  return static_cast<int>(max(int64_t(0), N - first + step - 1) / step);
 }
 
-// Vectors of a thread: vector k of thread l of a team is k * team + l, so that
-// the team's loads of one k lie next to each other (against runs of vectors per
-// warp: 215 and 291 us for the layer norm of 65536 x 5120 bf16).
-struct Spread {
-  int team, l;
-  __device__ __forceinline__ int at(int k) const { return k * team + l; }
+// A row pointer that a thread moves on by a fixed step.  Whole rows: at the
+// thread's first vector, others: at the row.  The step is kept in registers (it
+// would be multiplied out again for every row).
+template <typename T, bool kWhole>
+struct RowPtr {
+  char* p;
+  int64_t step;
+  __device__ __forceinline__ RowPtr(const void* base, int64_t row, int64_t ld, int64_t rows, int l)
+      : p(static_cast<char*>(const_cast<void*>(base)) +
+          row * ld * static_cast<int64_t>(sizeof(T)) + (kWhole ? 16 * l : 0)),
+        step(rows * ld * static_cast<int64_t>(sizeof(T))) {
+    asm volatile("" : "+l"(step));
+  }
 };
 
 // Words [S, S + 5) of a pair of blocks, shifted right by r bits (0 or 16).
@@ -125,72 +170,120 @@ __device__ __forceinline__ uint4 bytes_from(const uint4& lo, const uint4& hi, in
   }
 }
 
-// kElems elements of a row.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// A thread's places for one row in shared memory: vector k at k * blockDim * 16;
+// kWhole = false: after them, for each thread without a right neighbour in its
+// warp, the blocks after its own.
 template <typename T, bool kWhole, int kElems>
-struct RowRegs {
+struct RowCopy {
   static constexpr int VEC = 16 / sizeof(T), NV = kElems / VEC;
-  uint4 v[NV];       // loaded blocks; after finish(): the row's vectors
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int k = 0; k < NV; ++k) v[k] = make_uint4(0, 0, 0, 0);
+  // threads of a block without a right neighbour in their warp
+  static __host__ __device__ __forceinline__ int ends(int threads, int team) {
+    return threads / (team < 32 ? team : 32);
   }
-  // starts the loads of a row
-  __device__ __forceinline__ void load(const T* p, int D, const Spread& s) {
-    const char* base = reinterpret_cast<const char*>(p);
-    if (!kWhole) base -= reinterpret_cast<uintptr_t>(p) & 15;
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (s.at(k) * VEC < D) v[k] = reinterpret_cast<const uint4*>(base)[s.at(k)];
+  static __host__ __device__ __forceinline__ int bytes(int threads, int team) {
+    return NV * 16 * (threads + (kWhole ? 0 : ends(threads, team)));
   }
-  // the vectors themselves, zeros past the row's end
-  __device__ __forceinline__ void finish(const T* p, int D, const Spread& s) {
-    if (kWhole) return;
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
-    const uint4* base = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - off);
-    const int last = (off + D * static_cast<int>(sizeof(T)) - 1) / 16;  // the row's last block
+  char* own;
+  char* end;
+  int pitch, end_pitch;
+  __device__ __forceinline__ RowCopy(char* place, const Team& t)
+      : own(place + threadIdx.x * 16),
+        end(place + NV * blockDim.x * 16 + threadIdx.x / (t.size < 32 ? t.size : 32) * 16),
+        pitch(blockDim.x * 16),
+        end_pitch(ends(blockDim.x, t.size) * 16) {}
+  // starts the copies of the row at p (see RowPtr)
+  __device__ __forceinline__ void start(const char* p, int D, const Team& t) const {
+    const uint32_t to = smem_u32(own);
+    if (kWhole) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int left = D - s.at(k) * VEC;
-      if (off != 0 && left > 0) v[k] = bytes_from(v[k], base[min(s.at(k) + 1, last)], off);
-      if (left < VEC) {
-        uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      for (int k = 0; k < NV; ++k)
+        if (k < t.mine) copy16(to + k * pitch, p + k * t.size * 16);
+    } else {
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+      const int last = (off + D * static_cast<int>(sizeof(T)) - 1) / 16;  // the row's last block
+      const char* from = p - off + 16 * t.l;
+      const uint32_t to_end = smem_u32(end);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (sizeof(T) == 4) {
-            if (q >= left) w[q] = 0u;
-          } else {
-            if (2 * q >= left) w[q] = 0u;
-            if (2 * q + 1 >= left) w[q] &= 0xffffu;
-          }
-        }
-        v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int k = 0; k < NV; ++k) {
+        if (t.at(k) <= last) copy16(to + k * pitch, from + k * t.size * 16);
+        if (t.last && t.at(k) < last)
+          copy16(to_end + k * end_pitch, from + k * t.size * 16 + 16);
       }
     }
   }
-  // vector k as pairs (for the packed fp32 instructions)
-  __device__ __forceinline__ void unpack(int k, float2 (&x)[VEC / 2]) const {
-    float f[VEC];
-    Elem<T>::unpack(v[k], f);
+  // zeros in the place of a row, or where no row is copied to
+  __device__ __forceinline__ void clear(bool row, const Team& t) const {
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) x[e] = make_float2(f[2 * e], f[2 * e + 1]);
+    for (int k = 0; k < NV; ++k) {
+      if (row || (kWhole && k >= t.mine))
+        *reinterpret_cast<uint4*>(own + k * pitch) = make_uint4(0, 0, 0, 0);
+      if (!kWhole && row && t.last)
+        *reinterpret_cast<uint4*>(end + k * end_pitch) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  // the row's vectors as pairs (for the packed fp32 instructions), zeros past its end
+  __device__ __forceinline__ void read(const char* p, int D, const Team& t,
+                                       float2 (&x)[NV][VEC / 2]) const {
+    const int off = kWhole ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      // (whole rows: places past the row's end were cleared and are never written)
+      uint4 v = *reinterpret_cast<const uint4*>(own + k * pitch);
+      if (!kWhole) {
+        uint4 right;
+        right.x = __shfl_down_sync(0xffffffffu, v.x, 1);
+        right.y = __shfl_down_sync(0xffffffffu, v.y, 1);
+        right.z = __shfl_down_sync(0xffffffffu, v.z, 1);
+        right.w = __shfl_down_sync(0xffffffffu, v.w, 1);
+        if (t.last) right = *reinterpret_cast<const uint4*>(end + k * end_pitch);
+        v = bytes_from(v, right, off);
+        const int left = D - t.at(k) * VEC;
+        if (left < VEC) {
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (sizeof(T) == 4) {
+              if (q >= left) w[q] = 0u;
+            } else {
+              if (2 * q >= left) w[q] = 0u;
+              if (2 * q + 1 >= left) w[q] &= 0xffffu;
+            }
+          }
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      float f[VEC];
+      Elem<T>::unpack(v, f);
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) x[k][e] = make_float2(f[2 * e], f[2 * e + 1]);
+    }
   }
 };
 
-// Writes the vector at columns j.. of a row (one per lane, all lanes of the warp
-// take part).  A row inside a block: each lane writes the block that begins with
-// its left neighbour's last elements, where the warp holds that neighbour and the
-// row fills the block; what no such block covers goes element by element.
+// Writes the vector k of a row (one per lane, all lanes of the warp take part).  A
+// row inside a block: each lane writes the block that begins with its left
+// neighbour's last elements, where the warp holds that neighbour and the row
+// fills the block; what no such block covers goes element by element.
 template <typename T, bool kWhole>
-__device__ __forceinline__ void store_vector(T* row, int k, int D, const Spread& s,
+__device__ __forceinline__ void store_vector(char* p, int k, bool in_row, int D, const Team& t,
                                              const float2 (&pairs)[8 / sizeof(T)]) {
   constexpr int VEC = 16 / sizeof(T);
-  const int j = s.at(k) * VEC;
   float x[VEC];
 #pragma unroll
   for (int e = 0; e < VEC / 2; ++e) x[2 * e] = pairs[e].x, x[2 * e + 1] = pairs[e].y;
   const uint4 own = Elem<T>::pack(x);
   if (kWhole) {
-    if (j < D) *reinterpret_cast<uint4*>(row + j) = own;
+    if (in_row && k < t.mine) *reinterpret_cast<uint4*>(p + k * t.size * 16) = own;
     return;
   }
   uint4 left_of;
@@ -198,14 +291,14 @@ __device__ __forceinline__ void store_vector(T* row, int k, int D, const Spread&
   left_of.y = __shfl_up_sync(0xffffffffu, own.y, 1);
   left_of.z = __shfl_up_sync(0xffffffffu, own.z, 1);
   left_of.w = __shfl_up_sync(0xffffffffu, own.w, 1);
-  const int left = D - j;  // elements of this vector (VEC or fewer, none when <= 0)
+  T* row = reinterpret_cast<T*>(p);
+  const int j = t.at(k) * VEC;
+  const int left = in_row ? D - j : 0;  // elements of this vector (VEC or fewer)
   if (left <= 0) return;
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
   const int o = off / static_cast<int>(sizeof(T));
-  const int lane = threadIdx.x & 31;
-  const bool begins = lane == 0 || s.l == 0, ends = lane == 31 || s.l == s.team - 1;
-  const bool head = (o == 0 || !begins) && left >= VEC - o;
-  const bool tail = !ends && left >= 2 * VEC - o;  // in the right neighbour's block
+  const bool head = (o == 0 || !t.first) && left >= VEC - o;
+  const bool tail = !t.last && left >= 2 * VEC - o;  // in the right neighbour's block
   if (head)
     *reinterpret_cast<uint4*>(reinterpret_cast<char*>(row + j) - off) =
         bytes_from(left_of, own, 16 - off);
@@ -282,55 +375,53 @@ struct NormArgs {
   int team, teams;
 };
 
-// A team works on kRows rows at a time (two, where threads of kLane elements can
-// hold a row): one read of the weights and one exchange between its warps serve
+// A team works on kRows rows at a time (two, where threads of kFwdLane
+// elements can hold a row): one read of the weights and one exchange between its warps serve
 // both.
 template <typename T, bool kWhole, bool kCenter, int kElems, int kRows>
 __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
-  extern __shared__ float4 weights[];  // weight, then bias
-  __shared__ __align__(16) float2 red_all[2][kFwdThreads<T> / 32 + 2];
-  using Row = RowRegs<T, kWhole, kElems>;
-  constexpr int VEC = Row::VEC, NV = Row::NV, P = VEC / 2;
-  const int team = a.team, id = threadIdx.x / team, l = threadIdx.x - id * team;
-  // an even number of places for each team
-  float2* red0 = red_all[0] + (team > 32 ? id * ((team + 32) / 64 * 2) : 0);
-  float2* red1 = red_all[1] + (team > 32 ? id * ((team + 32) / 64 * 2) : 0);
-  // teams of one warp go on together
-  const int lead = team < 32 ? (threadIdx.x & ~31) / team : id;
-  const int64_t all = static_cast<int64_t>(gridDim.x) * a.teams;
-  int64_t first = static_cast<int64_t>(blockIdx.x) * a.teams + lead;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + id;  // and row + all
+  extern __shared__ float4 weights[];  // weight, then bias, then the rows' copies
+  constexpr int kPlaces = kRedPlaces<kFwdThreads<T>>;
+  __shared__ __align__(16) float2 red[2 * kPlaces];
+  using Copy = RowCopy<T, kWhole, kElems>;
+  constexpr int VEC = Copy::VEC, NV = Copy::NV, P = VEC / 2;
   const int D = static_cast<int>(a.D);
-  const Spread spread{team, l};
-  const T* x = static_cast<const T*>(a.x);
-  T* y = static_cast<T*>(a.y);
-  Row next[kRows];
+  const int nvec = (D + VEC - 1) / VEC;
+  const Team team(a.team, nvec, red, kPlaces);
+  const int64_t all = static_cast<int64_t>(gridDim.x) * a.teams;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + team.id;  // then row + all, ...
+  int rows = rows_from(row, all, a.N);  // of this team, and of the warp's first one
+  int turns = a.team < 32 ? __shfl_sync(0xffffffffu, rows, 0) : rows;
+  RowPtr<T, kWhole> x(a.x, row, a.ldx, all, team.l), y(a.y, row, a.ldy, all, team.l);
+  float* mean_out = a.mean != nullptr ? a.mean + row : nullptr;
+  float* rstd_out = a.rstd != nullptr ? a.rstd + row : nullptr;
+  char* places = reinterpret_cast<char*>(weights + (kCenter ? 2 : 1) * nvec * (VEC / 4));
+  const int row_bytes = Copy::bytes(blockDim.x, a.team);
+  const Copy copy[2] = {Copy(places, team), Copy(places + (kRows - 1) * row_bytes, team)};
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
-    next[r].clear();
-    if (row + r * all < a.N) next[r].load(x + (row + r * all) * a.ldx, D, spread);
+    copy[r].clear(false, team);
+    if (r < rows) copy[r].start(x.p + r * x.step, D, team);
   }
-  const int nvec = (D + VEC - 1) / VEC;
+  copies_commit();
   const float4* bias = weights + nvec * (VEC / 4);
   stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
   if (kCenter) stage_weights<VEC>(weights + nvec * (VEC / 4), a.bias, a.w_f32, 0.0f, D);
   bool staged = false;  // the block's weights are there: needed late in the first row
   const float inv_n = 1.0f / static_cast<float>(D);
-  for (; first < a.N; first += kRows * all) {
+  for (; turns > 0; turns -= kRows, rows -= kRows) {
     float2 f[kRows][NV][P];
+    copies_wait();
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      if (row + r * all < a.N) next[r].finish(x + (row + r * all) * a.ldx, D, spread);
-#pragma unroll
-      for (int k = 0; k < NV; ++k) next[r].unpack(k, f[r][k]);
-    }
-    const int64_t here = row;
-    row += kRows * all;
+    for (int r = 0; r < kRows; ++r) copy[r].read(x.p + r * x.step, D, team, f[r]);
+    x.p += kRows * x.step;
+    __syncwarp();
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-      if (row + r * all < a.N) next[r].load(x + (row + r * all) * a.ldx, D, spread);
+      if (kRows + r < rows) copy[r].start(x.p + r * x.step, D, team);
+    copies_commit();
     // sums: a chain of additions for each place in a vector
-    float mean[kRows] = {};
+    float mean[2] = {};
     if (kCenter) {
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
@@ -343,12 +434,11 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
           for (int e = 0; e < P; ++e) s[e] = __fadd2_rn(s[e], f[r][k][e]);
         mean[r] = sum_pairs(s);
       }
-      float none = 0.0f;
-      team_sum(mean[0], kRows > 1 ? mean[kRows - 1] : none, team, id, red0);
+      team.sum(mean[0], mean[1], 0);
 #pragma unroll
       for (int r = 0; r < kRows; ++r) mean[r] = __fmul_rn(mean[r], inv_n);
     }
-    float rstd[kRows];
+    float rstd[2] = {};
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       float2 q[P];
@@ -356,7 +446,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
       for (int e = 0; e < P; ++e) q[e] = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int j = spread.at(k) * VEC;
+        const int j = team.at(k) * VEC;
 #pragma unroll
         for (int e = 0; e < P; ++e) {
           if (kCenter) f[r][k][e] = __fadd2_rn(f[r][k][e], both(-mean[r]));
@@ -366,49 +456,47 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
             if (j + 2 * e >= D) d.x = 0.0f;
             if (j + 2 * e + 1 >= D) d.y = 0.0f;
           }
-          if (!kWhole || j < D) q[e] = __ffma2_rn(d, d, q[e]);
+          if (!kWhole || k < team.mine) q[e] = __ffma2_rn(d, d, q[e]);
         }
       }
       rstd[r] = sum_pairs(q);
     }
-    float none = 0.0f;
-    team_sum(rstd[0], kRows > 1 ? rstd[kRows - 1] : none, team, id, red1);
+    team.sum(rstd[0], rstd[1], 1);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) rstd[r] = rsqrtf(__fmaf_rn(rstd[r], inv_n, a.eps));
     if (!staged) __syncthreads();
     staged = true;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (spread.at(k) * VEC < D) {
-        float2 w[P], b[P];
-        weight_vec<VEC>(weights, nvec, spread.at(k), w);
-        if (kCenter) weight_vec<VEC>(bias, nvec, spread.at(k), b);
+      float2 w[P], b[P];
+      const int i = min(team.at(k), nvec - 1);  // past the row's end: not written
+      weight_vec<VEC>(weights, nvec, i, w);
+      if (kCenter) weight_vec<VEC>(bias, nvec, i, b);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
+      for (int r = 0; r < kRows; ++r)
 #pragma unroll
-          for (int e = 0; e < P; ++e) {
-            const float2 h = __fmul2_rn(f[r][k][e], both(rstd[r]));
-            f[r][k][e] = kCenter ? __ffma2_rn(h, w[e], b[e]) : __fmul2_rn(h, w[e]);
-          }
-      }
+        for (int e = 0; e < P; ++e) {
+          const float2 h = __fmul2_rn(f[r][k][e], both(rstd[r]));
+          f[r][k][e] = kCenter ? __ffma2_rn(h, w[e], b[e]) : __fmul2_rn(h, w[e]);
+        }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        store_vector<T, kWhole>(y.p + r * y.step, k, r < rows, D, team, f[r][k]);
+    }
+    y.p += kRows * y.step;
+    if (team.l == 0) {
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        const bool in_row = here + r * all < a.N;
-        store_vector<T, kWhole>(y + (in_row ? here + r * all : 0) * a.ldy, k, in_row ? D : 0,
-                                spread, f[r][k]);
+        if (kCenter && r < rows && mean_out != nullptr) mean_out[r * all] = mean[r];
+        if (r < rows && rstd_out != nullptr) rstd_out[r * all] = rstd[r];
       }
+      if (kCenter && mean_out != nullptr) mean_out += kRows * all;
+      if (rstd_out != nullptr) rstd_out += kRows * all;
     }
-    if (l == 0) {
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (here + r * all >= a.N) continue;
-        if (kCenter && a.mean != nullptr) a.mean[here + r * all] = mean[r];
-        if (a.rstd != nullptr) a.rstd[here + r * all] = rstd[r];
-      }
-    }
-    if (!kCenter && team > 32) named_barrier(1 + id, team);  // red1 is free again
+    if (!kCenter && a.team > 32) named_barrier(1 + team.id, a.team);  // the sums' places
   }
   if (!staged) __syncthreads();  // warps without a row
+  copies_wait();
 }
 
 struct NormBwdArgs {
@@ -430,102 +518,92 @@ struct NormBwdArgs {
   int team, teams;
 };
 
-// kWide: the column sums in shared memory, one row at a time in a block.
-template <typename T, bool kWhole, bool kCenter, bool kWide>
-__global__ void __launch_bounds__(kWide ? kBwdThreadsWide : kBwdThreads)
-    norm_bwd_kernel(NormBwdArgs a) {
-  // weight; column sums: teams * D (kWide: D) for grad_weight, as many for grad_bias
+template <typename T, bool kWhole, bool kCenter>
+__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a) {
+  // weight; the rows' copies (at the end: the teams' column sums)
   extern __shared__ float4 weights[];
-  __shared__ __align__(16) float2 red_all[2][kBwdThreadsWide / 32 + 2];
-  using Row = RowRegs<T, kWhole, kLane>;
-  constexpr int VEC = Row::VEC, NV = Row::NV, P = VEC / 2;
-  const int team = a.team, id = threadIdx.x / team, l = threadIdx.x - id * team;
-  const int lead = team < 32 ? (threadIdx.x & ~31) / team : id;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * a.teams;
-  int64_t first = static_cast<int64_t>(blockIdx.x) * a.teams + lead;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + id;
+  constexpr int kPlaces = kRedPlaces<kBwdThreads>;
+  __shared__ __align__(16) float2 red[2 * kPlaces];
+  using Copy = RowCopy<T, kWhole, kBwdLane>;
+  constexpr int VEC = Copy::VEC, NV = Copy::NV, P = VEC / 2;
   const int D = static_cast<int>(a.D);
-  const T* xr = static_cast<const T*>(a.x) + (row < a.N ? row : 0) * a.ldx;
-  const T* gr = static_cast<const T*>(a.dy) + (row < a.N ? row : 0) * a.lddy;
-  const Spread spread{team, l};
-  T* dxr = static_cast<T*>(a.dx) + (row < a.N ? row : 0) * a.lddx;
   const int nvec = (D + VEC - 1) / VEC;
-  float* sums = reinterpret_cast<float*>(weights + nvec * (VEC / 4));
-  Row nx, ng;
-  float nmean = 0.0f, nrstd = 0.0f;
-  nx.clear();
-  ng.clear();
-  auto prefetch = [&]() {
-    if (row >= a.N) return;
-    nx.load(xr, D, spread);
-    ng.load(gr, D, spread);
-    nrstd = a.rstd[row];
-    if (kCenter) nmean = a.mean[row];
-  };
-  if (!kWide) prefetch();
+  const Team team(a.team, nvec, red, kPlaces);
+  const int64_t all = static_cast<int64_t>(gridDim.x) * a.teams;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + team.id;  // then row + all, ...
+  int rows = rows_from(row, all, a.N);  // of this team, and of the warp's first one
+  int turns = a.team < 32 ? __shfl_sync(0xffffffffu, rows, 0) : rows;
+  RowPtr<T, kWhole> x(a.x, row, a.ldx, all, team.l), dy(a.dy, row, a.lddy, all, team.l);
+  RowPtr<T, kWhole> dx(a.dx, row, a.lddx, all, team.l);
+  char* places = reinterpret_cast<char*>(weights + nvec * (VEC / 4));
+  const Copy cx(places, team);
+  const Copy cg(places + Copy::bytes(blockDim.x, a.team), team);
+  cx.clear(rows <= 0, team);
+  cg.clear(rows <= 0, team);
+  if (rows > 0) {
+    cx.start(x.p, D, team);
+    cg.start(dy.p, D, team);
+  }
+  copies_commit();
+  const float* mean_in = kCenter ? a.mean + row : nullptr;
+  const float* rstd_in = a.rstd + row;
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  if (rows > 0) {
+    next_rstd = *rstd_in;
+    if (kCenter) next_mean = *mean_in;
+  }
   stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
   float2 dw[NV][P] = {}, db[NV][P] = {};
-  if (kWide) {
-    for (int j = threadIdx.x; j < (kCenter ? 2 : 1) * nvec * VEC; j += blockDim.x) sums[j] = 0.0f;
-  }
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(D);
   int parity = 0;
-  for (; first < a.N; first += step) {
-    if (kWide) prefetch();  // no registers for a second row
-    const bool in_row = row < a.N;
-    const float mean = nmean, rstd = nrstd;
-    if (in_row) {
-      nx.finish(xr, D, spread);
-      ng.finish(gr, D, spread);
-    } else {
-      ng.clear();  // adds nothing to the column sums
-    }
+  for (; turns > 0; --turns, --rows) {
+    const float mean = next_mean, rstd = next_rstd;
     float2 h[NV][P], u[NV][P];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      nx.unpack(k, h[k]);
-      ng.unpack(k, u[k]);
+    copies_wait();
+    cx.read(x.p, D, team, h);
+    cg.read(dy.p, D, team, u);
+    x.p += x.step;
+    dy.p += dy.step;
+    __syncwarp();
+    if (rows > 1) {
+      rstd_in += all;
+      next_rstd = *rstd_in;
+      if (kCenter) {
+        mean_in += all;
+        next_mean = *mean_in;
+      }
+      cx.start(x.p, D, team);
+      cg.start(dy.p, D, team);
+    } else {
+      // a warp whose other teams go on: a row of zeros adds nothing
+      cx.clear(true, team);
+      cg.clear(true, team);
+      next_rstd = next_mean = 0.0f;
     }
-    row += step;
-    if (row < a.N) xr += step * a.ldx, gr += step * a.lddy;
-    if (!kWide) prefetch();
+    copies_commit();
     float2 s1[P], s2[P];  // a chain of additions for each place in a vector
 #pragma unroll
-    for (int e = 0; e < P; ++e) s1[e] = s2[e] = make_float2(0.0f, 0.0f);
+    for (int e = 0; e < P; ++e) s1[e] = s2[e] = both(0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int j = spread.at(k) * VEC;
-      if (j >= D) continue;
+      // past the row's end the incoming gradient is 0, and so are all sums
       float2 w[P];
-      weight_vec<VEC>(weights, nvec, spread.at(k), w);
+      weight_vec<VEC>(weights, nvec, min(team.at(k), nvec - 1), w);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        // past the row's end the incoming gradient is 0, and so are all sums
         if (kCenter) h[k][e] = __fadd2_rn(h[k][e], both(-mean));
         h[k][e] = __fmul2_rn(h[k][e], both(rstd));
         const float2 g = u[k][e];
         u[k][e] = __fmul2_rn(g, w[e]);
         if (kCenter) s1[e] = __fadd2_rn(s1[e], u[k][e]);
         s2[e] = __ffma2_rn(u[k][e], h[k][e], s2[e]);
-        if (kWide) {
-          // pairs of the vector's quarters, laid out as the weights
-          float2* to = reinterpret_cast<float2*>(sums + 4 * ((e / 2) * nvec + spread.at(k))) +
-                       (e & 1);
-          *to = __ffma2_rn(g, h[k][e], *to);
-          if (kCenter) {
-            to += 2 * nvec * (VEC / 4);
-            *to = __fadd2_rn(*to, g);
-          }
-        } else {
-          dw[k][e] = __ffma2_rn(g, h[k][e], dw[k][e]);
-          if (kCenter) db[k][e] = __fadd2_rn(db[k][e], g);
-        }
+        dw[k][e] = __ffma2_rn(g, h[k][e], dw[k][e]);
+        if (kCenter) db[k][e] = __fadd2_rn(db[k][e], g);
       }
     }
-    float c1 = sum_pairs(s1), c2 = sum_pairs(s2);
-    team_sum(c2, c1, team, id,
-             red_all[parity] + (team > 32 ? id * ((team + 32) / 64 * 2) : 0));
+    float c1 = kCenter ? sum_pairs(s1) : 0.0f, c2 = sum_pairs(s2);
+    team.sum(c2, c1, parity);
     parity ^= 1;
     if (a.dx == nullptr) continue;
     c1 = __fmul_rn(c1, inv_n);
@@ -539,38 +617,34 @@ __global__ void __launch_bounds__(kWide ? kBwdThreadsWide : kBwdThreads)
         t = __ffma2_rn(h[k][e], both(-c2), t);
         u[k][e] = __fmul2_rn(t, both(rstd));
       }
-      store_vector<T, kWhole>(dxr, k, in_row ? D : 0, spread, u[k]);
+      store_vector<T, kWhole>(dx.p, k, rows > 0, D, team, u[k]);
     }
-    if (row < a.N) dxr += step * a.lddx;
+    dx.p += dx.step;
   }
+  copies_wait();
   if (a.part == nullptr) return;
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
-  if (!kWide) {
-    // the teams' sums side by side, then in team order
-    float* to = a.teams == 1 ? part : sums + id * D;
-    const int64_t bias_at = static_cast<int64_t>(a.teams) * D;
+  // the teams' sums side by side, then in team order
+  float* sums = reinterpret_cast<float*>(places);
+  float* to = a.teams == 1 ? part : sums + team.id * D;
+  const int64_t bias_at = static_cast<int64_t>(a.teams) * D;
+  __syncthreads();  // the copies are no longer needed
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int j = spread.at(k) * VEC;
+  for (int k = 0; k < NV; ++k) {
+    const int j = team.at(k) * VEC;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (j + e >= D) continue;
-        to[j + e] = (e & 1) ? dw[k][e / 2].y : dw[k][e / 2].x;
-        if (kCenter) to[bias_at + j + e] = (e & 1) ? db[k][e / 2].y : db[k][e / 2].x;
-      }
+    for (int e = 0; e < VEC; ++e) {
+      if (j + e >= D) continue;
+      to[j + e] = (e & 1) ? dw[k][e / 2].y : dw[k][e / 2].x;
+      if (kCenter) to[bias_at + j + e] = (e & 1) ? db[k][e / 2].y : db[k][e / 2].x;
     }
-    if (a.teams == 1) return;
   }
+  if (a.teams == 1) return;
   __syncthreads();
-  for (int64_t j = threadIdx.x; j < (kCenter ? 2 : 1) * a.D; j += blockDim.x) {
-    const int64_t which = j / a.D, c = j - which * a.D;
+  for (int j = threadIdx.x; j < (kCenter ? 2 : 1) * D; j += blockDim.x) {
+    const int which = j / D, c = j - which * D;
     float s = 0.0f;
-    if (kWide) {
-      const int i = static_cast<int>(c) / VEC, e = static_cast<int>(c) % VEC;
-      s = sums[4 * (which * nvec * (VEC / 4) + (e / 4) * nvec + i) + e % 4];
-    } else {
-      for (int t = 0; t < a.teams; ++t) s += sums[(which * a.teams + t) * a.D + c];
-    }
+    for (int t = 0; t < a.teams; ++t) s += sums[(which * a.teams + t) * D + c];
     part[j] = s;
   }
 }
@@ -705,8 +779,6 @@ static bool whole(int dt, const void* p, int64_t ld) {
 // A weight vector in shared memory, to whole row vectors.
 static size_t weight_bytes(int64_t D) { return round_up(static_cast<size_t>(D), 8) * 4; }
 
-constexpr int kSmemMost = 224 * 1024;
-
 // Allows a kernel kSmemMost bytes of shared memory, once per device.
 template <typename K>
 static int raise_smem(K kern, std::atomic<uint64_t>& raised) {
@@ -723,29 +795,34 @@ static int raise_smem(K kern, std::atomic<uint64_t>& raised) {
   return rc;
 }
 
+// Launches norm_fwd_kernel; returns 1 (nothing launched) when a row does not fit.
 template <typename T, bool kWhole, bool kCenter, int kElems, int kRows>
 static int launch_norm_fwd_k(NormArgs a, cudaStream_t s) {
+  if (a.D > int64_t(kFwdThreads<T>) * kElems) return 1;
   static std::atomic<uint64_t> raised{0};
   const int rc = raise_smem(norm_fwd_kernel<T, kWhole, kCenter, kElems, kRows>, raised);
   if (rc != FLCE_OK) return rc;
-  const NormPlan p = norm_plan(a.N, a.D, kElems, kFwdBlock, kFwdThreads<T>);
+  const NormPlan p = norm_plan(a.N, a.D, kElems, kFwdThreads<T>);
   a.team = p.team;
   a.teams = p.teams;
-  const size_t smem = weight_bytes(a.D) * (kCenter ? 2 : 1);
+  const int threads = p.team * p.teams;
+  const size_t smem = weight_bytes(a.D) * (kCenter ? 2 : 1) +
+                      kRows * RowCopy<T, kWhole, kElems>::bytes(threads, p.team);
+  if (smem > kSmemMost) return 1;
   norm_fwd_kernel<T, kWhole, kCenter, kElems, kRows>
-      <<<static_cast<unsigned>(p.blocks), p.team * p.teams, smem, s>>>(a);
+      <<<static_cast<unsigned>(p.blocks), threads, smem, s>>>(a);
   return launch_status("norm_fwd_kernel launch");
 }
 
 template <typename T, bool kCenter>
 static int launch_norm_fwd(NormArgs a, int dt, cudaStream_t s) {
   const bool w = whole(dt, a.x, a.ldx) && whole(dt, a.y, a.ldy) && whole(dt, nullptr, a.D);
-  if (a.D <= int64_t(kFwdThreads<T>) * kLane)
-    return w ? launch_norm_fwd_k<T, true, kCenter, kLane, 2>(a, s)
-             : launch_norm_fwd_k<T, false, kCenter, kLane, 2>(a, s);
-  if (a.D <= int64_t(kFwdThreads<T>) * kLaneLong)
-    return w ? launch_norm_fwd_k<T, true, kCenter, kLaneLong, 1>(a, s)
-             : launch_norm_fwd_k<T, false, kCenter, kLaneLong, 1>(a, s);
+  int rc = w ? launch_norm_fwd_k<T, true, kCenter, kFwdLane, 2>(a, s)
+             : launch_norm_fwd_k<T, false, kCenter, kFwdLane, 2>(a, s);
+  if (rc == 1)
+    rc = w ? launch_norm_fwd_k<T, true, kCenter, kFwdLaneLong, 1>(a, s)
+           : launch_norm_fwd_k<T, false, kCenter, kFwdLaneLong, 1>(a, s);
+  if (rc != 1) return rc;
   const int grid = static_cast<int>(std::min<int64_t>(a.N, sm_count() * 8));
   norm_fwd_long_kernel<T, kCenter><<<grid, kLongThreads, 0, s>>>(a);
   return launch_status("norm_fwd_long_kernel launch");
@@ -773,37 +850,27 @@ static int norm_fwd(NormArgs a, int dt, int wdt, flce_stream_t stream) {
                          : launch_norm_fwd<float, kCenter>(a, dt, s);
 }
 
-// Column sums in registers, in shared memory, or by kernels of their own.
-static bool bwd_narrow(int64_t D) { return D <= int64_t(kBwdThreads) * kLane; }
-static bool bwd_held(int64_t D) { return D <= int64_t(kBwdThreadsWide) * kLane; }
+// Whether norm_bwd_kernel can hold a row.
+static bool bwd_held(int64_t D) { return D <= int64_t(kBwdThreads) * kBwdLane; }
 
 static int64_t bwd_slices(int64_t N, int64_t D) {
-  if (bwd_held(D)) return norm_plan(N, D, kLane, kBwdBlock, kBwdThreads).blocks;
+  if (bwd_held(D)) return norm_plan(N, D, kBwdLane, kBwdThreads).blocks;
   return std::min<int64_t>(64, N);
 }
 
 template <typename T, bool kWhole, bool kCenter>
 static int launch_norm_bwd_held(NormBwdArgs a, cudaStream_t s) {
-  const NormPlan p = norm_plan(a.N, a.D, kLane, kBwdBlock, kBwdThreads);
+  static std::atomic<uint64_t> raised{0};
+  const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter>, raised);
+  if (rc != FLCE_OK) return rc;
+  const NormPlan p = norm_plan(a.N, a.D, kBwdLane, kBwdThreads);
   a.team = p.team;
   a.teams = p.teams;
-  const unsigned grid = static_cast<unsigned>(p.blocks);
   const int threads = p.team * p.teams;
-  const size_t per = static_cast<size_t>(a.D) * sizeof(float) * (kCenter ? 2 : 1);
-  const size_t w = weight_bytes(a.D);
-  if (bwd_narrow(a.D)) {
-    static std::atomic<uint64_t> raised{0};
-    const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, false>, raised);
-    if (rc != FLCE_OK) return rc;
-    const size_t smem = w + (p.teams > 1 ? p.teams * per : 0);
-    norm_bwd_kernel<T, kWhole, kCenter, false><<<grid, threads, smem, s>>>(a);
-  } else {
-    static std::atomic<uint64_t> raised{0};
-    const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, true>, raised);
-    if (rc != FLCE_OK) return rc;
-    norm_bwd_kernel<T, kWhole, kCenter, true>
-        <<<grid, threads, w * (kCenter ? 3 : 2), s>>>(a);
-  }
+  const size_t sums = p.teams > 1 ? 2 * p.teams * static_cast<size_t>(a.D) * sizeof(float) : 0;
+  const size_t copies = 2 * RowCopy<T, kWhole, kBwdLane>::bytes(threads, p.team);
+  norm_bwd_kernel<T, kWhole, kCenter><<<static_cast<unsigned>(p.blocks), threads,
+                                        weight_bytes(a.D) + std::max(sums, copies), s>>>(a);
   return launch_status("norm_bwd_kernel launch");
 }
 
