@@ -25,14 +25,15 @@
 
 namespace flce {
 
-// Elements of a row per thread (in the forward, where two rows at a time or one
-// fit the registers).
-constexpr int kFwdLane = 16, kFwdLaneLong = 32, kBwdLane = 16;
-constexpr int kBlock = 256;      // threads of a block, where a team is not larger
+// Elements of a row per thread in the forward, where two rows at a time or one
+// fit the registers.
+constexpr int kFwdLane = 16, kFwdLaneLong = 32;
+constexpr int kBlock = 512;      // threads of a block, where a team is not larger
 // Most threads of a block, and of an SM: what registers and shared memory allow.
 template <typename T>
 constexpr int kFwdThreads = sizeof(T) == 2 ? 640 : 512;
-constexpr int kBwdThreads = 512;
+template <int kElems>
+constexpr int kBwdThreads = kElems == 8 ? 640 : 512;
 constexpr int kSmemMost = 224 * 1024;
 
 // How a row is spread: `team` threads to a row (a power of two up to a warp,
@@ -176,8 +177,9 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
+template <int N>
 __device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A thread's places for one row in shared memory: vector k at k * blockDim * 16;
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
   const float inv_n = 1.0f / static_cast<float>(D);
   for (; turns > 0; turns -= kRows, rows -= kRows) {
     float2 f[kRows][NV][P];
-    copies_wait();
+    copies_wait<0>();
 #pragma unroll
     for (int r = 0; r < kRows; ++r) copy[r].read(x.p + r * x.step, D, team, f[r]);
     x.p += kRows * x.step;
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
     if (!kCenter && a.team > 32) named_barrier(1 + team.id, a.team);  // the sums' places
   }
   if (!staged) __syncthreads();  // warps without a row
-  copies_wait();
+  copies_wait<0>();
 }
 
 struct NormBwdArgs {
@@ -518,13 +520,14 @@ struct NormBwdArgs {
   int team, teams;
 };
 
-template <typename T, bool kWhole, bool kCenter>
-__global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a) {
+// kAhead: rows copied ahead.
+template <typename T, bool kWhole, bool kCenter, int kElems, int kAhead>
+__global__ void __launch_bounds__(kBwdThreads<kElems>) norm_bwd_kernel(NormBwdArgs a) {
   // weight; the rows' copies (at the end: the teams' column sums)
   extern __shared__ float4 weights[];
-  constexpr int kPlaces = kRedPlaces<kBwdThreads>;
+  constexpr int kPlaces = kRedPlaces<kBwdThreads<kElems>>;
   __shared__ __align__(16) float2 red[2 * kPlaces];
-  using Copy = RowCopy<T, kWhole, kBwdLane>;
+  using Copy = RowCopy<T, kWhole, kElems>;
   constexpr int VEC = Copy::VEC, NV = Copy::NV, P = VEC / 2;
   const int D = static_cast<int>(a.D);
   const int nvec = (D + VEC - 1) / VEC;
@@ -536,52 +539,55 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a) {
   RowPtr<T, kWhole> x(a.x, row, a.ldx, all, team.l), dy(a.dy, row, a.lddy, all, team.l);
   RowPtr<T, kWhole> dx(a.dx, row, a.lddx, all, team.l);
   char* places = reinterpret_cast<char*>(weights + nvec * (VEC / 4));
-  const Copy cx(places, team);
-  const Copy cg(places + Copy::bytes(blockDim.x, a.team), team);
-  cx.clear(rows <= 0, team);
-  cg.clear(rows <= 0, team);
-  if (rows > 0) {
-    cx.start(x.p, D, team);
-    cg.start(dy.p, D, team);
-  }
-  copies_commit();
+  const int row_bytes = Copy::bytes(blockDim.x, a.team);
   const float* mean_in = kCenter ? a.mean + row : nullptr;
   const float* rstd_in = a.rstd + row;
-  float next_mean = 0.0f, next_rstd = 0.0f;
-  if (rows > 0) {
-    next_rstd = *rstd_in;
-    if (kCenter) next_mean = *mean_in;
+  // rows in even and odd turns, each in places of its own
+  struct Ahead {
+    Copy x, g;
+    float mean, rstd;
+  };
+  Ahead even{Copy(places, team), Copy(places + row_bytes, team), 0.0f, 0.0f};
+  Ahead odd{Copy(places + 2 * (kAhead - 1) * row_bytes, team),
+            Copy(places + (2 * kAhead - 1) * row_bytes, team), 0.0f, 0.0f};
+  auto fetch = [&](Ahead& f, int ahead) {  // the row `ahead` of x.p
+    if (ahead < rows) {
+      f.x.start(x.p + ahead * x.step, D, team);
+      f.g.start(dy.p + ahead * dy.step, D, team);
+      f.rstd = rstd_in[ahead * all];
+      if (kCenter) f.mean = mean_in[ahead * all];
+    } else {
+      // a warp whose other teams go on: a row of zeros adds nothing
+      f.x.clear(true, team);
+      f.g.clear(true, team);
+      f.rstd = f.mean = 0.0f;
+    }
+    copies_commit();
+  };
+  even.x.clear(false, team);
+  even.g.clear(false, team);
+  fetch(even, 0);
+  if (kAhead == 2) {
+    odd.x.clear(false, team);
+    odd.g.clear(false, team);
+    fetch(odd, 1);
   }
   stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
   float2 dw[NV][P] = {}, db[NV][P] = {};
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(D);
-  int parity = 0;
-  for (; turns > 0; --turns, --rows) {
-    const float mean = next_mean, rstd = next_rstd;
+  auto turn = [&](Ahead& f, int parity) {
+    const float mean = f.mean, rstd = f.rstd;
     float2 h[NV][P], u[NV][P];
-    copies_wait();
-    cx.read(x.p, D, team, h);
-    cg.read(dy.p, D, team, u);
+    copies_wait<kAhead - 1>();
+    f.x.read(x.p, D, team, h);
+    f.g.read(dy.p, D, team, u);
+    __syncwarp();
+    fetch(f, kAhead);
     x.p += x.step;
     dy.p += dy.step;
-    __syncwarp();
-    if (rows > 1) {
-      rstd_in += all;
-      next_rstd = *rstd_in;
-      if (kCenter) {
-        mean_in += all;
-        next_mean = *mean_in;
-      }
-      cx.start(x.p, D, team);
-      cg.start(dy.p, D, team);
-    } else {
-      // a warp whose other teams go on: a row of zeros adds nothing
-      cx.clear(true, team);
-      cg.clear(true, team);
-      next_rstd = next_mean = 0.0f;
-    }
-    copies_commit();
+    rstd_in += all;
+    if (kCenter) mean_in += all;
     float2 s1[P], s2[P];  // a chain of additions for each place in a vector
 #pragma unroll
     for (int e = 0; e < P; ++e) s1[e] = s2[e] = both(0.0f);
@@ -604,8 +610,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a) {
     }
     float c1 = kCenter ? sum_pairs(s1) : 0.0f, c2 = sum_pairs(s2);
     team.sum(c2, c1, parity);
-    parity ^= 1;
-    if (a.dx == nullptr) continue;
+    if (a.dx == nullptr) return;
     c1 = __fmul_rn(c1, inv_n);
     c2 = __fmul_rn(c2, inv_n);
 #pragma unroll
@@ -620,8 +625,18 @@ __global__ void __launch_bounds__(kBwdThreads) norm_bwd_kernel(NormBwdArgs a) {
       store_vector<T, kWhole>(dx.p, k, rows > 0, D, team, u[k]);
     }
     dx.p += dx.step;
+  };
+  if (kAhead == 2) {
+    for (; turns > 0; turns -= 2) {
+      turn(even, 0);
+      --rows;
+      if (turns > 1) turn(odd, 1);
+      --rows;
+    }
+  } else {
+    for (; turns > 0; --turns, --rows) turn(even, turns & 1);
   }
-  copies_wait();
+  copies_wait<0>();
   if (a.part == nullptr) return;
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
   // the teams' sums side by side, then in team order
@@ -850,39 +865,67 @@ static int norm_fwd(NormArgs a, int dt, int wdt, flce_stream_t stream) {
                          : launch_norm_fwd<float, kCenter>(a, dt, s);
 }
 
-// Whether norm_bwd_kernel can hold a row.
-static bool bwd_held(int64_t D) { return D <= int64_t(kBwdThreads) * kBwdLane; }
-
-static int64_t bwd_slices(int64_t N, int64_t D) {
-  if (bwd_held(D)) return norm_plan(N, D, kBwdLane, kBwdThreads).blocks;
-  return std::min<int64_t>(64, N);
+// Elements per thread in norm_bwd_kernel (0: rows too long for it).  Eight where
+// only one team of sixteen fits an SM (layer norm 65536 x 5120 bf16: 412 against
+// 511 us), and for fp32, whose rows copied ahead take the registers (RMS norm
+// 8192 x 4096: 65 against 77 us); else sixteen (bf16: 39 against 48 us).  The same
+// for all strides and alignments: the order of the sums depends on it.
+static int bwd_elems(int64_t D, bool f32) {
+  if (D > int64_t(kBwdThreads<16>) * 16) return 0;
+  const bool fits8 = D <= int64_t(kBwdThreads<8>) * 8;
+  return fits8 && (f32 || D > int64_t(kBwdThreads<16>) / 2 * 16) ? 8 : 16;
 }
 
-template <typename T, bool kWhole, bool kCenter>
-static int launch_norm_bwd_held(NormBwdArgs a, cudaStream_t s) {
+static NormPlan bwd_plan(int64_t N, int64_t D, int elems) {
+  return norm_plan(N, D, elems, elems == 8 ? kBwdThreads<8> : kBwdThreads<16>);
+}
+
+// Most partial sums: the workspace does not depend on the type.
+static int64_t bwd_slices(int64_t N, int64_t D) {
+  int64_t n = std::min<int64_t>(64, N);
+  if (bwd_elems(D, false) > 0) n = std::max(n, bwd_plan(N, D, bwd_elems(D, false)).blocks);
+  if (bwd_elems(D, true) > 0) n = std::max(n, bwd_plan(N, D, bwd_elems(D, true)).blocks);
+  return n;
+}
+
+template <typename T, bool kWhole, bool kCenter, int kElems, int kAhead>
+static int launch_norm_bwd_k(NormBwdArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> raised{0};
-  const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter>, raised);
+  const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, kElems, kAhead>, raised);
   if (rc != FLCE_OK) return rc;
-  const NormPlan p = norm_plan(a.N, a.D, kBwdLane, kBwdThreads);
+  const NormPlan p = bwd_plan(a.N, a.D, kElems);
   a.team = p.team;
   a.teams = p.teams;
+  a.slices = p.blocks;
   const int threads = p.team * p.teams;
   const size_t sums = p.teams > 1 ? 2 * p.teams * static_cast<size_t>(a.D) * sizeof(float) : 0;
-  const size_t copies = 2 * RowCopy<T, kWhole, kBwdLane>::bytes(threads, p.team);
-  norm_bwd_kernel<T, kWhole, kCenter><<<static_cast<unsigned>(p.blocks), threads,
-                                        weight_bytes(a.D) + std::max(sums, copies), s>>>(a);
+  const size_t copies = 2 * kAhead * RowCopy<T, kWhole, kElems>::bytes(threads, p.team);
+  norm_bwd_kernel<T, kWhole, kCenter, kElems, kAhead>
+      <<<static_cast<unsigned>(p.blocks), threads, weight_bytes(a.D) + std::max(sums, copies),
+         s>>>(a);
   return launch_status("norm_bwd_kernel launch");
 }
 
 template <typename T, bool kCenter>
+static int launch_norm_bwd_held(NormBwdArgs& a, int elems, bool whole, cudaStream_t s) {
+  constexpr int kAhead16 = sizeof(T) == 2 ? 2 : 1;
+  if (whole)
+    return elems == 8 ? launch_norm_bwd_k<T, true, kCenter, 8, 2>(a, s)
+                      : launch_norm_bwd_k<T, true, kCenter, 16, kAhead16>(a, s);
+  return elems == 8 ? launch_norm_bwd_k<T, false, kCenter, 8, 2>(a, s)
+                    : launch_norm_bwd_k<T, false, kCenter, 16, 1>(a, s);
+}
+
+template <typename T, bool kCenter>
 static int launch_norm_bwd(NormBwdArgs a, int dt, cudaStream_t s) {
-  if (a.N > 0 && bwd_held(a.D)) {
-    const bool w = whole(dt, a.x, a.ldx) && whole(dt, a.dy, a.lddy) &&
-                   whole(dt, a.dx, a.dx != nullptr ? a.lddx : 0) && whole(dt, nullptr, a.D);
-    const int rc = w ? launch_norm_bwd_held<T, true, kCenter>(a, s)
-                     : launch_norm_bwd_held<T, false, kCenter>(a, s);
+  const bool w = whole(dt, a.x, a.ldx) && whole(dt, a.dy, a.lddy) &&
+                 whole(dt, a.dx, a.dx != nullptr ? a.lddx : 0) && whole(dt, nullptr, a.D);
+  const int elems = bwd_elems(a.D, dt == FLCE_F32);
+  if (a.N > 0 && elems > 0) {
+    const int rc = launch_norm_bwd_held<T, kCenter>(a, elems, w, s);
     if (rc != FLCE_OK) return rc;
   } else if (a.N > 0) {
+    a.slices = std::min<int64_t>(64, a.N);
     if (a.part != nullptr) {
       const dim3 g(static_cast<unsigned>((a.D + kLongThreads - 1) / kLongThreads),
                    static_cast<unsigned>(a.slices));
@@ -929,7 +972,6 @@ static int norm_bwd(NormBwdArgs a, int dt, int wdt, void* ws, size_t ws_bytes,
     if (!aligned(ws, 16)) return FLCE_EALIGN;
   }
   a.part = cols ? static_cast<float*>(ws) : nullptr;
-  a.slices = a.N > 0 ? bwd_slices(a.N, a.D) : 0;
   a.w_f32 = wdt == FLCE_F32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dt == FLCE_BF16 ? launch_norm_bwd<__nv_bfloat16, kCenter>(a, dt, s)
