@@ -17,7 +17,7 @@ from .api import (  # noqa: E402,F401
 )
 from .ops import (  # noqa: E402,F401
     Head4, NormGrads, NormOut, embedding, embedding_bwd, embedding_bwd_workspace_bytes,
-    embedding_fwd, head4_logits, head4_quantize, head4_workspace_bytes, layer_norm,
+    embedding_fwd, head4_logits, head4_quantize, layer_norm,
     layer_norm_bwd, layer_norm_fwd, norm_bwd_workspace_bytes, rms_norm, rms_norm_bwd,
     rms_norm_fwd,
 )

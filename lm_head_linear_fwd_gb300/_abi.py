@@ -81,9 +81,8 @@ _SIGNATURES = {
                             _i, _p, _sz, _p]),
     "rms_norm_bwd": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _p, _i64, _p, _i, _p,
                           _sz, _p]),
-    "head4_workspace_bytes": (_sz, [_i, _i64, _i64, _i64]),
     "head4_logits": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _i, _i64, _p, _p, _i,
-                          _i64, _p, _sz, _p]),
+                          _i64, _p]),
     "head4_quantize": (_i, [_p, _i, _i64, _i64, _i64, _i, _p, _i64, _p, _i, _p, _p]),
     "flce_gemm": (_i, [_i, _i, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _p]),
 }
@@ -178,6 +177,5 @@ rms_norm_fwd = _call("rms_norm_fwd")
 norm_bwd_workspace_bytes = _call("norm_bwd_workspace_bytes")
 layer_norm_bwd = _call("layer_norm_bwd")
 rms_norm_bwd = _call("rms_norm_bwd")
-head4_workspace_bytes = _call("head4_workspace_bytes")
 head4_logits = _call("head4_logits")
 head4_quantize = _call("head4_quantize")

@@ -618,16 +618,10 @@ static int check_head4(const void* packed, int64_t ldp, const void* scales, int 
 
 using namespace flce;
 
-extern "C" size_t head4_workspace_bytes(int dt, int64_t M, int64_t D, int64_t V) {
-  (void)dt, (void)M, (void)D, (void)V;
-  return 0;
-}
-
 extern "C" int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t ldx,
                             const uint8_t* packed, int64_t ldp, const void* scales, int dt_s,
                             const uint8_t* zeros, int group, int64_t V, const void* bias, void* y,
-                            int dt_y, int64_t ldy, void* ws, size_t ws_bytes,
-                            flce_stream_t stream) {
+                            int dt_y, int64_t ldy, flce_stream_t stream) {
   if (!valid_dtype(dt) || !valid_dtype(dt_y)) return FLCE_EDTYPE;
   if (M < 0) return FLCE_ESHAPE;
   int rc = check_head4(packed, ldp, scales, dt_s, group, V, D);
@@ -635,9 +629,6 @@ extern "C" int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t
   if (rc == FLCE_OK) rc = check_matrix(y, dt_y, M, V, ldy);
   if (rc != FLCE_OK) return rc;
   if (!aligned(bias, dtype_size(dt))) return FLCE_EALIGN;
-  const size_t need = head4_workspace_bytes(dt, M, D, V);
-  if (need > 0 && (ws == nullptr || ws_bytes < need)) return FLCE_EWORKSPACE;
-  if (!aligned(ws, 16)) return FLCE_EALIGN;
   if (M == 0) return FLCE_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Head4Args a{};

@@ -23,21 +23,36 @@ stream into the capture.
 from __future__ import annotations
 
 import dataclasses
+import functools
 from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .api import _cuda, _dtype_code, _ptr, _stream, new_status
+from .api import _cuda, _dtype_code, _ptr, new_status
+from .api import _stream as _stream_of
+
+# A call on a few tokens costs less on the device than its checks here, so these
+# ask a tensor for each property once.  The stream's handle comes from the same
+# place that torch.cuda.current_stream takes it from.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device):
+    if _raw_stream is None or device.index is None:
+        return _stream_of(device)
+    return _raw_stream(device.index)
 
 
 def _matrix(t, name):
-    """A CUDA [rows, cols] argument with unit column stride; its row stride."""
+    """A CUDA [rows, cols] argument with unit column stride: rows, cols, row stride."""
     _cuda(t, name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be 2-D with unit stride along its rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    rows, cols = shape
+    return rows, cols, stride[0] if rows > 1 else cols
 
 
 def _rows_of(t):
@@ -50,7 +65,7 @@ def _output(t, name, shape, dtype, device):
     """An optional caller-owned output, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} of shape {list(shape)} on {device}")
     if len(shape) == 1 and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -62,18 +77,19 @@ def _vector(t, name, n, dtype=None):
     if t is None:
         return None
     _cuda(t, name)
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{n}] tensor")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     return t
 
 
 def _ids(ids):
     _cuda(ids, "ids")
-    if ids.dtype != torch.int64 or ids.dim() != 1:
+    shape = ids.shape
+    if ids.dtype is not torch.int64 or len(shape) != 1:
         raise ValueError("ids must be int64 of shape [N]")
-    return ids.contiguous()
+    return ids.contiguous(), shape[0]
 
 
 def _padding(padding_idx, V):
@@ -97,18 +113,19 @@ def embedding_fwd(ids, W, scale=1.0, *, out=None, status=None) -> torch.Tensor:
     """out[i] = scale * W[ids[i]] for ids [N] int64 and W [V, D] (bf16 or fp32,
     row stride free).  An id outside [0, V) gives a row of zeros and sets
     ``status`` (FLCE_ELABEL).  ``out``/``status`` let a caller reuse buffers."""
-    ldw = _matrix(W, "W")
-    ids = _ids(ids)
-    N, (V, D) = ids.shape[0], W.shape
-    out = _output(out, "out", (N, D), W.dtype, W.device)
-    ldo = _matrix(out, "out")
-    status = status if status is not None else new_status(W.device)
-    rc = _abi.embedding_fwd(_ptr(ids), _ptr(W), _dtype_code(W), N, D, V, ldw, float(scale),
-                            _ptr(out), ldo, _ptr(status), _stream(W.device))
+    V, D, ldw = _matrix(W, "W")
+    ids, N = _ids(ids)
+    dev = W.device
+    out = _output(out, "out", (N, D), W.dtype, dev)
+    ldo = _matrix(out, "out")[2]
+    status = status if status is not None else new_status(dev)
+    rc = _abi.embedding_fwd(ids.data_ptr(), W.data_ptr(), _dtype_code(W), N, D, V, ldw, float(scale),
+                            out.data_ptr(), ldo, status.data_ptr(), _stream(dev))
     _abi.check(rc, "embedding_fwd")
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def embedding_bwd_workspace_bytes(N: int, D: int, V: int) -> int:
     """Bytes of device workspace embedding_bwd needs."""
     return int(_abi.embedding_bwd_workspace_bytes(N, D, V))
@@ -122,17 +139,16 @@ def embedding_bwd(ids, grad_out, V, scale=1.0, padding_idx=None, *, grad_W=None,
     (``grad_W``, or a new tensor of ``grad_dtype``), or with
     ``accumulate_grad_W`` added to the fp32 ``grad_W``, whose other rows are
     not touched.  Tokens with id ``padding_idx`` are left out."""
-    ldg = _matrix(grad_out, "grad_out")
-    ids = _ids(ids)
-    N, D = grad_out.shape
-    if ids.shape[0] != N:
+    N, D, ldg = _matrix(grad_out, "grad_out")
+    ids, n = _ids(ids)
+    if n != N:
         raise ValueError(f"ids must be int64 of shape [{N}]")
     V = int(V)
     dev = grad_out.device
     if accumulate_grad_W and grad_W is None:
         raise ValueError("accumulate_grad_W needs grad_W")
     grad_W = _output(grad_W, "grad_W", (V, D), grad_dtype if grad_W is None else grad_W.dtype, dev)
-    ldw = _matrix(grad_W, "grad_W")
+    ldw = _matrix(grad_W, "grad_W")[2]
     ws = _workspace(ws, embedding_bwd_workspace_bytes(N, D, V), dev)
     status = status if status is not None else new_status(dev)
     rc = _abi.embedding_bwd(_ptr(ids), _ptr(grad_out), _dtype_code(grad_out), N, D, V, ldg,
@@ -195,11 +211,10 @@ class NormGrads:
     grad_bias: Optional[torch.Tensor]    # fp32
 
 
-def _norm_params(x, weight, bias):
-    D = x.shape[1]
+def _norm_params(D, weight, bias):
     _vector(weight, "weight", D)
     _vector(bias, "bias", D)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+    if weight is not None and bias is not None and weight.dtype is not bias.dtype:
         raise TypeError("weight and bias must share one dtype")
     p = weight if weight is not None else bias
     return _abi.FLCE_F32 if p is None else _dtype_code(p)
@@ -210,29 +225,30 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, mean=None,
     """Layer norm of the rows of x [N, D] (bf16 or fp32, row stride free) with
     weight and bias [D] (each optional, bf16 or fp32).  Returns y (dtype of x;
     ``y`` may be x itself) and the fp32 mean and rstd the backward needs."""
-    ldx = _matrix(x, "x")
-    N, D = x.shape
-    wdt = _norm_params(x, weight, bias)
-    y = _output(y, "y", (N, D), x.dtype, x.device)
-    ldy = _matrix(y, "y")
-    mean = _output(mean, "mean", (N,), torch.float32, x.device)
-    rstd = _output(rstd, "rstd", (N,), torch.float32, x.device)
-    rc = _abi.layer_norm_fwd(_ptr(x), _dtype_code(x), N, D, ldx, _ptr(weight), _ptr(bias), wdt,
-                             float(eps), _ptr(y), ldy, _ptr(mean), _ptr(rstd), _stream(x.device))
+    N, D, ldx = _matrix(x, "x")
+    wdt = _norm_params(D, weight, bias)
+    dev = x.device
+    y = _output(y, "y", (N, D), x.dtype, dev)
+    ldy = _matrix(y, "y")[2]
+    mean = _output(mean, "mean", (N,), torch.float32, dev)
+    rstd = _output(rstd, "rstd", (N,), torch.float32, dev)
+    rc = _abi.layer_norm_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _ptr(weight), _ptr(bias),
+                             wdt, float(eps), y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(),
+                             _stream(dev))
     _abi.check(rc, "layer_norm_fwd")
     return NormOut(y, mean, rstd)
 
 
 def rms_norm_fwd(x, weight=None, eps=1e-5, *, y=None, rstd=None) -> NormOut:
     """RMS norm of the rows of x [N, D]: layer norm without the mean and bias."""
-    ldx = _matrix(x, "x")
-    N, D = x.shape
-    wdt = _norm_params(x, weight, None)
-    y = _output(y, "y", (N, D), x.dtype, x.device)
-    ldy = _matrix(y, "y")
-    rstd = _output(rstd, "rstd", (N,), torch.float32, x.device)
-    rc = _abi.rms_norm_fwd(_ptr(x), _dtype_code(x), N, D, ldx, _ptr(weight), wdt, float(eps),
-                           _ptr(y), ldy, _ptr(rstd), _stream(x.device))
+    N, D, ldx = _matrix(x, "x")
+    wdt = _norm_params(D, weight, None)
+    dev = x.device
+    y = _output(y, "y", (N, D), x.dtype, dev)
+    ldy = _matrix(y, "y")[2]
+    rstd = _output(rstd, "rstd", (N,), torch.float32, dev)
+    rc = _abi.rms_norm_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _ptr(weight), wdt,
+                           float(eps), y.data_ptr(), ldy, rstd.data_ptr(), _stream(dev))
     _abi.check(rc, "rms_norm_fwd")
     return NormOut(y, None, rstd)
 
@@ -242,11 +258,10 @@ def norm_bwd_workspace_bytes(N: int, D: int) -> int:
     return int(_abi.norm_bwd_workspace_bytes(N, D))
 
 
-def _norm_bwd_args(x, grad_y, weight, rstd, want_x, want_w, want_b, grad_x, grad_weight,
+def _norm_bwd_args(x, N, D, grad_y, rstd, want_x, want_w, want_b, grad_x, grad_weight,
                    grad_bias, accumulate, ws):
-    N, D = x.shape
     dev = x.device
-    if grad_y.shape != x.shape or grad_y.dtype != x.dtype:
+    if grad_y.shape != (N, D) or grad_y.dtype is not x.dtype:
         raise ValueError("grad_y must have the shape and dtype of x")
     _vector(rstd, "rstd", N, torch.float32)
     if rstd is None:
@@ -258,7 +273,7 @@ def _norm_bwd_args(x, grad_y, weight, rstd, want_x, want_w, want_b, grad_x, grad
     gb = _output(grad_bias, "grad_bias", (D,), torch.float32, dev) if want_b else None
     if want_w or want_b:
         ws = _workspace(ws, norm_bwd_workspace_bytes(N, D), dev)
-    return gx, 0 if gx is None else _matrix(gx, "grad_x"), gw, gb, ws
+    return gx, 0 if gx is None else _matrix(gx, "grad_x")[2], gw, gb, ws
 
 
 def layer_norm_bwd(x, grad_y, mean, rstd, weight=None, *, want_grad_x=True,
@@ -267,15 +282,14 @@ def layer_norm_bwd(x, grad_y, mean, rstd, weight=None, *, want_grad_x=True,
     """Gradients of layer_norm_fwd from its x, mean, rstd and the incoming
     grad_y: grad_x (dtype of x; ``grad_x`` may be grad_y itself), grad_weight
     and grad_bias (fp32; added to the given ones when ``accumulate``)."""
-    ldx = _matrix(x, "x")
-    ldg = _matrix(grad_y, "grad_y")
-    N, D = x.shape
-    wdt = _norm_params(x, weight, None)
+    N, D, ldx = _matrix(x, "x")
+    ldg = _matrix(grad_y, "grad_y")[2]
+    wdt = _norm_params(D, weight, None)
     if mean is None:
         raise ValueError("mean must be given")
     _vector(mean, "mean", N, torch.float32)
     want_w = weight is not None if want_grad_weight is None else want_grad_weight
-    gx, ldgx, gw, gb, ws = _norm_bwd_args(x, grad_y, weight, rstd, want_grad_x, want_w,
+    gx, ldgx, gw, gb, ws = _norm_bwd_args(x, N, D, grad_y, rstd, want_grad_x, want_w,
                                           want_grad_bias, grad_x, grad_weight, grad_bias,
                                           accumulate, ws)
     rc = _abi.layer_norm_bwd(_ptr(x), _dtype_code(x), N, D, ldx, _ptr(grad_y), ldg, _ptr(weight),
@@ -289,12 +303,11 @@ def layer_norm_bwd(x, grad_y, mean, rstd, weight=None, *, want_grad_x=True,
 def rms_norm_bwd(x, grad_y, rstd, weight=None, *, want_grad_x=True, want_grad_weight=None,
                  grad_x=None, grad_weight=None, accumulate=False, ws=None) -> NormGrads:
     """Gradients of rms_norm_fwd (see layer_norm_bwd)."""
-    ldx = _matrix(x, "x")
-    ldg = _matrix(grad_y, "grad_y")
-    N, D = x.shape
-    wdt = _norm_params(x, weight, None)
+    N, D, ldx = _matrix(x, "x")
+    ldg = _matrix(grad_y, "grad_y")[2]
+    wdt = _norm_params(D, weight, None)
     want_w = weight is not None if want_grad_weight is None else want_grad_weight
-    gx, ldgx, gw, _, ws = _norm_bwd_args(x, grad_y, weight, rstd, want_grad_x, want_w, False,
+    gx, ldgx, gw, _, ws = _norm_bwd_args(x, N, D, grad_y, rstd, want_grad_x, want_w, False,
                                          grad_x, grad_weight, None, accumulate, ws)
     rc = _abi.rms_norm_bwd(_ptr(x), _dtype_code(x), N, D, ldx, _ptr(grad_y), ldg, _ptr(weight),
                            wdt, _ptr(rstd), _ptr(gx), ldgx, _ptr(gw), 1 if accumulate else 0,
@@ -375,10 +388,10 @@ class Head4:
 
 
 def _head4_args(head):
-    ldp = _matrix(head.packed, "packed")
-    if head.packed.shape[1] < (head.D + 127) // 128 * 64:
+    V, width, ldp = _matrix(head.packed, "packed")
+    if width < (head.D + 127) // 128 * 64:
         raise ValueError("packed must hold ceil(D / 128) * 64 bytes per row")
-    shape = (head.V, -(-head.D // head.group))
+    shape = (V, -(-head.D // head.group))
     _cuda(head.scales, "scales")
     if head.scales.shape != shape or not head.scales.is_contiguous():
         raise ValueError(f"scales must be a contiguous {list(shape)} tensor")
@@ -386,18 +399,17 @@ def _head4_args(head):
         _cuda(head.zeros, "zeros")
         if head.zeros.shape != shape or not head.zeros.is_contiguous():
             raise ValueError(f"zeros must be a contiguous {list(shape)} tensor")
-    if head.packed.dtype != torch.uint8 or \
-            (head.zeros is not None and head.zeros.dtype != torch.uint8):
+    if head.packed.dtype is not torch.uint8 or \
+            (head.zeros is not None and head.zeros.dtype is not torch.uint8):
         raise TypeError("packed and zeros must be uint8")
-    return ldp
+    return V, ldp
 
 
 def head4_quantize(W, group=128, *, zero_point=False, scale_dtype=None) -> Head4:
     """Rounds a head W [V, D] (bf16 or fp32, finite, row stride free) to 4 bits
     with a scale, and with ``zero_point`` a zero point, per ``group`` columns
     (32, 64 or 128) of a row.  ``scale_dtype`` defaults to W's."""
-    ldw = _matrix(W, "W")
-    V, D = W.shape
+    V, D, ldw = _matrix(W, "W")
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     G = -(-D // group)
@@ -413,30 +425,24 @@ def head4_quantize(W, group=128, *, zero_point=False, scale_dtype=None) -> Head4
     return head
 
 
-def head4_workspace_bytes(dt_code: int, M: int, D: int, V: int) -> int:
-    """Bytes of device workspace head4_logits needs."""
-    return int(_abi.head4_workspace_bytes(dt_code, M, D, V))
-
-
-def head4_logits(x, head: Head4, bias=None, *, out=None, out_dtype=torch.float32,
-                 ws=None) -> torch.Tensor:
+def head4_logits(x, head: Head4, bias=None, *, out=None,
+                 out_dtype=torch.float32) -> torch.Tensor:
     """Logits [M, V] of the hidden states x [M, D] (bf16 or fp32): x times the
     head's 4-bit weights transposed (+ bias [V], dtype of x).  Made for M up to
     a few tens (decoding); ``out`` (bf16 or fp32) or ``out_dtype`` sets the
     logits' dtype."""
-    ldx = _matrix(x, "x")
-    M, D = x.shape
+    M, D, ldx = _matrix(x, "x")
     if D != head.D:
         raise ValueError(f"x must be [M, {head.D}]")
-    ldp = _head4_args(head)
-    _vector(bias, "bias", head.V, x.dtype)
-    out = _output(out, "out", (M, head.V), out_dtype if out is None else out.dtype, x.device)
-    ldo = _matrix(out, "out")
+    V, ldp = _head4_args(head)
+    _vector(bias, "bias", V, x.dtype)
+    dev = x.device
+    out = _output(out, "out", (M, V), out_dtype if out is None else out.dtype, dev)
+    ldo = _matrix(out, "out")[2]
     dt = _dtype_code(x)
-    ws = _workspace(ws, head4_workspace_bytes(dt, M, D, head.V), x.device)
-    rc = _abi.head4_logits(_ptr(x), dt, M, D, ldx, _ptr(head.packed), ldp, _ptr(head.scales),
-                           _dtype_code(head.scales), _ptr(head.zeros), head.group, head.V,
-                           _ptr(bias), _ptr(out), _dtype_code(out), ldo, _ptr(ws),
-                           0 if ws is None else ws.numel(), _stream(x.device))
+    rc = _abi.head4_logits(x.data_ptr(), dt, M, D, ldx, head.packed.data_ptr(), ldp,
+                           head.scales.data_ptr(), _dtype_code(head.scales), _ptr(head.zeros),
+                           head.group, V, _ptr(bias), out.data_ptr(), _dtype_code(out), ldo,
+                           _stream(dev))
     _abi.check(rc, "head4_logits")
     return out
