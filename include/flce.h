@@ -527,11 +527,12 @@ FLCE_API int rms_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64_t l
 
 /* x: [M, ldx] of dtype dt; bias: [V] of dtype dt or NULL; y: [M, ldy] of dtype
  * dt_y.  M == 0 is valid.  Made for M up to a few tens: the weights are read
- * again for every 32 bf16 (10 fp32) tokens. */
+ * again for every 32 bf16 (10 fp32) tokens.  status (may be NULL): set only if
+ * a wait inside the kernel gave up (FLCE_ETIMEOUT). */
 FLCE_API int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t ldx,
                           const uint8_t* packed, int64_t ldp, const void* scales, int dt_s,
                           const uint8_t* zeros, int group, int64_t V, const void* bias, void* y,
-                          int dt_y, int64_t ldy, flce_stream_t stream);
+                          int dt_y, int64_t ldy, int32_t* status, flce_stream_t stream);
 
 /* Rounds W [V, ldw] (dtype dt) to that layout.  Without zeros: scale =
  * max |w| / 7 of the group, q = clamp(round(w / scale), -8, 7) + 8.  With

@@ -82,7 +82,7 @@ _SIGNATURES = {
     "rms_norm_bwd": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _p, _i64, _p, _i, _p,
                           _sz, _p]),
     "head4_logits": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _i, _i64, _p, _p, _i,
-                          _i64, _p]),
+                          _i64, _p, _p]),
     "head4_quantize": (_i, [_p, _i, _i64, _i64, _i64, _i, _p, _i64, _p, _i, _p, _p]),
     "flce_gemm": (_i, [_i, _i, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _p]),
 }

@@ -426,11 +426,11 @@ def head4_quantize(W, group=128, *, zero_point=False, scale_dtype=None) -> Head4
 
 
 def head4_logits(x, head: Head4, bias=None, *, out=None,
-                 out_dtype=torch.float32) -> torch.Tensor:
+                 out_dtype=torch.float32, status=None) -> torch.Tensor:
     """Logits [M, V] of the hidden states x [M, D] (bf16 or fp32): x times the
     head's 4-bit weights transposed (+ bias [V], dtype of x).  Made for M up to
     a few tens (decoding); ``out`` (bf16 or fp32) or ``out_dtype`` sets the
-    logits' dtype."""
+    logits' dtype.  ``status``: a word for a wait that gave up (new_status)."""
     M, D, ldx = _matrix(x, "x")
     if D != head.D:
         raise ValueError(f"x must be [M, {head.D}]")
@@ -443,6 +443,6 @@ def head4_logits(x, head: Head4, bias=None, *, out=None,
     rc = _abi.head4_logits(x.data_ptr(), dt, M, D, ldx, head.packed.data_ptr(), ldp,
                            head.scales.data_ptr(), _dtype_code(head.scales), _ptr(head.zeros),
                            head.group, V, _ptr(bias), out.data_ptr(), _dtype_code(out), ldo,
-                           _stream(dev))
+                           _ptr(status), _stream(dev))
     _abi.check(rc, "head4_logits")
     return out

@@ -96,7 +96,8 @@ def test_norm_bwd(abi):
 def test_head4(abi):
     call = _caller(abi.head4_logits, dict(x=A, dt=0, M=2, D=200, ldx=200, packed=B, ldp=128,
                                           scales=C, dts=0, zeros=None, group=64, V=10, bias=None,
-                                          y=0x30000000, dty=1, ldy=10, stream=None))
+                                          y=0x30000000, dty=1, ldy=10, status=None,
+                                          stream=None))
     assert call(dt=2) == call(dts=2) == call(dty=2) == EDTYPE
     assert call(M=-1) == call(D=0) == call(V=0) == call(group=48) == call(ldp=112) == ESHAPE
     assert call(ldx=199) == call(ldy=9) == ESHAPE
