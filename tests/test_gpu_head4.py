@@ -62,6 +62,40 @@ def test_logits(lh, M, D, V, group, dtype, sdt, out, zero):
         assert (wide[:, 0] == 7).all() and (wide[:, 1 + V:] == 7).all()
 
 
+@pytest.mark.parametrize("M,group,dtype", [(1, 32, BF), (12, 64, BF), (20, 64, BF), (32, 32, BF),
+                                           (7, 128, F32), (3, 64, F32)])
+def test_logits_of_many_rows_and_columns(lh, M, group, dtype):
+    """More tiles than a launch holds at once, more columns than stay on chip."""
+    V, D = 90001, 2600
+    x = _randn((M, D), dtype, 11)
+    head = _head(lh, V, D, group, True, BF, 12)
+    y = lh.head4_logits(x, head)
+    for rows in (slice(0, 300), slice(38800, 39300), slice(77700, 78100), slice(89700, 90001)):
+        part = lh.Head4(head.packed[rows], head.scales[rows], head.zeros[rows], D, group)
+        Wq = R.head4_weights(part.packed, part.scales, part.zeros, D, group)
+        ref, bound = R.head4(x, Wq, None, group, F32)
+        R.close(y[:, rows], ref, bound, (M, group, rows))
+    # every row, up to the order of the sums of rows that split a tile's columns
+    again = torch.cat([lh.head4_logits(x, lh.Head4(head.packed[i:i + 45000],
+                                                   head.scales[i:i + 45000],
+                                                   head.zeros[i:i + 45000], D, group))
+                       for i in range(0, V, 45000)], 1)
+    scale = (x.float().abs().sum(1, keepdim=True) * 15 * 0.021)
+    assert ((y - again).abs() <= scale * (D + 8) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("M", [3, 12, 32])
+def test_specials_stay_in_their_token(lh, M):
+    head = _head(lh, 300, 600, 64, True, BF, 13)
+    x = _randn((M, 600), BF, 14)
+    want = lh.head4_logits(x, head)
+    x[1, 5], x[2, 599] = float("inf"), float("nan")
+    y = lh.head4_logits(x, head)
+    keep = [m for m in range(M) if m not in (1, 2)]
+    assert torch.equal(y[keep], want[keep])
+    assert not y[1].isfinite().any() and y[2].isnan().all()
+
+
 def test_one_hot_reads_every_weight(lh):
     """x = e_k gives column k of the weights exactly (bf16 scales, fp32 logits)."""
     D, V = 300, 70
