@@ -242,12 +242,8 @@ struct RowCopy {
       // (whole rows: places past the row's end were cleared and are never written)
       uint4 v = *reinterpret_cast<const uint4*>(own + k * pitch);
       if (!kWhole) {
-        uint4 right;
-        right.x = __shfl_down_sync(0xffffffffu, v.x, 1);
-        right.y = __shfl_down_sync(0xffffffffu, v.y, 1);
-        right.z = __shfl_down_sync(0xffffffffu, v.z, 1);
-        right.w = __shfl_down_sync(0xffffffffu, v.w, 1);
-        if (t.last) right = *reinterpret_cast<const uint4*>(end + k * end_pitch);
+        const uint4 right = *reinterpret_cast<const uint4*>(
+            t.last ? end + k * end_pitch : own + k * pitch + 16);
         v = bytes_from(v, right, off);
         const int left = D - t.at(k) * VEC;
         if (left < VEC) {
@@ -414,6 +410,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
   for (; turns > 0; turns -= kRows, rows -= kRows) {
     float2 f[kRows][NV][P];
     copies_wait<0>();
+    if (!kWhole) __syncwarp();  // the right neighbour's blocks
 #pragma unroll
     for (int r = 0; r < kRows; ++r) copy[r].read(x.p + r * x.step, D, team, f[r]);
     x.p += kRows * x.step;
@@ -580,6 +577,7 @@ __global__ void __launch_bounds__(kBwdThreads<kElems>) norm_bwd_kernel(NormBwdAr
     const float mean = f.mean, rstd = f.rstd;
     float2 h[NV][P], u[NV][P];
     copies_wait<kAhead - 1>();
+    if (!kWhole) __syncwarp();  // the right neighbour's blocks
     f.x.read(x.p, D, team, h);
     f.g.read(dy.p, D, team, u);
     __syncwarp();
