@@ -154,6 +154,37 @@ def test_quantize(lh, V, D, group, zero, dtype, sdt):
         assert ((y - W.float().cpu()).abs() <= step * 0.5 * (1 + 1e-6)).all()
 
 
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("dtype,group", [(F32, 32), (BF, 64), (F32, 128), (BF, 128)])
+def test_quantize_halves_and_extremes(lh, dtype, group, zero):
+    """Quotients that end in one half, scales near the ends of fp32, many rows: the
+    nibbles of an exact division, rounded to even."""
+    V, D = 9001, 640
+    g = torch.Generator().manual_seed(21)
+    W = torch.randint(-14, 15, (V, D), generator=g).float() / 2 + 0.0
+    W[:, ::group] = 7.0 if not zero else 7.5   # the group's largest: scales of 1 (and 2^k)
+    if zero:
+        W[:, 1::group] = -7.5
+        W.clamp_(-7.5, 7.5)
+    W *= 2.0 ** torch.randint(-90, 91, (V, 1), generator=g).float()
+    W[:40] *= 0
+    W[40:80] = torch.randn(40, D, generator=g) * 2e-38
+    W[80:120] = torch.randn(40, D, generator=g) * 1e37
+    W[120:4000] = torch.randn(3880, D, generator=g)
+    W = W.to(dtype)
+    h = lh.head4_quantize(W.cuda(), group, zero_point=zero, scale_dtype=dtype)
+    Wg = W.float().view(V, D // group, group)
+    lo, hi = Wg.amin(2).clamp(max=0), Wg.amax(2).clamp(min=0)
+    s = ((hi - lo) / 15 if zero else torch.maximum(hi, -lo) / 7).to(dtype).float()
+    s[s == 0] = 1
+    z = (-lo / s).round().clamp(0, 15) if zero else torch.full_like(s, 8)
+    q = ((Wg / s[:, :, None]).round() + z[:, :, None]).clamp(0, 15).view(V, D)
+    assert torch.equal(h.scales.float().cpu(), s)
+    if zero:
+        assert torch.equal(h.zeros.cpu().float(), z)
+    assert torch.equal(R.unpack4(h.packed, D).float(), q)
+
+
 def test_stream_graph_and_far_rows(lh):
     D, V = 512, 1000
     head = _head(lh, V, D, 128, False, BF, 1)
