@@ -42,7 +42,8 @@ constexpr int kLookupThreads = 128;
 constexpr int kLookupLane = 32;  // elements of a row per lane and task
 
 // One warp copies 32 * kLookupLane elements of one row at a time, all its loads
-// in flight together.
+// in flight together.  Bound by memory: 65536 rows of 5120 bf16 take 130 us (6.3 TB/s
+// with each table row counted once).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kLookupThreads)
     embedding_fwd_kernel(const int64_t* __restrict__ ids, const T* __restrict__ W, int64_t N,
@@ -138,6 +139,9 @@ static void launch_fwd(const int64_t* ids, const void* W, int64_t N, int64_t D, 
 //    whose tokens all lie in its chunk.  A run of equal ids over several chunks
 //    leaves one partial sum per chunk; the last CTA to arrive (an integer
 //    ticket) adds the partial sums in chunk order and writes the row.
+//
+// Bound by the gradient's stores where it is written whole (8192 x 4096 tokens into
+// 128256 rows of fp32: 336 us, 6.5 TB/s), else by the two steps in a row.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -364,21 +368,25 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
 
 // The sort of up to kRankShare tokens per SM: every CTA finds the places of its
 // share of the tokens by itself.  It orders its share, then runs over all ids
-// and looks up by bisection between which of its tokens each belongs; the
-// running sum of these counts is the number of tokens before each of its own.
+// and looks up by bisection how many of its tokens come after each; the running
+// sum of these counts is the number of tokens before each of its own.  Indices
+// outside the share lie all before or all after it, so keys alone decide.
 // No passes, and no CTA waits for another.  Where rows are to be filled, half of
 // the warps start on that at once and the others join them.
-// The work grows with N times the bisection's steps on every SM, the cluster's
-// sort with N alone but it starts higher: 8192 tokens 10.7 against 20 us, 32768
-// tokens 49 against 28 us (with the launch, cold caches).
+// Bound by the look-ups' instructions on every SM: 8192 tokens take 8 us.  The work
+// grows with N times the bisection's steps, the cluster's sort with N alone but it
+// starts higher: gradients (added) of 8192 x 4096 with this 43.8 us, with the sort
+// 56.2; of 16384 x 1024 33.6 and 37.9; of 32768 x 1024 56.7 and 52.4.
 constexpr int kRankShare = 128;
+constexpr int kRankAhead = 4;  // ids a thread looks up together
 
 __global__ void __launch_bounds__(kSortThreads) embedding_rank_kernel(SortArgs a) {
-  __shared__ uint64_t own[kRankShare], ordered[kRankShare];
+  __shared__ uint64_t own[kRankShare];
+  __shared__ uint32_t ordered[2 * kRankShare], token[kRankShare];  // own keys in order
   __shared__ uint32_t before[kRankShare + 1];
   __shared__ uint32_t mark[kFillRows / 32];
   __shared__ int next_row;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int64_t k = blockIdx.x * int64_t(kSortThreads) + tid; k < a.tickets;
        k += gridDim.x * int64_t(kSortThreads))
     a.ticket[k] = 0;
@@ -398,42 +406,64 @@ __global__ void __launch_bounds__(kSortThreads) embedding_rank_kernel(SortArgs a
     const int m = static_cast<int>(max(int64_t(0), min(share, a.N - t0)));
     if (tid <= kRankShare) before[tid] = 0;
     // a token as one number: by key, then by index
-    uint64_t e = 0;
     if (tid < m) {
       bool ok;
       const uint32_t key = sort_key(a, a.ids[t0 + tid], &ok);
       if (!ok) set_status(a.status, FLCE_ELABEL);
-      e = static_cast<uint64_t>(key) << 32 | static_cast<uint64_t>(t0 + tid);
-      own[tid] = e;
+      own[tid] = static_cast<uint64_t>(key) << 32 | static_cast<uint64_t>(t0 + tid);
     }
+    if (tid >= m && tid < 2 * kRankShare) ordered[tid] = 0xffffffffu;  // above every key
     named_barrier(1, team);
-    if (tid < m) {
+    // the order of the own tokens, a warp to a token
+    for (int i = warp; i < m; i += team / 32) {
+      const uint64_t e = own[i];
       int r = 0;
-      for (int j = 0; j < m; ++j) r += own[j] < e;
-      ordered[r] = e;
-    }
-    named_barrier(1, team);
-    if (m > 0) {
-#pragma unroll 4
-      for (int64_t i = tid; i < a.N; i += team) {
-        bool ok;
-        const uint32_t key = sort_key(a, a.ids[i], &ok);
-        const uint64_t x = static_cast<uint64_t>(key) << 32 | static_cast<uint64_t>(i);
-        int lo = 0;  // number of own tokens up to x
-#pragma unroll
-        for (int step = kRankShare / 2; step > 0; step /= 2)
-          if (lo + step <= m && ordered[lo + step - 1] <= x) lo += step;
-        if (lo < m && ordered[lo] <= x) ++lo;
-        if (lo < m) atomicAdd(&before[lo], 1u);
+      for (int j = lane; j < m; j += 32) r += own[j] < e;
+      r = __reduce_add_sync(0xffffffffu, r);
+      if (lane == 0) {
+        ordered[r] = static_cast<uint32_t>(e >> 32);
+        token[r] = static_cast<uint32_t>(e);
       }
     }
     named_barrier(1, team);
-    if (tid < m) {
-      uint32_t s = 0;
-      for (int j = 0; j <= tid; ++j) s += before[j];
-      if (in_range(s, a.N, a.status))
-        a.buf0[s] = make_uint2(static_cast<uint32_t>(ordered[tid] >> 32),
-                               static_cast<uint32_t>(ordered[tid]));
+    if (m > 0) {
+      int top = 1;
+      while (2 * top <= m) top *= 2;
+      for (int64_t i0 = tid; i0 < a.N; i0 += kRankAhead * team) {
+        uint32_t bound[kRankAhead];
+        int lo[kRankAhead];
+#pragma unroll
+        for (int k = 0; k < kRankAhead; ++k) {
+          // own tokens before token i: those of smaller keys, and the equal ones where
+          // all own tokens come first (past the end: i = N - 1 again, not counted)
+          const int64_t i = min(i0 + k * team, a.N - 1);
+          bool ok;
+          bound[k] = sort_key(a, a.ids[i], &ok) + (i > t0 ? 1u : 0u);
+          lo[k] = 0;
+        }
+        for (int step = top; step > 0; step >>= 1)
+#pragma unroll
+          for (int k = 0; k < kRankAhead; ++k)
+            if (ordered[lo[k] + step - 1] < bound[k]) lo[k] += step;
+#pragma unroll
+        for (int k = 0; k < kRankAhead; ++k) {
+          const int64_t i = i0 + k * team;
+          if (i < a.N && (i < t0 || i >= t0 + m) && lo[k] < m) atomicAdd(&before[lo[k]], 1u);
+        }
+      }
+    }
+    named_barrier(1, team);
+    // a warp to 32 own tokens: the counts up to each, and it itself
+    if (warp * 32 < m) {
+      uint32_t s = before[tid];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
+      }
+      for (int w = 0; w < warp; ++w) s += __reduce_add_sync(0xffffffffu, before[w * 32 + lane]);
+      s += static_cast<uint32_t>(tid);
+      if (tid < m && in_range(s, a.N, a.status)) a.buf0[s] = make_uint2(ordered[tid], token[tid]);
     }
   }
   if (!fill) return;

@@ -375,7 +375,8 @@ struct NormArgs {
 
 // A team works on kRows rows at a time (two, where threads of kFwdLane
 // elements can hold a row): one read of the weights and one exchange between its warps serve
-// both.
+// both.  Layer norm 65536 x 5120 bf16: 209 us (6.4 TB/s); RMS norm 8192 x 4096 fp32:
+// 44 us (6.0 TB/s); rows of 1601 that start inside blocks, 8191 of them: 28 us, of 1600 14.
 template <typename T, bool kWhole, bool kCenter, int kElems, int kRows>
 __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
   extern __shared__ float4 weights[];  // weight, then bias, then the rows' copies
@@ -517,7 +518,9 @@ struct NormBwdArgs {
   int team, teams;
 };
 
-// kAhead: rows copied ahead.
+// kAhead: rows copied ahead.  Bound by the latency from a row's loads over its sums to
+// its stores (16 warps of 126 registers to an SM).  RMS norm 8192 x 4096 bf16: 38.6 us
+// with norm_bwd_finish_kernel (5.2 TB/s); layer norm 8191 x 1600: 30 us, x 1601: 39.
 template <typename T, bool kWhole, bool kCenter, int kElems, int kAhead>
 __global__ void __launch_bounds__(kBwdThreads<kElems>) norm_bwd_kernel(NormBwdArgs a) {
   // weight; the rows' copies (at the end: the teams' column sums)
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_bwd_long_cols_kernel(NormBw
 // ---------------------------------------------------------------- column sums
 
 // 32 columns per block: 32 warps add up every 32nd slice, then the warps' sums
-// in warp order.  blockIdx.y: grad_weight, grad_bias.
+// in warp order.  Bound by latency: about 3 us for 152 slices of 4096 columns.  blockIdx.y: grad_weight, grad_bias.
 __global__ void __launch_bounds__(1024) norm_bwd_finish_kernel(NormBwdArgs a) {
   __shared__ float red[32][33];
   float* out = blockIdx.y == 0 ? a.dw : a.db;
