@@ -545,6 +545,25 @@ FLCE_API int head4_quantize(const void* W, int dt, int64_t V, int64_t D, int64_t
                             uint8_t* packed, int64_t ldp, void* scales, int dt_s, uint8_t* zeros,
                             flce_stream_t stream);
 
+/* ------------------------------------------------- arguments from memory
+ *
+ * flce_call makes the call that `entry` names with the arguments that stand in
+ * `args`, eight bytes each in the order of the entry point's own: integers as
+ * int64, pointers as addresses, floats as doubles, in the machine's byte order.
+ * For callers whose foreign-function interface converts arguments one by one.
+ * bytes must be eight times the number of arguments (else FLCE_EINVAL); an
+ * unknown entry gives FLCE_ENOSUP. */
+enum {
+  FLCE_CALL_EMBEDDING_FWD = 0,
+  FLCE_CALL_EMBEDDING_BWD = 1,
+  FLCE_CALL_LAYER_NORM_FWD = 2,
+  FLCE_CALL_RMS_NORM_FWD = 3,
+  FLCE_CALL_LAYER_NORM_BWD = 4,
+  FLCE_CALL_RMS_NORM_BWD = 5,
+  FLCE_CALL_HEAD4_LOGITS = 6
+};
+FLCE_API int flce_call(int entry, const void* args, size_t bytes);
+
 #ifdef __cplusplus
 }
 #endif

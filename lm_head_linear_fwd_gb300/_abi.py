@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import platform
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", platform.machine(), "libflce.so")
@@ -84,6 +85,7 @@ _SIGNATURES = {
     "head4_logits": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _i, _i64, _p, _p, _i,
                           _i64, _p, _p]),
     "head4_quantize": (_i, [_p, _i, _i64, _i64, _i64, _i, _p, _i64, _p, _i, _p, _p]),
+    "flce_call": (_i, [_i, ctypes.c_char_p, _sz]),
     "flce_gemm": (_i, [_i, _i, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _p]),
 }
 
@@ -138,6 +140,30 @@ def _call(name):
         return getattr(load(), name)(*args)
     f.__name__ = name
     return f
+
+
+def _packed(name, entry):
+    """The call with its arguments handed over as one block of memory (flce_call):
+    converting them one by one takes longer than a launch.  A null pointer is 0."""
+    code = {_p: "Q", _f: "d"}
+    args = struct.Struct("=" + "".join(code.get(t, "q") for t in _SIGNATURES[name][1]))
+    pack, size = args.pack, args.size
+
+    def f(*args):
+        return load().flce_call(entry, pack(*args), size)
+    f.__name__ = name
+    return f
+
+
+class packed:
+    """The operators that are also called on a few tokens at a time."""
+    embedding_fwd = staticmethod(_packed("embedding_fwd", 0))
+    embedding_bwd = staticmethod(_packed("embedding_bwd", 1))
+    layer_norm_fwd = staticmethod(_packed("layer_norm_fwd", 2))
+    rms_norm_fwd = staticmethod(_packed("rms_norm_fwd", 3))
+    layer_norm_bwd = staticmethod(_packed("layer_norm_bwd", 4))
+    rms_norm_bwd = staticmethod(_packed("rms_norm_bwd", 5))
+    head4_logits = staticmethod(_packed("head4_logits", 6))
 
 
 flce_status_string = _call("flce_status_string")

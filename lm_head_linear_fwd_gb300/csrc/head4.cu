@@ -241,7 +241,14 @@ __global__ void __launch_bounds__(256) head4_quantize_kernel(Quant4Args a) {
           word += __float_as_uint(x[8 * half + j]) * place;
           extra += 0x4b400000u * place;
         }
-        to[4 * half] = word - extra;
+        word -= extra;
+        const int64_t left = a.D - (block * 128 + k_lane + 8 * half);
+        if (left < 8) {  // columns past the end: 0
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j >= left) word &= ~(15u << (4 * ((j >> 1) + 4 * (j & 1))));
+        }
+        to[4 * half] = word;
       }
       const int64_t gi = (block * 128 + k_lane) >> group_bits;
       if (writes_group && gi < a.G) {

@@ -30,8 +30,10 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .api import _cuda, _dtype_code, _ptr, new_status
+from .api import _cuda, _dtype_code, new_status
 from .api import _stream as _stream_of
+
+_call = _abi.packed
 
 # A call on a few tokens costs less on the device than its checks here, so these
 # ask a tensor for each property once.  The stream's handle comes from the same
@@ -43,6 +45,10 @@ def _stream(device):
     if _raw_stream is None or device.index is None:
         return _stream_of(device)
     return _raw_stream(device.index)
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def _matrix(t, name):
@@ -119,8 +125,8 @@ def embedding_fwd(ids, W, scale=1.0, *, out=None, status=None) -> torch.Tensor:
     out = _output(out, "out", (N, D), W.dtype, dev)
     ldo = _matrix(out, "out")[2]
     status = status if status is not None else new_status(dev)
-    rc = _abi.embedding_fwd(ids.data_ptr(), W.data_ptr(), _dtype_code(W), N, D, V, ldw, float(scale),
-                            out.data_ptr(), ldo, status.data_ptr(), _stream(dev))
+    rc = _call.embedding_fwd(ids.data_ptr(), W.data_ptr(), _dtype_code(W), N, D, V, ldw,
+                             float(scale), out.data_ptr(), ldo, status.data_ptr(), _stream(dev))
     _abi.check(rc, "embedding_fwd")
     return out
 
@@ -151,10 +157,10 @@ def embedding_bwd(ids, grad_out, V, scale=1.0, padding_idx=None, *, grad_W=None,
     ldw = _matrix(grad_W, "grad_W")[2]
     ws = _workspace(ws, embedding_bwd_workspace_bytes(N, D, V), dev)
     status = status if status is not None else new_status(dev)
-    rc = _abi.embedding_bwd(_ptr(ids), _ptr(grad_out), _dtype_code(grad_out), N, D, V, ldg,
-                            float(scale), _padding(padding_idx, V), _ptr(grad_W),
-                            _dtype_code(grad_W), ldw, 1 if accumulate_grad_W else 0, _ptr(ws),
-                            0 if ws is None else ws.numel(), _ptr(status), _stream(dev))
+    rc = _call.embedding_bwd(_addr(ids), _addr(grad_out), _dtype_code(grad_out), N, D, V, ldg,
+                             float(scale), _padding(padding_idx, V), _addr(grad_W),
+                             _dtype_code(grad_W), ldw, 1 if accumulate_grad_W else 0, _addr(ws),
+                             0 if ws is None else ws.numel(), _addr(status), _stream(dev))
     _abi.check(rc, "embedding_bwd")
     return grad_W
 
@@ -232,9 +238,9 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, mean=None,
     ldy = _matrix(y, "y")[2]
     mean = _output(mean, "mean", (N,), torch.float32, dev)
     rstd = _output(rstd, "rstd", (N,), torch.float32, dev)
-    rc = _abi.layer_norm_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _ptr(weight), _ptr(bias),
-                             wdt, float(eps), y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(),
-                             _stream(dev))
+    rc = _call.layer_norm_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _addr(weight), _addr(bias),
+                              wdt, float(eps), y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(),
+                              _stream(dev))
     _abi.check(rc, "layer_norm_fwd")
     return NormOut(y, mean, rstd)
 
@@ -247,8 +253,8 @@ def rms_norm_fwd(x, weight=None, eps=1e-5, *, y=None, rstd=None) -> NormOut:
     y = _output(y, "y", (N, D), x.dtype, dev)
     ldy = _matrix(y, "y")[2]
     rstd = _output(rstd, "rstd", (N,), torch.float32, dev)
-    rc = _abi.rms_norm_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _ptr(weight), wdt,
-                           float(eps), y.data_ptr(), ldy, rstd.data_ptr(), _stream(dev))
+    rc = _call.rms_norm_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _addr(weight), wdt,
+                            float(eps), y.data_ptr(), ldy, rstd.data_ptr(), _stream(dev))
     _abi.check(rc, "rms_norm_fwd")
     return NormOut(y, None, rstd)
 
@@ -292,10 +298,10 @@ def layer_norm_bwd(x, grad_y, mean, rstd, weight=None, *, want_grad_x=True,
     gx, ldgx, gw, gb, ws = _norm_bwd_args(x, N, D, grad_y, rstd, want_grad_x, want_w,
                                           want_grad_bias, grad_x, grad_weight, grad_bias,
                                           accumulate, ws)
-    rc = _abi.layer_norm_bwd(_ptr(x), _dtype_code(x), N, D, ldx, _ptr(grad_y), ldg, _ptr(weight),
-                             wdt, _ptr(mean), _ptr(rstd), _ptr(gx), ldgx, _ptr(gw), _ptr(gb),
-                             1 if accumulate else 0, _ptr(ws), 0 if ws is None else ws.numel(),
-                             _stream(x.device))
+    rc = _call.layer_norm_bwd(_addr(x), _dtype_code(x), N, D, ldx, _addr(grad_y), ldg,
+                              _addr(weight), wdt, _addr(mean), _addr(rstd), _addr(gx), ldgx, _addr(gw), _addr(gb),
+                              1 if accumulate else 0, _addr(ws), 0 if ws is None else ws.numel(),
+                              _stream(x.device))
     _abi.check(rc, "layer_norm_bwd")
     return NormGrads(gx, gw, gb)
 
@@ -309,9 +315,9 @@ def rms_norm_bwd(x, grad_y, rstd, weight=None, *, want_grad_x=True, want_grad_we
     want_w = weight is not None if want_grad_weight is None else want_grad_weight
     gx, ldgx, gw, _, ws = _norm_bwd_args(x, N, D, grad_y, rstd, want_grad_x, want_w, False,
                                          grad_x, grad_weight, None, accumulate, ws)
-    rc = _abi.rms_norm_bwd(_ptr(x), _dtype_code(x), N, D, ldx, _ptr(grad_y), ldg, _ptr(weight),
-                           wdt, _ptr(rstd), _ptr(gx), ldgx, _ptr(gw), 1 if accumulate else 0,
-                           _ptr(ws), 0 if ws is None else ws.numel(), _stream(x.device))
+    rc = _call.rms_norm_bwd(_addr(x), _dtype_code(x), N, D, ldx, _addr(grad_y), ldg, _addr(weight),
+                            wdt, _addr(rstd), _addr(gx), ldgx, _addr(gw), 1 if accumulate else 0,
+                            _addr(ws), 0 if ws is None else ws.numel(), _stream(x.device))
     _abi.check(rc, "rms_norm_bwd")
     return NormGrads(gx, gw, None)
 
@@ -418,8 +424,8 @@ def head4_quantize(W, group=128, *, zero_point=False, scale_dtype=None) -> Head4
                  torch.empty(V, G, dtype=torch.uint8, device=W.device) if zero_point else None,
                  D, group)
     ldp = head.packed.shape[1]
-    rc = _abi.head4_quantize(_ptr(W), _dtype_code(W), V, D, ldw, group, _ptr(head.packed), ldp,
-                             _ptr(head.scales), _dtype_code(head.scales), _ptr(head.zeros),
+    rc = _abi.head4_quantize(_addr(W), _dtype_code(W), V, D, ldw, group, _addr(head.packed), ldp,
+                             _addr(head.scales), _dtype_code(head.scales), _addr(head.zeros),
                              _stream(W.device))
     _abi.check(rc, "head4_quantize")
     return head
@@ -440,9 +446,9 @@ def head4_logits(x, head: Head4, bias=None, *, out=None,
     out = _output(out, "out", (M, V), out_dtype if out is None else out.dtype, dev)
     ldo = _matrix(out, "out")[2]
     dt = _dtype_code(x)
-    rc = _abi.head4_logits(x.data_ptr(), dt, M, D, ldx, head.packed.data_ptr(), ldp,
-                           head.scales.data_ptr(), _dtype_code(head.scales), _ptr(head.zeros),
-                           head.group, V, _ptr(bias), out.data_ptr(), _dtype_code(out), ldo,
-                           _ptr(status), _stream(dev))
+    rc = _call.head4_logits(x.data_ptr(), dt, M, D, ldx, head.packed.data_ptr(), ldp,
+                            head.scales.data_ptr(), _dtype_code(head.scales), _addr(head.zeros),
+                            head.group, V, _addr(bias), out.data_ptr(), _dtype_code(out), ldo,
+                            _addr(status), _stream(dev))
     _abi.check(rc, "head4_logits")
     return out

@@ -154,6 +154,15 @@ def test_quantize(lh, V, D, group, zero, dtype, sdt):
         assert ((y - W.float().cpu()).abs() <= step * 0.5 * (1 + 1e-6)).all()
 
 
+@pytest.mark.parametrize("D", [1, 7, 65, 127, 129, 250])
+def test_quantize_leaves_zeros_past_the_last_column(lh, D):
+    W = _randn((50, D), BF, 22)
+    for zero in (False, True):
+        h = lh.head4_quantize(W, 32, zero_point=zero)
+        every = R.unpack4(h.packed, h.packed.shape[1] * 2)
+        assert (every[:, D:] == 0).all() and (every[:, :D] != 0).any()
+
+
 @pytest.mark.parametrize("zero", [False, True])
 @pytest.mark.parametrize("dtype,group", [(F32, 32), (BF, 64), (F32, 128), (BF, 128)])
 def test_quantize_halves_and_extremes(lh, dtype, group, zero):

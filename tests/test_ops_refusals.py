@@ -160,3 +160,37 @@ def test_python_calls_refuse_on_the_device(abi):
                          accumulate_grad_W=True)
     with pytest.raises(lh.FlceError):  # rows that overlap
         lh.layer_norm_fwd(w.expand(4, 8))
+
+
+@no_gpu
+def test_arguments_from_memory_reach_their_places(abi):
+    """flce_call answers as the entry point does, with every argument wrong in turn."""
+    P = [A + (k << 28) for k in range(9)]
+    calls = {
+        "embedding_fwd": [P[0], P[1], 0, 4, 8, 10, 8, 1.0, P[2], 8, P[3], 0],
+        "embedding_bwd": [P[0], P[1], 0, 4, 8, 10, 8, 1.0, -1, P[2], 1, 8, 0, P[3], 1 << 20, P[4],
+                          0],
+        "layer_norm_fwd": [P[0], 0, 4, 8, 8, P[1], P[2], 0, 1e-5, P[3], 8, P[4], P[5], 0],
+        "rms_norm_fwd": [P[0], 0, 4, 8, 8, P[1], 0, 1e-5, P[2], 8, P[3], 0],
+        "layer_norm_bwd": [P[0], 0, 4, 8, 8, P[1], 8, P[2], 0, P[3], P[4], P[5], 8, P[6], P[7], 0,
+                           P[8], 1 << 20, 0],
+        "rms_norm_bwd": [P[0], 0, 4, 8, 8, P[1], 8, P[2], 0, P[3], P[4], 8, P[5], 0, P[6], 1 << 20,
+                         0],
+        "head4_logits": [P[0], 0, 2, 100, 100, P[1], 64, P[2], 0, P[3], 64, 10, P[4], P[5], 0, 10,
+                         P[6], 0]}
+    for name, good in calls.items():
+        types = abi._SIGNATURES[name][1]
+        assert len(types) == len(good), name
+        refused = 0
+        for k, t in enumerate(types[:-1]):  # (any stream is taken)
+            for bad in {abi._f: (2.0,), abi._p: (0, good[k] + 1)}.get(t, (-7, 1 << 40)):
+                if t is abi._i and bad > 9:
+                    bad = 9
+                args = good[:k] + [bad] + good[k + 1:]
+                want = getattr(abi, name)(*args)
+                assert getattr(abi.packed, name)(*args) == want < 0, (name, k, bad, want)
+                refused += want != -7  # not only the missing device
+        assert refused >= len(types)
+    call = abi.load().flce_call
+    assert call(99, bytes(96), 96) == ENOSUP
+    assert call(0, bytes(88), 88) == call(0, None, 96) == EINVAL
