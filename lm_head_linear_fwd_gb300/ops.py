@@ -61,6 +61,14 @@ def _matrix(t, name):
     return rows, cols, stride[0] if rows > 1 else cols
 
 
+def _row_stride(t, name, rows, cols):
+    """The row stride of a [rows, cols] output on the right device."""
+    stride = t.stride()
+    if stride[1] != 1 and cols > 1:
+        raise ValueError(f"{name} must be 2-D with unit stride along its rows")
+    return stride[0] if rows > 1 else cols
+
+
 def _rows_of(t):
     """t as the calls take it: unit column stride, rows that do not overlap."""
     ok = (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])
@@ -71,7 +79,7 @@ def _output(t, name, shape, dtype, device):
     """An optional caller-owned output, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device.index:
         raise ValueError(f"{name} must be {dtype} of shape {list(shape)} on {device}")
     if len(shape) == 1 and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -123,7 +131,7 @@ def embedding_fwd(ids, W, scale=1.0, *, out=None, status=None) -> torch.Tensor:
     ids, N = _ids(ids)
     dev = W.device
     out = _output(out, "out", (N, D), W.dtype, dev)
-    ldo = _matrix(out, "out")[2]
+    ldo = _row_stride(out, "out", N, D)
     status = status if status is not None else new_status(dev)
     rc = _call.embedding_fwd(ids.data_ptr(), W.data_ptr(), _dtype_code(W), N, D, V, ldw,
                              float(scale), out.data_ptr(), ldo, status.data_ptr(), _stream(dev))
@@ -235,7 +243,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, mean=None,
     wdt = _norm_params(D, weight, bias)
     dev = x.device
     y = _output(y, "y", (N, D), x.dtype, dev)
-    ldy = _matrix(y, "y")[2]
+    ldy = _row_stride(y, "y", N, D)
     mean = _output(mean, "mean", (N,), torch.float32, dev)
     rstd = _output(rstd, "rstd", (N,), torch.float32, dev)
     rc = _call.layer_norm_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _addr(weight), _addr(bias),
@@ -251,7 +259,7 @@ def rms_norm_fwd(x, weight=None, eps=1e-5, *, y=None, rstd=None) -> NormOut:
     wdt = _norm_params(D, weight, None)
     dev = x.device
     y = _output(y, "y", (N, D), x.dtype, dev)
-    ldy = _matrix(y, "y")[2]
+    ldy = _row_stride(y, "y", N, D)
     rstd = _output(rstd, "rstd", (N,), torch.float32, dev)
     rc = _call.rms_norm_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _addr(weight), wdt,
                             float(eps), y.data_ptr(), ldy, rstd.data_ptr(), _stream(dev))
@@ -444,7 +452,7 @@ def head4_logits(x, head: Head4, bias=None, *, out=None,
     _vector(bias, "bias", V, x.dtype)
     dev = x.device
     out = _output(out, "out", (M, V), out_dtype if out is None else out.dtype, dev)
-    ldo = _matrix(out, "out")[2]
+    ldo = _row_stride(out, "out", M, V)
     dt = _dtype_code(x)
     rc = _call.head4_logits(x.data_ptr(), dt, M, D, ldx, head.packed.data_ptr(), ldp,
                             head.scales.data_ptr(), _dtype_code(head.scales), _addr(head.zeros),
