@@ -117,7 +117,7 @@ def _padding(padding_idx, V):
 
 def _workspace(ws, nbytes, device):
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
     return ws
 
 
@@ -162,7 +162,7 @@ def embedding_bwd(ids, grad_out, V, scale=1.0, padding_idx=None, *, grad_W=None,
     if accumulate_grad_W and grad_W is None:
         raise ValueError("accumulate_grad_W needs grad_W")
     grad_W = _output(grad_W, "grad_W", (V, D), grad_dtype if grad_W is None else grad_W.dtype, dev)
-    ldw = _matrix(grad_W, "grad_W")[2]
+    ldw = _row_stride(grad_W, "grad_W", V, D)
     ws = _workspace(ws, embedding_bwd_workspace_bytes(N, D, V), dev)
     status = status if status is not None else new_status(dev)
     rc = _call.embedding_bwd(_addr(ids), _addr(grad_out), _dtype_code(grad_out), N, D, V, ldg,
@@ -267,6 +267,7 @@ def rms_norm_fwd(x, weight=None, eps=1e-5, *, y=None, rstd=None) -> NormOut:
     return NormOut(y, None, rstd)
 
 
+@functools.lru_cache(maxsize=256)
 def norm_bwd_workspace_bytes(N: int, D: int) -> int:
     """Bytes of device workspace layer_norm_bwd and rms_norm_bwd need."""
     return int(_abi.norm_bwd_workspace_bytes(N, D))
@@ -287,7 +288,7 @@ def _norm_bwd_args(x, N, D, grad_y, rstd, want_x, want_w, want_b, grad_x, grad_w
     gb = _output(grad_bias, "grad_bias", (D,), torch.float32, dev) if want_b else None
     if want_w or want_b:
         ws = _workspace(ws, norm_bwd_workspace_bytes(N, D), dev)
-    return gx, 0 if gx is None else _matrix(gx, "grad_x")[2], gw, gb, ws
+    return gx, 0 if gx is None else _row_stride(gx, "grad_x", N, D), gw, gb, ws
 
 
 def layer_norm_bwd(x, grad_y, mean, rstd, weight=None, *, want_grad_x=True,
@@ -307,7 +308,8 @@ def layer_norm_bwd(x, grad_y, mean, rstd, weight=None, *, want_grad_x=True,
                                           want_grad_bias, grad_x, grad_weight, grad_bias,
                                           accumulate, ws)
     rc = _call.layer_norm_bwd(_addr(x), _dtype_code(x), N, D, ldx, _addr(grad_y), ldg,
-                              _addr(weight), wdt, _addr(mean), _addr(rstd), _addr(gx), ldgx, _addr(gw), _addr(gb),
+                              _addr(weight), wdt, _addr(mean), _addr(rstd), _addr(gx), ldgx,
+                              _addr(gw), _addr(gb),
                               1 if accumulate else 0, _addr(ws), 0 if ws is None else ws.numel(),
                               _stream(x.device))
     _abi.check(rc, "layer_norm_bwd")
