@@ -264,6 +264,8 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
     }
     return;
   }
+  // the other CTAs' shared memory may be written once all of them have started
+  cluster_sync();
   for (int64_t k = rank * kSortThreads + tid; k < a.tickets; k += C * kSortThreads)
     a.ticket[k] = 0;
   const int R = 1 << a.bits;
