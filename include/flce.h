@@ -527,12 +527,20 @@ FLCE_API int rms_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64_t l
 
 /* x: [M, ldx] of dtype dt; bias: [V] of dtype dt or NULL; y: [M, ldy] of dtype
  * dt_y.  M == 0 is valid.  Made for M up to a few tens: the weights are read
- * again for every 32 bf16 (10 fp32) tokens.  status (may be NULL): set only if
- * a wait inside the kernel gave up (FLCE_ETIMEOUT). */
+ * again for every 32 bf16 (10 fp32) tokens.  A wait inside the kernel that gives
+ * up leaves NaN in the logits it was for and sets FLCE_ETIMEOUT in *status
+ * (status may be NULL). */
 FLCE_API int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t ldx,
                           const uint8_t* packed, int64_t ldp, const void* scales, int dt_s,
                           const uint8_t* zeros, int group, int64_t V, const void* bias, void* y,
                           int dt_y, int64_t ldy, int32_t* status, flce_stream_t stream);
+
+/* Self-test of that failure path: four warpgroups of one block wait as
+ * head4_logits does, the last one on a barrier that nothing completes.  After
+ * limit_ns (at most 2 s, else FLCE_ESHAPE) y[0..3] is 1, 1, 1, NaN and *status
+ * FLCE_ETIMEOUT; the context stays usable. */
+FLCE_API int head4_wait_selftest(float* y, int32_t* status, uint64_t limit_ns,
+                                 flce_stream_t stream);
 
 /* Rounds W [V, ldw] (dtype dt) to that layout.  Without zeros: scale =
  * max |w| / 7 of the group, q = clamp(round(w / scale), -8, 7) + 8.  With

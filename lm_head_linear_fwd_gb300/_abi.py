@@ -85,6 +85,7 @@ _SIGNATURES = {
     "head4_logits": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _p, _i, _i64, _p, _p, _i,
                           _i64, _p, _p]),
     "head4_quantize": (_i, [_p, _i, _i64, _i64, _i64, _i, _p, _i64, _p, _i, _p, _p]),
+    "head4_wait_selftest": (_i, [_p, _p, ctypes.c_uint64, _p]),
     "flce_call": (_i, [_i, ctypes.c_char_p, _sz]),
     "flce_gemm": (_i, [_i, _i, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _p]),
 }
@@ -205,3 +206,4 @@ layer_norm_bwd = _call("layer_norm_bwd")
 rms_norm_bwd = _call("rms_norm_bwd")
 head4_logits = _call("head4_logits")
 head4_quantize = _call("head4_quantize")
+head4_wait_selftest = _call("head4_wait_selftest")

@@ -348,3 +348,13 @@ extern "C" int head4_quantize(const void* W, int dt, int64_t V, int64_t D, int64
 #undef HEAD4_QUANTIZE
   return launch_status("head4_quantize_kernel launch");
 }
+
+extern "C" int head4_wait_selftest(float* y, int32_t* status, uint64_t limit_ns,
+                                   flce_stream_t stream) {
+  if (y == nullptr || status == nullptr) return FLCE_EINVAL;
+  if (!aligned(y, 4) || !aligned(status, 4)) return FLCE_EALIGN;
+  if (limit_ns > 2000000000ull) return FLCE_ESHAPE;
+  head4_wait_selftest_kernel<<<1, 32 * kWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      y, status, limit_ns);
+  return launch_status("head4_wait_selftest_kernel launch");
+}

@@ -71,6 +71,27 @@ __device__ __forceinline__ void tmem_add32(uint32_t taddr, float s, float (&acc)
   for (int i = 0; i < 32; ++i) acc[i] += s * __uint_as_float(r[i]);
 }
 
+// Waits for a phase by a whole warp, converged again afterwards (the tensor memory
+// instructions that follow are the warp's).  A wait that gives up says so in *failed
+// and leaves NaN in the sums, which stays there: no logit is wrong in silence.
+template <int N>
+__device__ __forceinline__ void wait_or_nan(uint64_t* bar, uint32_t parity, volatile int* failed,
+                                            float (&acc)[N], uint64_t limit_ns = kWaitLimitNs) {
+  const bool ok = mbar_wait(bar, parity, failed, limit_ns);
+  if (!__all_sync(0xffffffffu, ok)) {
+    *failed = 1;
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = __uint_as_float(0x7fffffffu);
+  }
+}
+
+// Whether a wait of any warp of the block gave up; for all threads, after their last
+// wait.
+__device__ __forceinline__ bool some_wait_failed(volatile int* failed) {
+  __syncthreads();
+  return *failed != 0;
+}
+
 // G32: 32-column pieces per group; ST: the scales' type.
 template <int G32, typename ST>
 __global__ void __launch_bounds__(32 * kWarps, 1)
@@ -133,7 +154,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   float later[kSums];   // scales of the sums that are still to be read
   // waits for the MMAs of the step before and adds up its sums
   auto add_sums = [&]() {
-    if (!mbar_wait(&done[group], (used - 1) & 1, failed)) *failed = 1;
+    wait_or_nan(&done[group], (used - 1) & 1, failed, acc);
     tc_fence_after();
 #pragma unroll
     for (int d = 0; d < kSums; ++d) tmem_add32(tm_d + d * N + my_lanes, later[d], acc);
@@ -255,13 +276,41 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     }
   }
   cp_async_wait<0>();
-  if (threadIdx.x == 0 && *failed) set_status(a.status, FLCE_ETIMEOUT);
   tc_fence_before();
-  __syncthreads();
+  if (some_wait_failed(failed)) {
+    // once more for the MMAs still under way, which read the memory freed below
+    if (used > 0) mbar_wait(&done[group], (used - 1) & 1, nullptr);
+    __syncthreads();
+    if (threadIdx.x == 0) set_status(a.status, FLCE_ETIMEOUT);
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem_base_sh, 512);
   }
+}
+
+// The same wait and report with an mbarrier per warpgroup, of which nothing completes
+// the last one's.  y[g] is what warpgroup g holds afterwards: 1, the last one NaN.
+__global__ void __launch_bounds__(32 * kWarps) head4_wait_selftest_kernel(float* y,
+                                                                          int32_t* status,
+                                                                          uint64_t limit_ns) {
+  constexpr int kGroups = kWarps / 4;
+  __shared__ __align__(8) uint64_t done[kGroups];
+  __shared__ int failed_sh;
+  volatile int* failed = &failed_sh;
+  const int group = threadIdx.x >> 7, in_group = threadIdx.x & 127;
+  if (threadIdx.x == 0) {
+    failed_sh = 0;
+    for (int g = 0; g < kGroups; ++g) mbar_init(&done[g], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (in_group == 0 && group + 1 < kGroups) mbar_arrive(&done[group]);
+  __syncwarp();
+  float acc[1] = {1.0f};
+  wait_or_nan(&done[group], 0, failed, acc, limit_ns);
+  if (in_group == 0) y[group] = acc[0];
+  if (some_wait_failed(failed) && threadIdx.x == 0) set_status(status, FLCE_ETIMEOUT);
 }
 
 }  // namespace flce

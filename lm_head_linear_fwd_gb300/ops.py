@@ -446,7 +446,8 @@ def head4_logits(x, head: Head4, bias=None, *, out=None,
     """Logits [M, V] of the hidden states x [M, D] (bf16 or fp32): x times the
     head's 4-bit weights transposed (+ bias [V], dtype of x).  Made for M up to
     a few tens (decoding); ``out`` (bf16 or fp32) or ``out_dtype`` sets the
-    logits' dtype.  ``status``: a word for a wait that gave up (new_status)."""
+    logits' dtype.  A wait inside the kernel that gives up leaves NaN in its
+    logits, and FLCE_ETIMEOUT in ``status`` (new_status), if given."""
     M, D, ldx = _matrix(x, "x")
     if D != head.D:
         raise ValueError(f"x must be [M, {head.D}]")

@@ -45,3 +45,16 @@ def test_cluster_has_started_before_its_shared_memory_is_used(name, body):
     syncs = [m.start() for m in re.finditer(r"cluster_sync\(\)", body)]
     assert syncs and syncs[0] < uses[0], name
     assert syncs[-1] > uses[-1], name
+
+
+def test_a_wait_that_gave_up_is_reported_after_the_last_one():
+    """head4_many_kernel: the flag is read for the report behind a barrier of the block
+    that all warps pass after their waits, and the tensor memory is freed after that."""
+    body = dict(KERNELS)["head4_many_kernel"]
+    reads = [m.start() for m in re.finditer(r"some_wait_failed\(failed\)", body)]
+    assert len(reads) == 1 and not re.search(r"[^a-z]\*failed\b", body.replace("int* failed", ""))
+    assert body.rindex("add_sums()") < reads[0]
+    assert reads[0] < body.index("set_status(a.status, FLCE_ETIMEOUT)") < body.index("tmem_dealloc(")
+    src = open(os.path.join(CSRC, "head4_many.cuh")).read()
+    helper = src[src.index("bool some_wait_failed"):]
+    assert helper.index("__syncthreads()") < helper.index("*failed != 0")
