@@ -432,7 +432,12 @@ FLCE_API int flce_grad_scale(void* x, int dt, int64_t n, const float* g, flce_st
  *   grad_W[v] (+)= scale * sum over i with ids[i] == v of grad_out[i],
  * which joins the head's grad_W when accumulated.  The source pages only name
  * the tied layout (Liger-Kernel issue #941); these calls have no counterpart
- * there, and neither do the norms and the 4-bit head below. */
+ * there, and neither do the norms and the 4-bit head below.
+ *
+ * Here and below two matrices overlap when their rows share a byte: column slices
+ * of one buffer do not, nor its even and odd rows.  With different row strides the
+ * check goes by their greatest common divisor and refuses (FLCE_EINVAL) what a
+ * multiple of it would let meet. */
 
 /* Lookup.  ids: [N] int64; W: [V, ldw], out: [N, ldo], both of dtype dt with
  * unit column stride (ldw, ldo >= D; any alignment of an element).  The

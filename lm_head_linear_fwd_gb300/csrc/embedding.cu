@@ -797,7 +797,7 @@ extern "C" int embedding_fwd(const int64_t* ids, const void* W, int dt, int64_t 
   if (rc != FLCE_OK) return rc;
   if (!aligned(ids, 8) || !aligned(status, 4)) return FLCE_EALIGN;
   const size_t es = dtype_size(dt);
-  if (overlap(W, span_bytes(V, D, ldw, es), out, span_bytes(N, D, ldo, es))) return FLCE_EINVAL;
+  if (overlap(Span(W, V, D, ldw, es), Span(out, N, D, ldo, es))) return FLCE_EINVAL;
   if (N == 0) return FLCE_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int vec = vec_width(0, W, dt, ldw, out, dt, ldo);
@@ -833,8 +833,8 @@ extern "C" int embedding_bwd(const int64_t* ids, const void* grad_out, int dt, i
   if (rc == FLCE_OK) rc = check_matrix(grad_W, dt_grad, V, D, ldw);
   if (rc != FLCE_OK) return rc;
   if (!aligned(ids, 8) || !aligned(status, 4)) return FLCE_EALIGN;
-  if (overlap(grad_out, span_bytes(N, D, ldg, dtype_size(dt)), grad_W,
-              span_bytes(V, D, ldw, dtype_size(dt_grad))))
+  if (overlap(Span(grad_out, N, D, ldg, dtype_size(dt)),
+              Span(grad_W, V, D, ldw, dtype_size(dt_grad))))
     return FLCE_EINVAL;
   const size_t need = embedding_bwd_workspace_bytes(N, D, V);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return FLCE_EWORKSPACE;

@@ -856,8 +856,7 @@ static int norm_fwd(NormArgs a, int dt, int wdt, flce_stream_t stream) {
       !aligned(a.mean, 4) || !aligned(a.rstd, 4))
     return FLCE_EALIGN;
   if (a.x == a.y ? a.ldx != a.ldy && a.N > 1
-                 : overlap(a.x, span_bytes(a.N, a.D, a.ldx, es), a.y,
-                           span_bytes(a.N, a.D, a.ldy, es)))
+                 : overlap(Span(a.x, a.N, a.D, a.ldx, es), Span(a.y, a.N, a.D, a.ldy, es)))
     return FLCE_EINVAL;
   if (a.N == 0) return FLCE_OK;
   a.w_f32 = wdt == FLCE_F32;
@@ -960,10 +959,10 @@ static int norm_bwd(NormBwdArgs a, int dt, int wdt, void* ws, size_t ws_bytes,
       !aligned(a.dw, 4) || !aligned(a.db, 4))
     return FLCE_EALIGN;
   if (a.dx != nullptr) {
-    const int64_t n = span_bytes(a.N, a.D, a.lddx, es);
-    if (overlap(a.x, span_bytes(a.N, a.D, a.ldx, es), a.dx, n)) return FLCE_EINVAL;
+    const Span dx(a.dx, a.N, a.D, a.lddx, es);
+    if (overlap(Span(a.x, a.N, a.D, a.ldx, es), dx)) return FLCE_EINVAL;
     if (a.dx == a.dy ? a.lddx != a.lddy && a.N > 1
-                     : overlap(a.dy, span_bytes(a.N, a.D, a.lddy, es), a.dx, n))
+                     : overlap(Span(a.dy, a.N, a.D, a.lddy, es), dx))
       return FLCE_EINVAL;
   }
   const bool cols = a.dw != nullptr || a.db != nullptr;

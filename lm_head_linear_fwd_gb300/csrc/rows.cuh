@@ -2,20 +2,38 @@
 // head4.cu): argument checks and element access.
 #pragma once
 
+#include <numeric>
+
 #include "common.cuh"
 #include "host.h"
 
 namespace flce {
 
-// Bytes from the first to the last element of a [rows, cols] matrix.
-inline int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, size_t es) {
-  return rows <= 0 ? 0 : ((rows - 1) * ld + cols) * static_cast<int64_t>(es);
-}
+// The bytes of a [rows, cols] matrix whose rows start ld elements of es bytes apart.
+struct Span {
+  uintptr_t p;
+  int64_t rows, row, step;  // bytes of a row, and from one to the next
+  Span(const void* base, int64_t rows, int64_t cols, int64_t ld, size_t es)
+      : p(reinterpret_cast<uintptr_t>(base)),
+        rows(base == nullptr ? 0 : rows),
+        row(cols * static_cast<int64_t>(es)),
+        step(rows > 1 ? ld * static_cast<int64_t>(es) : 0) {}
+  bool empty() const { return rows <= 0 || row <= 0; }
+  uintptr_t end() const { return p + static_cast<uintptr_t>((rows - 1) * step + row); }
+};
 
-inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) &&
-         y < x + static_cast<uintptr_t>(na);
+// Whether two matrices share a byte.  The distance from a row of b to a row of a is
+// a.p - b.p plus some multiple of g = gcd(a.step, b.step); rows meet where it lies
+// between -a.row and b.row.  Column slices of one buffer, and its even and odd rows,
+// are apart.  Exact for equal strides; different ones may count as meeting though
+// the rows that would are not there.
+inline bool overlap(const Span& a, const Span& b) {
+  if (a.empty() || b.empty() || a.p >= b.end() || b.p >= a.end()) return false;
+  const int64_t g = std::gcd(a.step, b.step);
+  if (g == 0) return true;  // one row each
+  const int64_t far = static_cast<int64_t>(a.p >= b.p ? a.p - b.p : b.p - a.p) % g;
+  const int64_t r = a.p >= b.p || far == 0 ? far : g - far;
+  return r < b.row || g - r < a.row;
 }
 
 // A [rows, cols] matrix argument: present when it has rows, element-aligned,
