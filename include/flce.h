@@ -531,7 +531,7 @@ FLCE_API int rms_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64_t l
  * their scales add up in fp32, in a fixed order. */
 
 /* x: [M, ldx] of dtype dt; bias: [V] of dtype dt or NULL; y: [M, ldy] of dtype
- * dt_y.  M == 0 is valid.  Made for M up to a few tens: the weights are read
+ * dt_y, which overlaps no input.  M == 0 is valid.  Made for M up to a few tens: the weights are read
  * again for every 32 bf16 (10 fp32) tokens.  A wait inside the kernel that gives
  * up leaves NaN in the logits it was for and sets FLCE_ETIMEOUT in *status
  * (status may be NULL). */
@@ -553,7 +553,7 @@ FLCE_API int head4_wait_selftest(float* y, int32_t* status, uint64_t limit_ns,
  * z = round(-min / scale), q = clamp(round(w / scale) + z, 0, 15).  The scale
  * is rounded to dt_s first and q formed with the rounded one; round is to the
  * nearest, ties to even.  A group of zeros has scale 1.  Padding columns hold q = 0.
- * W must be finite. */
+ * W must be finite.  packed, scales and zeros overlap neither W nor each other. */
 FLCE_API int head4_quantize(const void* W, int dt, int64_t V, int64_t D, int64_t ldw, int group,
                             uint8_t* packed, int64_t ldp, void* scales, int dt_s, uint8_t* zeros,
                             flce_stream_t stream);

@@ -271,6 +271,19 @@ static int check_head4(const void* packed, int64_t ldp, const void* scales, int 
   return FLCE_OK;
 }
 
+// The parts of a head: what head4_logits reads and head4_quantize writes.
+struct HeadSpans {
+  Span packed, scales, zeros;
+  HeadSpans(const void* packed, int64_t ldp, const void* scales, int dt_s, const void* zeros,
+            int group, int64_t V, int64_t D)
+      : packed(packed, V, (D + 127) / 128 * 64, ldp, 1),
+        scales(scales, 1, V * ((D + group - 1) / group), 0, dtype_size(dt_s)),
+        zeros(zeros, 1, V * ((D + group - 1) / group), 0, 1) {}
+  bool meet(const Span& s) const {
+    return overlap(packed, s) || overlap(scales, s) || overlap(zeros, s);
+  }
+};
+
 }  // namespace flce
 
 using namespace flce;
@@ -286,6 +299,11 @@ extern "C" int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t
   if (rc == FLCE_OK) rc = check_matrix(y, dt_y, M, V, ldy);
   if (rc != FLCE_OK) return rc;
   if (!aligned(bias, dtype_size(dt)) || !aligned(status, 4)) return FLCE_EALIGN;
+  const Span out(y, M, V, ldy, dtype_size(dt_y));
+  if (HeadSpans(packed, ldp, scales, dt_s, zeros, group, V, D).meet(out) ||
+      overlap(Span(x, M, D, ldx, dtype_size(dt)), out) ||
+      overlap(Span(bias, 1, V, 0, dtype_size(dt)), out))
+    return FLCE_EINVAL;
   if (M == 0) return FLCE_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Head4Args a{};
@@ -323,6 +341,10 @@ extern "C" int head4_quantize(const void* W, int dt, int64_t V, int64_t D, int64
   int rc = check_head4(packed, ldp, scales, dt_s, group, V, D);
   if (rc == FLCE_OK) rc = check_matrix(W, dt, V, D, ldw);
   if (rc != FLCE_OK) return rc;
+  const HeadSpans to(packed, ldp, scales, dt_s, zeros, group, V, D);
+  if (to.meet(Span(W, V, D, ldw, dtype_size(dt))) || overlap(to.packed, to.scales) ||
+      overlap(to.packed, to.zeros) || overlap(to.scales, to.zeros))
+    return FLCE_EINVAL;
   const Quant4Args a{W, V, D, ldw, group, packed, ldp, scales, zeros, (D + group - 1) / group};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t blocks = (D + 127) / 128;

@@ -87,6 +87,46 @@ def test_against_bytes_marked_one_by_one(abi):
     assert min(seen.values()) > 500
 
 
+@no_gpu
+def test_head4_outputs_lie_apart_from_inputs(abi):
+    V, D, M, group = 40, 200, 3, 64
+    G, ldp = 4, 128
+    P = [A + (k << 24) for k in range(6)]
+
+    def logits(**kw):
+        a = dict(x=P[0], dt=0, M=M, D=D, ldx=D, packed=P[1], ldp=ldp, scales=P[2], dts=1,
+                 zeros=P[3], group=group, V=V, bias=P[4], y=P[5], dty=1, ldy=V, status=None,
+                 stream=None)
+        assert set(kw) <= set(a)
+        return abi.head4_logits(*dict(a, **kw).values())
+
+    assert logits() == ECUDA
+    n = 4 * M * V
+    ends = {"x": 2 * M * D, "packed": V * ldp, "scales": 4 * V * G, "zeros": V * G, "bias": 2 * V}
+    for k, (name, size) in enumerate(ends.items()):
+        step = 16 if name == "packed" else 4
+        for at in (P[5] - size + step, P[5], P[5] + n - step):
+            assert logits(**{name: at}) == EINVAL, (name, at)
+        for at in (P[5] - (size + step - 1) // step * step, P[5] + n):
+            assert logits(**{name: at}) == ECUDA, (name, at)
+    # x and y as slices of the columns of one buffer
+    assert logits(x=P[5] + 2 * 80, ldx=300, ldy=300, dty=0) == ECUDA
+    assert logits(x=P[5] + 2 * 39, ldx=300, ldy=300, dty=0) == EINVAL
+    assert logits(M=0, x=P[5]) == 0
+
+    def quantize(**kw):
+        a = dict(W=P[0], dt=0, V=V, D=D, ldw=D, group=group, packed=P[1], ldp=ldp, scales=P[2],
+                 dts=1, zeros=P[3], stream=None)
+        assert set(kw) <= set(a)
+        return abi.head4_quantize(*dict(a, **kw).values())
+
+    assert quantize() == quantize(zeros=None) == ECUDA
+    for kw in (dict(packed=P[0]), dict(scales=P[0] + 2 * V * D - 4), dict(zeros=P[0] + 1),
+               dict(scales=P[1]), dict(zeros=P[1] + V * ldp - 1), dict(zeros=P[2])):
+        assert quantize(**kw) == EINVAL, kw
+    assert quantize(scales=P[0] + 2 * V * D) == quantize(zeros=P[1] + V * ldp) == ECUDA
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("D,gap", [(64, 0), (37, 0), (201, 3), (1600, 1)])
