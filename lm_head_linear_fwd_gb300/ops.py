@@ -51,9 +51,19 @@ def _addr(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _matrix(t, name):
+def _on(t, name, device):
+    """t lies on `device` (a tensor elsewhere has another index, on the host -1)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device.index:
+        _cuda(t, name)
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _matrix(t, name, device=None):
     """A CUDA [rows, cols] argument with unit column stride: rows, cols, row stride."""
-    _cuda(t, name)
+    if device is None:
+        _cuda(t, name)
+    else:
+        _on(t, name, device)
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be 2-D with unit stride along its rows")
@@ -86,11 +96,11 @@ def _output(t, name, shape, dtype, device):
     return t
 
 
-def _vector(t, name, n, dtype=None):
+def _vector(t, name, n, device, dtype=None):
     """An optional contiguous [n] argument."""
     if t is None:
         return None
-    _cuda(t, name)
+    _on(t, name, device)
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{n}] tensor")
     if dtype is not None and t.dtype is not dtype:
@@ -98,8 +108,8 @@ def _vector(t, name, n, dtype=None):
     return t
 
 
-def _ids(ids):
-    _cuda(ids, "ids")
+def _ids(ids, device):
+    _on(ids, "ids", device)
     shape = ids.shape
     if ids.dtype is not torch.int64 or len(shape) != 1:
         raise ValueError("ids must be int64 of shape [N]")
@@ -116,9 +126,24 @@ def _padding(padding_idx, V):
 
 
 def _workspace(ws, nbytes, device):
+    """The caller's workspace or a new one, and its bytes."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
-    return ws
+        return (torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes) if nbytes > 0 \
+            else (None, 0)
+    _on(ws, "ws", device)
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _status(status, device):
+    """The caller's status word or a new one."""
+    if status is None:
+        return new_status(device)
+    _on(status, "status", device)
+    if status.dtype is not torch.int32 or status.numel() < 1:
+        raise ValueError("status must be an int32 word (new_status)")
+    return status
 
 
 # ------------------------------------------------------------------ embedding
@@ -128,11 +153,11 @@ def embedding_fwd(ids, W, scale=1.0, *, out=None, status=None) -> torch.Tensor:
     row stride free).  An id outside [0, V) gives a row of zeros and sets
     ``status`` (FLCE_ELABEL).  ``out``/``status`` let a caller reuse buffers."""
     V, D, ldw = _matrix(W, "W")
-    ids, N = _ids(ids)
     dev = W.device
+    ids, N = _ids(ids, dev)
     out = _output(out, "out", (N, D), W.dtype, dev)
     ldo = _row_stride(out, "out", N, D)
-    status = status if status is not None else new_status(dev)
+    status = _status(status, dev)
     rc = _call.embedding_fwd(ids.data_ptr(), W.data_ptr(), _dtype_code(W), N, D, V, ldw,
                              float(scale), out.data_ptr(), ldo, status.data_ptr(), _stream(dev))
     _abi.check(rc, "embedding_fwd")
@@ -154,21 +179,21 @@ def embedding_bwd(ids, grad_out, V, scale=1.0, padding_idx=None, *, grad_W=None,
     ``accumulate_grad_W`` added to the fp32 ``grad_W``, whose other rows are
     not touched.  Tokens with id ``padding_idx`` are left out."""
     N, D, ldg = _matrix(grad_out, "grad_out")
-    ids, n = _ids(ids)
+    dev = grad_out.device
+    ids, n = _ids(ids, dev)
     if n != N:
         raise ValueError(f"ids must be int64 of shape [{N}]")
     V = int(V)
-    dev = grad_out.device
     if accumulate_grad_W and grad_W is None:
         raise ValueError("accumulate_grad_W needs grad_W")
     grad_W = _output(grad_W, "grad_W", (V, D), grad_dtype if grad_W is None else grad_W.dtype, dev)
     ldw = _row_stride(grad_W, "grad_W", V, D)
-    ws = _workspace(ws, embedding_bwd_workspace_bytes(N, D, V), dev)
-    status = status if status is not None else new_status(dev)
+    ws, ws_bytes = _workspace(ws, embedding_bwd_workspace_bytes(N, D, V), dev)
+    status = _status(status, dev)
     rc = _call.embedding_bwd(_addr(ids), _addr(grad_out), _dtype_code(grad_out), N, D, V, ldg,
                              float(scale), _padding(padding_idx, V), _addr(grad_W),
                              _dtype_code(grad_W), ldw, 1 if accumulate_grad_W else 0, _addr(ws),
-                             0 if ws is None else ws.numel(), _addr(status), _stream(dev))
+                             ws_bytes, _addr(status), _stream(dev))
     _abi.check(rc, "embedding_bwd")
     return grad_W
 
@@ -225,9 +250,9 @@ class NormGrads:
     grad_bias: Optional[torch.Tensor]    # fp32
 
 
-def _norm_params(D, weight, bias):
-    _vector(weight, "weight", D)
-    _vector(bias, "bias", D)
+def _norm_params(D, weight, bias, device):
+    _vector(weight, "weight", D, device)
+    _vector(bias, "bias", D, device)
     if weight is not None and bias is not None and weight.dtype is not bias.dtype:
         raise TypeError("weight and bias must share one dtype")
     p = weight if weight is not None else bias
@@ -240,8 +265,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, mean=None,
     weight and bias [D] (each optional, bf16 or fp32).  Returns y (dtype of x;
     ``y`` may be x itself) and the fp32 mean and rstd the backward needs."""
     N, D, ldx = _matrix(x, "x")
-    wdt = _norm_params(D, weight, bias)
     dev = x.device
+    wdt = _norm_params(D, weight, bias, dev)
     y = _output(y, "y", (N, D), x.dtype, dev)
     ldy = _row_stride(y, "y", N, D)
     mean = _output(mean, "mean", (N,), torch.float32, dev)
@@ -256,8 +281,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, *, y=None, mean=None,
 def rms_norm_fwd(x, weight=None, eps=1e-5, *, y=None, rstd=None) -> NormOut:
     """RMS norm of the rows of x [N, D]: layer norm without the mean and bias."""
     N, D, ldx = _matrix(x, "x")
-    wdt = _norm_params(D, weight, None)
     dev = x.device
+    wdt = _norm_params(D, weight, None, dev)
     y = _output(y, "y", (N, D), x.dtype, dev)
     ldy = _row_stride(y, "y", N, D)
     rstd = _output(rstd, "rstd", (N,), torch.float32, dev)
@@ -278,7 +303,7 @@ def _norm_bwd_args(x, N, D, grad_y, rstd, want_x, want_w, want_b, grad_x, grad_w
     dev = x.device
     if grad_y.shape != (N, D) or grad_y.dtype is not x.dtype:
         raise ValueError("grad_y must have the shape and dtype of x")
-    _vector(rstd, "rstd", N, torch.float32)
+    _vector(rstd, "rstd", N, dev, torch.float32)
     if rstd is None:
         raise ValueError("rstd must be given")
     if accumulate and ((want_w and grad_weight is None) or (want_b and grad_bias is None)):
@@ -286,9 +311,9 @@ def _norm_bwd_args(x, N, D, grad_y, rstd, want_x, want_w, want_b, grad_x, grad_w
     gx = _output(grad_x, "grad_x", (N, D), x.dtype, dev) if want_x else None
     gw = _output(grad_weight, "grad_weight", (D,), torch.float32, dev) if want_w else None
     gb = _output(grad_bias, "grad_bias", (D,), torch.float32, dev) if want_b else None
-    if want_w or want_b:
-        ws = _workspace(ws, norm_bwd_workspace_bytes(N, D), dev)
-    return gx, 0 if gx is None else _row_stride(gx, "grad_x", N, D), gw, gb, ws
+    ws, ws_bytes = _workspace(ws, norm_bwd_workspace_bytes(N, D), dev) if want_w or want_b \
+        else (None, 0)
+    return gx, 0 if gx is None else _row_stride(gx, "grad_x", N, D), gw, gb, ws, ws_bytes
 
 
 def layer_norm_bwd(x, grad_y, mean, rstd, weight=None, *, want_grad_x=True,
@@ -298,20 +323,19 @@ def layer_norm_bwd(x, grad_y, mean, rstd, weight=None, *, want_grad_x=True,
     grad_y: grad_x (dtype of x; ``grad_x`` may be grad_y itself), grad_weight
     and grad_bias (fp32; added to the given ones when ``accumulate``)."""
     N, D, ldx = _matrix(x, "x")
-    ldg = _matrix(grad_y, "grad_y")[2]
-    wdt = _norm_params(D, weight, None)
+    ldg = _matrix(grad_y, "grad_y", x.device)[2]
+    wdt = _norm_params(D, weight, None, x.device)
     if mean is None:
         raise ValueError("mean must be given")
-    _vector(mean, "mean", N, torch.float32)
+    _vector(mean, "mean", N, x.device, torch.float32)
     want_w = weight is not None if want_grad_weight is None else want_grad_weight
-    gx, ldgx, gw, gb, ws = _norm_bwd_args(x, N, D, grad_y, rstd, want_grad_x, want_w,
-                                          want_grad_bias, grad_x, grad_weight, grad_bias,
-                                          accumulate, ws)
+    gx, ldgx, gw, gb, ws, ws_bytes = _norm_bwd_args(x, N, D, grad_y, rstd, want_grad_x, want_w,
+                                                    want_grad_bias, grad_x, grad_weight, grad_bias,
+                                                    accumulate, ws)
     rc = _call.layer_norm_bwd(_addr(x), _dtype_code(x), N, D, ldx, _addr(grad_y), ldg,
                               _addr(weight), wdt, _addr(mean), _addr(rstd), _addr(gx), ldgx,
                               _addr(gw), _addr(gb),
-                              1 if accumulate else 0, _addr(ws), 0 if ws is None else ws.numel(),
-                              _stream(x.device))
+                              1 if accumulate else 0, _addr(ws), ws_bytes, _stream(x.device))
     _abi.check(rc, "layer_norm_bwd")
     return NormGrads(gx, gw, gb)
 
@@ -320,14 +344,14 @@ def rms_norm_bwd(x, grad_y, rstd, weight=None, *, want_grad_x=True, want_grad_we
                  grad_x=None, grad_weight=None, accumulate=False, ws=None) -> NormGrads:
     """Gradients of rms_norm_fwd (see layer_norm_bwd)."""
     N, D, ldx = _matrix(x, "x")
-    ldg = _matrix(grad_y, "grad_y")[2]
-    wdt = _norm_params(D, weight, None)
+    ldg = _matrix(grad_y, "grad_y", x.device)[2]
+    wdt = _norm_params(D, weight, None, x.device)
     want_w = weight is not None if want_grad_weight is None else want_grad_weight
-    gx, ldgx, gw, _, ws = _norm_bwd_args(x, N, D, grad_y, rstd, want_grad_x, want_w, False,
-                                         grad_x, grad_weight, None, accumulate, ws)
+    gx, ldgx, gw, _, ws, ws_bytes = _norm_bwd_args(x, N, D, grad_y, rstd, want_grad_x, want_w,
+                                                   False, grad_x, grad_weight, None, accumulate, ws)
     rc = _call.rms_norm_bwd(_addr(x), _dtype_code(x), N, D, ldx, _addr(grad_y), ldg, _addr(weight),
                             wdt, _addr(rstd), _addr(gx), ldgx, _addr(gw), 1 if accumulate else 0,
-                            _addr(ws), 0 if ws is None else ws.numel(), _stream(x.device))
+                            _addr(ws), ws_bytes, _stream(x.device))
     _abi.check(rc, "rms_norm_bwd")
     return NormGrads(gx, gw, None)
 
@@ -403,16 +427,18 @@ class Head4:
         return self.packed.shape[0]
 
 
-def _head4_args(head):
-    V, width, ldp = _matrix(head.packed, "packed")
+def _head4_args(head, device):
+    V, width, ldp = _matrix(head.packed, "packed", device)
+    if head.group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
     if width < (head.D + 127) // 128 * 64:
         raise ValueError("packed must hold ceil(D / 128) * 64 bytes per row")
     shape = (V, -(-head.D // head.group))
-    _cuda(head.scales, "scales")
+    _on(head.scales, "scales", device)
     if head.scales.shape != shape or not head.scales.is_contiguous():
         raise ValueError(f"scales must be a contiguous {list(shape)} tensor")
     if head.zeros is not None:
-        _cuda(head.zeros, "zeros")
+        _on(head.zeros, "zeros", device)
         if head.zeros.shape != shape or not head.zeros.is_contiguous():
             raise ValueError(f"zeros must be a contiguous {list(shape)} tensor")
     if head.packed.dtype is not torch.uint8 or \
@@ -451,9 +477,11 @@ def head4_logits(x, head: Head4, bias=None, *, out=None,
     M, D, ldx = _matrix(x, "x")
     if D != head.D:
         raise ValueError(f"x must be [M, {head.D}]")
-    V, ldp = _head4_args(head)
-    _vector(bias, "bias", V, x.dtype)
     dev = x.device
+    V, ldp = _head4_args(head, dev)
+    _vector(bias, "bias", V, dev, x.dtype)
+    if status is not None:
+        _status(status, dev)
     out = _output(out, "out", (M, V), out_dtype if out is None else out.dtype, dev)
     ldo = _row_stride(out, "out", M, V)
     dt = _dtype_code(x)
