@@ -7,6 +7,8 @@ import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
+                            reason="fake tensors of two GPUs; on a machine without one only")
 pytestmark = pytest.mark.filterwarnings("ignore:Accessing the data pointer of FakeTensor")
 
 
@@ -65,6 +67,7 @@ OPS = ["embedding_fwd", "embedding_bwd", "layer_norm_fwd", "rms_norm_fwd", "laye
        "rms_norm_bwd", "head4_logits"]
 
 
+@no_gpu
 @pytest.mark.parametrize("op", OPS)
 def test_every_tensor_lies_on_the_same_gpu(ops, op):
     good = _args(op)
@@ -78,6 +81,7 @@ def test_every_tensor_lies_on_the_same_gpu(ops, op):
     assert len(ops._call.reached) == 1
 
 
+@no_gpu
 @pytest.mark.parametrize("op", ["embedding_fwd", "embedding_bwd", "head4_logits"])
 def test_status_is_a_word(ops, op):
     good = _args(op)
@@ -91,6 +95,7 @@ def test_status_is_a_word(ops, op):
     assert ops._call.reached
 
 
+@no_gpu
 @pytest.mark.parametrize("op", ["embedding_bwd", "layer_norm_bwd", "rms_norm_bwd"])
 def test_workspace_counts_in_bytes(ops, op):
     good = _args(op)
@@ -101,8 +106,31 @@ def test_workspace_counts_in_bytes(ops, op):
         assert nbytes in ops._call.reached.pop()[1]
 
 
+@no_gpu
 def test_group_of_a_head(ops):
     for group in (0, -64, 48, 256):
         with pytest.raises(ValueError):
             _call(ops, "head4_logits", _args("head4_logits"), group=group)
     assert not ops._call.reached
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", OPS)
+def test_host_tensors_beside_device_ones(op):
+    from lm_head_linear_fwd_gb300 import ops
+    good, host = _args(op, "cuda"), _args(op, "cpu")
+    if "ids" in good:
+        good["ids"].fill_(V - 1)
+    if "ws" in good:  # what these sizes need
+        need = ops.embedding_bwd_workspace_bytes(N, D, V) if op == "embedding_bwd" \
+            else ops.norm_bwd_workspace_bytes(N, D)
+        good["ws"] = torch.zeros(-(-need // 4), device="cuda")
+    _call(ops, op, good)
+    for name in good:
+        with pytest.raises(ValueError):
+            _call(ops, op, dict(good, **{name: host[name]}))
+    if "status" in good:
+        with pytest.raises(ValueError):
+            _call(ops, op, dict(good, status=torch.zeros(1, dtype=torch.int64, device="cuda")))
+    _call(ops, op, good)
+    torch.cuda.synchronize()
