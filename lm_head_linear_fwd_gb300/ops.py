@@ -5,7 +5,7 @@ buffers optional):
     embedding_fwd, embedding_bwd, layer_norm_fwd, layer_norm_bwd,
     rms_norm_fwd, rms_norm_bwd, head4_quantize, head4_logits
 Autograd front ends:
-    embedding(ids, W, *, scale=1.0, padding_idx=None)
+    embedding(ids, W, *, scale=1.0, padding_idx=None, status=None)
     layer_norm(x, weight=None, bias=None, *, eps=1e-5)
     rms_norm(x, weight=None, *, eps=1e-5)
 
@@ -151,7 +151,8 @@ def _status(status, device):
 def embedding_fwd(ids, W, scale=1.0, *, out=None, status=None) -> torch.Tensor:
     """out[i] = scale * W[ids[i]] for ids [N] int64 and W [V, D] (bf16 or fp32,
     row stride free).  An id outside [0, V) gives a row of zeros and sets
-    ``status`` (FLCE_ELABEL).  ``out``/``status`` let a caller reuse buffers."""
+    ``status`` (FLCE_ELABEL; a word of the caller's, else nobody can read it).
+    ``out``/``status`` let a caller reuse buffers."""
     V, D, ldw = _matrix(W, "W")
     dev = W.device
     ids, N = _ids(ids, dev)
@@ -200,8 +201,9 @@ def embedding_bwd(ids, grad_out, V, scale=1.0, padding_idx=None, *, grad_W=None,
 
 class _Embedding(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, ids, W, scale, padding_idx):
-        status = new_status(W.device) if isinstance(W, torch.Tensor) and W.is_cuda else None
+    def forward(ctx, ids, W, scale, padding_idx, status):
+        if status is None and W.is_cuda:
+            status = new_status(W.device)
         out = embedding_fwd(ids, W, scale, status=status)
         ctx.save_for_backward(ids)
         ctx.args = (W.shape[0], W.dtype, scale, padding_idx)
@@ -215,20 +217,22 @@ class _Embedding(torch.autograd.Function):
         V, dtype, scale, padding_idx = ctx.args
         gW = embedding_bwd(ids, _rows_of(g), V, scale, padding_idx, grad_dtype=dtype,
                            status=ctx.status)
-        return None, gW, None, None
+        return None, gW, None, None, None
 
 
-def embedding(ids, W, *, scale=1.0, padding_idx=None):
+def embedding(ids, W, *, scale=1.0, padding_idx=None, status=None):
     """Embedding lookup scale * W[ids] with ids [...] int64, W [V, D]; returns
     [..., D].  The backward forms the dense gradient of W in W's dtype (one
     rounding of the fp32 sums); ids equal to ``padding_idx`` leave their row's
-    gradient 0."""
+    gradient 0.  An id outside [0, V) gives a row of zeros and no gradient; both
+    passes say so in ``status`` (new_status, read by check_status), if given:
+    without it such ids go unseen."""
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("W must be 2-D")
     if not isinstance(ids, torch.Tensor):
         raise ValueError("ids must be an int64 tensor")
     _padding(padding_idx, W.shape[0])
-    out = _Embedding.apply(ids.reshape(-1), W, float(scale), padding_idx)
+    out = _Embedding.apply(ids.reshape(-1), W, float(scale), padding_idx, status)
     return out.view(*ids.shape, W.shape[1])
 
 
