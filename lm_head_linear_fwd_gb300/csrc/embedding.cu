@@ -496,7 +496,7 @@ static int reduce_threads(int64_t D) { return D <= 32 * kReduceLane ? 32 : 128; 
 static ReducePlan reduce_plan(int64_t N, int64_t D) {
   const int64_t tile = reduce_threads(D) * kReduceLane;
   const int64_t tiles = (D + tile - 1) / tile;
-  const int64_t wave = 152 * 24 * 32 / reduce_threads(D);
+  const int64_t wave = int64_t(sm_count()) * 24 * 32 / reduce_threads(D);
   int64_t chunk = std::max<int64_t>(kMinChunk, (N * tiles + wave - 1) / wave);
   while (chunk < kMaxChunk && chunk * chunk < N / 8) ++chunk;
   chunk = std::min<int64_t>(kMaxChunk, (chunk + kReduceAhead - 1) / kReduceAhead * kReduceAhead);

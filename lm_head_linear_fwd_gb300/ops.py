@@ -125,9 +125,17 @@ def _padding(padding_idx, V):
     return p
 
 
-def _workspace(ws, nbytes, device):
+@functools.lru_cache(maxsize=512)
+def _workspace_bytes(query, device_index, *sizes):
+    """A workspace query's answer for a device: the plans go by its SMs."""
+    with torch.cuda.device(device_index):
+        return query(*sizes)
+
+
+def _workspace(ws, device, query, *sizes):
     """The caller's workspace or a new one, and its bytes."""
     if ws is None:
+        nbytes = _workspace_bytes(query, device.index, *sizes)
         return (torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes) if nbytes > 0 \
             else (None, 0)
     _on(ws, "ws", device)
@@ -165,9 +173,8 @@ def embedding_fwd(ids, W, scale=1.0, *, out=None, status=None) -> torch.Tensor:
     return out
 
 
-@functools.lru_cache(maxsize=256)
 def embedding_bwd_workspace_bytes(N: int, D: int, V: int) -> int:
-    """Bytes of device workspace embedding_bwd needs."""
+    """Bytes of device workspace embedding_bwd needs on the current device."""
     return int(_abi.embedding_bwd_workspace_bytes(N, D, V))
 
 
@@ -189,7 +196,7 @@ def embedding_bwd(ids, grad_out, V, scale=1.0, padding_idx=None, *, grad_W=None,
         raise ValueError("accumulate_grad_W needs grad_W")
     grad_W = _output(grad_W, "grad_W", (V, D), grad_dtype if grad_W is None else grad_W.dtype, dev)
     ldw = _row_stride(grad_W, "grad_W", V, D)
-    ws, ws_bytes = _workspace(ws, embedding_bwd_workspace_bytes(N, D, V), dev)
+    ws, ws_bytes = _workspace(ws, dev, embedding_bwd_workspace_bytes, N, D, V)
     status = _status(status, dev)
     rc = _call.embedding_bwd(_addr(ids), _addr(grad_out), _dtype_code(grad_out), N, D, V, ldg,
                              float(scale), _padding(padding_idx, V), _addr(grad_W),
@@ -296,9 +303,9 @@ def rms_norm_fwd(x, weight=None, eps=1e-5, *, y=None, rstd=None) -> NormOut:
     return NormOut(y, None, rstd)
 
 
-@functools.lru_cache(maxsize=256)
 def norm_bwd_workspace_bytes(N: int, D: int) -> int:
-    """Bytes of device workspace layer_norm_bwd and rms_norm_bwd need."""
+    """Bytes of device workspace layer_norm_bwd and rms_norm_bwd need on the current
+    device."""
     return int(_abi.norm_bwd_workspace_bytes(N, D))
 
 
@@ -315,7 +322,7 @@ def _norm_bwd_args(x, N, D, grad_y, rstd, want_x, want_w, want_b, grad_x, grad_w
     gx = _output(grad_x, "grad_x", (N, D), x.dtype, dev) if want_x else None
     gw = _output(grad_weight, "grad_weight", (D,), torch.float32, dev) if want_w else None
     gb = _output(grad_bias, "grad_bias", (D,), torch.float32, dev) if want_b else None
-    ws, ws_bytes = _workspace(ws, norm_bwd_workspace_bytes(N, D), dev) if want_w or want_b \
+    ws, ws_bytes = _workspace(ws, dev, norm_bwd_workspace_bytes, N, D) if want_w or want_b \
         else (None, 0)
     return gx, 0 if gx is None else _row_stride(gx, "grad_x", N, D), gw, gb, ws, ws_bytes
 

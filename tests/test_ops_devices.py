@@ -1,6 +1,7 @@
 """Arguments of another device, type or layout than a call needs are refused before
 their address is taken.  Fake tensors stand in for those of two GPUs; a call whose
 checks all pass ends at a stand-in for the library."""
+import contextlib
 import types
 
 import pytest
@@ -25,6 +26,7 @@ def ops(monkeypatch):
     monkeypatch.setattr(m, "_stream", lambda device: 0)
     monkeypatch.setattr(m, "embedding_bwd_workspace_bytes", lambda *a: 4096)
     monkeypatch.setattr(m, "norm_bwd_workspace_bytes", lambda *a: 4096)
+    monkeypatch.setattr(torch.cuda, "device", lambda index: contextlib.nullcontext())
     with FakeTensorMode():
         yield m
 
@@ -112,6 +114,31 @@ def test_group_of_a_head(ops):
         with pytest.raises(ValueError):
             _call(ops, "head4_logits", _args("head4_logits"), group=group)
     assert not ops._call.reached
+
+
+@no_gpu
+@pytest.mark.parametrize("op", ["embedding_bwd", "layer_norm_bwd", "rms_norm_bwd"])
+def test_workspace_is_asked_for_on_the_tensors_device(ops, op, monkeypatch):
+    """A device's answer is not another's: they differ in SMs."""
+    current, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(index):
+        old, current[0] = current[0], index
+        yield
+        current[0] = old
+
+    def query(*sizes):
+        asked.append(current[0])
+        return 1000 + current[0]
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(ops, "embedding_bwd_workspace_bytes", query)
+    monkeypatch.setattr(ops, "norm_bwd_workspace_bytes", query)
+    for index in (1, 0, 1, 0):
+        _call(ops, op, dict(_args(op, f"cuda:{index}"), ws=None))
+        assert 1000 + index in ops._call.reached[-1][1], index
+    assert sorted(asked) == [0, 1]  # once for each
 
 
 @pytest.mark.gpu
