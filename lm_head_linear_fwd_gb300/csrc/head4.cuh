@@ -8,7 +8,8 @@
 // A word's nibble pairs (p, p + 4) become bf16 pairs by putting the nibble into the
 // mantissa of 128: 128 + q, and one fused multiply-add to (q - z) 2^-11, both
 // exact.  The power of two keeps a group's sum (up to 128 * 15 |x|) within fp32
-// for any x; the scales carry its inverse.
+// for any x.  Its inverse comes last, with the bias: a scale times 2^11 could pass
+// fp32's range.
 #pragma once
 
 #include "rows.cuh"
@@ -277,20 +278,22 @@ struct RowStream {
       enter_scales();
     }
   }
-  // 2^11 times the scale of group gi of the stage
+  // the scale of group gi of the stage
   static __device__ __forceinline__ float scale_of(const uint32_t (&sc)[SW], int gi) {
-    if constexpr (SPW == 1) return 2048.0f * __uint_as_float(sc[gi]);
-    return 2048.0f * ((gi & 1) ? bf16_hi(sc[gi / 2]) : bf16_lo(sc[gi / 2]));
+    if constexpr (SPW == 1) return __uint_as_float(sc[gi]);
+    return (gi & 1) ? bf16_hi(sc[gi / 2]) : bf16_lo(sc[gi / 2]);
   }
 };
 
-// Logit of token m and row v from its sum, plus the row's bias.
+// The bias of row v; the logit of token m and row v from its sum and the bias.
 __device__ __forceinline__ float head4_bias(const Head4Args& a, int64_t v) {
   if (a.bias == nullptr) return 0.0f;
   return a.x_f32 ? static_cast<const float*>(a.bias)[v]
                  : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.bias) + v);
 }
-__device__ __forceinline__ void head4_put(const Head4Args& a, int64_t v, int m, float logit) {
+__device__ __forceinline__ void head4_put(const Head4Args& a, int64_t v, int m, float sum,
+                                          float bias) {
+  const float logit = __fmaf_rn(sum, 2048.0f, bias);  // sum: 2^-11 times the products'
   const int64_t at = m * a.ldy + v;
   if (a.y_f32)
     static_cast<float*>(a.y)[at] = logit;

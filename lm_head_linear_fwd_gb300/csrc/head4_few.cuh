@@ -153,8 +153,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                   } else {
                     sl = bf16_lo(s_lo[r]), sh = bf16_lo(s_hi[r]);
                   }
-                  sl *= 2048.0f;
-                  sh *= 2048.0f;
 #pragma unroll
                   for (int n = 0; n < NT; ++n) {
                     acc[r][n][0] += part[r][n][0] * sl;
@@ -200,7 +198,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     }
     if (!real) continue;
     auto put = [&](int64_t v, int m, float sum) {
-      if (v < a.V && m < a.M) head4_put(a, v, m, sum + head4_bias(a, v));
+      if (v < a.V && m < a.M) head4_put(a, v, m, sum, head4_bias(a, v));
     };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
