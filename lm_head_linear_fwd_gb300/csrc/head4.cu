@@ -201,7 +201,11 @@ __global__ void __launch_bounds__(256) head4_quantize_kernel(Quant4Args a) {
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
       }
-      s = round_to(__fdiv_rn(hi - lo, 15.0f), static_cast<const S*>(nullptr));
+      // (the range itself may pass fp32's; half of it does not)
+      const float range = __fadd_rn(hi, -lo);
+      s = range <= 3.40282347e38f ? __fdiv_rn(range, 15.0f)
+                                  : __fdiv_rn(__fadd_rn(0.5f * hi, -0.5f * lo), 7.5f);
+      s = round_to(s, static_cast<const S*>(nullptr));
       if (s == 0.0f) s = 1.0f;
       z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
     } else {
