@@ -125,3 +125,20 @@ def test_more_rows_than_a_block_marks_at_once(lh, N):
     lh.embedding_bwd(ids, dy, V, 1.0, grad_W=gW)
     ref, bound = R.embedding_grad(ids, dy, V, 1.0, None, None, F32)
     R.close(gW, ref, bound)
+
+
+def test_places_lie_within_the_list(lh, monkeypatch):
+    """The checked build looks at every place that a token is put at: none leaves the
+    list, and the bits are those of the ordinary build, for both ways to order tokens."""
+    from lm_head_linear_fwd_gb300 import _abi, build
+    ordinary, checked = _abi.load(), _abi.open_library(build.build(checked=True))
+    for N, kind in ((300, "uniform"), (5000, "heavy"), (20001, "bad"), (40000, "heavy")):
+        V, D = 1500, 8
+        ids, dy = _ids(N, V, 11, kind), _rows(N, D, BF, 12)
+        got = []
+        for lib in (ordinary, checked):
+            monkeypatch.setattr(_abi, "_lib", lib)
+            st = lh.new_status("cuda")
+            got.append(lh.embedding_bwd(ids, dy, V, 1.0, 3, status=st))
+            assert int(st.item()) == (-5 if kind == "bad" else 0)
+        assert torch.equal(*got)
