@@ -515,7 +515,6 @@ struct ReduceArgs {
   int64_t chunks, tiles;
   float* part;      // [chunks][2][tiles][threads of a block][kReduceLane]
   int32_t* ticket;  // [chunks][tiles]
-  int32_t* status;
 };
 
 // First chunk of the run of id v that chunk c begins inside (the one whose
@@ -887,7 +886,6 @@ extern "C" int embedding_bwd(const int64_t* ids, const void* grad_out, int dt, i
   ra.tiles = plan.tiles;
   ra.ticket = sa.ticket;
   ra.part = reinterpret_cast<float*>(base + 2 * w.buf + w.ticket);
-  ra.status = status;
   const int vec = vec_width(D, grad_out, dt, ldg, grad_W, dt_grad, ldw);
   using B = __nv_bfloat16;
   if (dt == FLCE_BF16)

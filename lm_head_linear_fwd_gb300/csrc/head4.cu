@@ -1,29 +1,13 @@
 // The head with 4-bit weights and group scales: logits of a few tokens, and
 // the rounding of a table to that layout.
 #include <algorithm>
-#include <atomic>
 
 #include "head4_few.cuh"
 #include "head4_many.cuh"
 
 namespace flce {
 
-constexpr int kSmemMost = 226 * 1024;
-
-// The kernel's limit on shared memory, raised once per device and kernel.
-template <typename K>
-static int raise_smem(K* kernel, std::atomic<uint64_t>& raised) {
-  int dev = 0;
-  int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
-  if (rc != FLCE_OK) return rc;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (raised.load() & bit) return FLCE_OK;
-  rc = cuda_status(
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost),
-      "cudaFuncSetAttribute(head4 kernel)");
-  if (rc == FLCE_OK) raised.fetch_or(bit);
-  return rc;
-}
+constexpr int kSmemMost = 226 * 1024;  // beside a few static words
 
 // Tiles of `rows` rows, and how many of a block's `units` share one; at most `fit`
 // stages of the tokens stand in shared memory.
@@ -41,7 +25,7 @@ static int plan_head4(Head4Args& a, int rows, int units, int64_t fit) {
 template <int G32, typename ST, int NT>
 static int launch_few(Head4Args a, cudaStream_t s) {
   static std::atomic<uint64_t> raised{0};
-  const int rc = raise_smem(head4_few_kernel<G32, ST, NT>, raised);
+  const int rc = raise_smem(head4_few_kernel<G32, ST, NT>, kSmemMost, raised);
   if (rc != FLCE_OK) return rc;
   const int64_t fit = ((kSmemMost - kRing) / a.cols - kXPad) / (2 * kStageCols);
   const int grid = plan_head4(a, 32, kWarps, fit);
@@ -53,7 +37,7 @@ static int launch_few(Head4Args a, cudaStream_t s) {
 template <int G32, typename ST>
 static int launch_many(Head4Args a, cudaStream_t s) {
   static std::atomic<uint64_t> raised{0};
-  const int rc = raise_smem(head4_many_kernel<G32, ST>, raised);
+  const int rc = raise_smem(head4_many_kernel<G32, ST>, kSmemMost, raised);
   if (rc != FLCE_OK) return rc;
   constexpr int kStageX = kManyCols * kStageCols * 2;
   const int grid = plan_head4(a, 128, kWarps / 4, (kSmemMost - kRing - 1024) / kStageX);

@@ -19,7 +19,6 @@
 // Bytes of a block outside the row are neither used nor written; a block with one
 // byte of the row lies within mapped memory as a whole.
 #include <algorithm>
-#include <atomic>
 
 #include "rows.cuh"
 
@@ -34,7 +33,7 @@ template <typename T>
 constexpr int kFwdThreads = sizeof(T) == 2 ? 640 : 512;
 template <int kElems>
 constexpr int kBwdThreads = kElems == 8 ? 640 : 512;
-constexpr int kSmemMost = 224 * 1024;
+constexpr int kSmemMost = 224 * 1024;  // beside the static sums of a team
 
 // How a row is spread: `team` threads to a row (a power of two up to a warp,
 // then whole warps), `teams` rows at a time in a block.
@@ -171,17 +170,6 @@ __device__ __forceinline__ uint4 bytes_from(const uint4& lo, const uint4& hi, in
   }
 }
 
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A thread's places for one row in shared memory: vector k at k * blockDim * 16;
 // kWhole = false: after them, for each thread without a right neighbour in its
 // warp, the blocks after its own.
@@ -209,7 +197,7 @@ struct RowCopy {
     if (kWhole) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (k < t.mine) copy16(to + k * pitch, p + k * t.size * 16);
+        if (k < t.mine) cp_async16(to + k * pitch, p + k * t.size * 16);
     } else {
       const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
       const int last = (off + D * static_cast<int>(sizeof(T)) - 1) / 16;  // the row's last block
@@ -217,9 +205,9 @@ struct RowCopy {
       const uint32_t to_end = smem_u32(end);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (t.at(k) <= last) copy16(to + k * pitch, from + k * t.size * 16);
+        if (t.at(k) <= last) cp_async16(to + k * pitch, from + k * t.size * 16);
         if (t.last && t.at(k) < last)
-          copy16(to_end + k * end_pitch, from + k * t.size * 16 + 16);
+          cp_async16(to_end + k * end_pitch, from + k * t.size * 16 + 16);
       }
     }
   }
@@ -402,7 +390,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
     copy[r].clear(false, team);
     if (r < rows) copy[r].start(x.p + r * x.step, D, team);
   }
-  copies_commit();
+  cp_async_commit();
   const float4* bias = weights + nvec * (VEC / 4);
   stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
   if (kCenter) stage_weights<VEC>(weights + nvec * (VEC / 4), a.bias, a.w_f32, 0.0f, D);
@@ -410,7 +398,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
   const float inv_n = 1.0f / static_cast<float>(D);
   for (; turns > 0; turns -= kRows, rows -= kRows) {
     float2 f[kRows][NV][P];
-    copies_wait<0>();
+    cp_async_wait<0>();
     if (!kWhole) __syncwarp();  // the right neighbour's blocks
 #pragma unroll
     for (int r = 0; r < kRows; ++r) copy[r].read(x.p + r * x.step, D, team, f[r]);
@@ -419,7 +407,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
       if (kRows + r < rows) copy[r].start(x.p + r * x.step, D, team);
-    copies_commit();
+    cp_async_commit();
     // sums: a chain of additions for each place in a vector
     float mean[2] = {};
     if (kCenter) {
@@ -496,7 +484,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
     if (!kCenter && a.team > 32) named_barrier(1 + team.id, a.team);  // the sums' places
   }
   if (!staged) __syncthreads();  // warps without a row
-  copies_wait<0>();
+  cp_async_wait<0>();
 }
 
 struct NormBwdArgs {
@@ -562,7 +550,7 @@ __global__ void __launch_bounds__(kBwdThreads<kElems>) norm_bwd_kernel(NormBwdAr
       f.g.clear(true, team);
       f.rstd = f.mean = 0.0f;
     }
-    copies_commit();
+    cp_async_commit();
   };
   even.x.clear(false, team);
   even.g.clear(false, team);
@@ -579,7 +567,7 @@ __global__ void __launch_bounds__(kBwdThreads<kElems>) norm_bwd_kernel(NormBwdAr
   auto turn = [&](Ahead& f, int parity) {
     const float mean = f.mean, rstd = f.rstd;
     float2 h[NV][P], u[NV][P];
-    copies_wait<kAhead - 1>();
+    cp_async_wait<kAhead - 1>();
     if (!kWhole) __syncwarp();  // the right neighbour's blocks
     f.x.read(x.p, D, team, h);
     f.g.read(dy.p, D, team, u);
@@ -637,7 +625,7 @@ __global__ void __launch_bounds__(kBwdThreads<kElems>) norm_bwd_kernel(NormBwdAr
   } else {
     for (; turns > 0; --turns, --rows) turn(even, turns & 1);
   }
-  copies_wait<0>();
+  cp_async_wait<0>();
   if (a.part == nullptr) return;
   float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.D;
   // the teams' sums side by side, then in team order
@@ -795,28 +783,12 @@ static bool whole(int dt, const void* p, int64_t ld) {
 // A weight vector in shared memory, to whole row vectors.
 static size_t weight_bytes(int64_t D) { return round_up(static_cast<size_t>(D), 8) * 4; }
 
-// Allows a kernel kSmemMost bytes of shared memory, once per device.
-template <typename K>
-static int raise_smem(K kern, std::atomic<uint64_t>& raised) {
-  int dev = 0;
-  int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
-  if (rc != FLCE_OK) return rc;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(raised.load() & bit)) {
-    rc = cuda_status(
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost),
-        "cudaFuncSetAttribute(norm kernel)");
-    if (rc == FLCE_OK) raised.fetch_or(bit);
-  }
-  return rc;
-}
-
 // Launches norm_fwd_kernel; returns 1 (nothing launched) when a row does not fit.
 template <typename T, bool kWhole, bool kCenter, int kElems, int kRows>
 static int launch_norm_fwd_k(NormArgs a, cudaStream_t s) {
   if (a.D > int64_t(kFwdThreads<T>) * kElems) return 1;
   static std::atomic<uint64_t> raised{0};
-  const int rc = raise_smem(norm_fwd_kernel<T, kWhole, kCenter, kElems, kRows>, raised);
+  const int rc = raise_smem(norm_fwd_kernel<T, kWhole, kCenter, kElems, kRows>, kSmemMost, raised);
   if (rc != FLCE_OK) return rc;
   const NormPlan p = norm_plan(a.N, a.D, kElems, kFwdThreads<T>);
   a.team = p.team;
@@ -891,7 +863,7 @@ static int64_t bwd_slices(int64_t N, int64_t D) {
 template <typename T, bool kWhole, bool kCenter, int kElems, int kAhead>
 static int launch_norm_bwd_k(NormBwdArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> raised{0};
-  const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, kElems, kAhead>, raised);
+  const int rc = raise_smem(norm_bwd_kernel<T, kWhole, kCenter, kElems, kAhead>, kSmemMost, raised);
   if (rc != FLCE_OK) return rc;
   const NormPlan p = bwd_plan(a.N, a.D, kElems);
   a.team = p.team;

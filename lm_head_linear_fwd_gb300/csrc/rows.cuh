@@ -2,6 +2,7 @@
 // head4.cu): argument checks and element access.
 #pragma once
 
+#include <atomic>
 #include <numeric>
 
 #include "common.cuh"
@@ -44,6 +45,37 @@ inline int check_matrix(const void* p, int dt, int64_t rows, int64_t cols, int64
   if (rows > 0 && ld > (int64_t(1) << 60) / rows) return FLCE_ESHAPE;
   if (!aligned(p, dtype_size(dt))) return FLCE_EALIGN;
   return FLCE_OK;
+}
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device.
+template <typename K>
+inline int raise_smem(K* kernel, int bytes, std::atomic<uint64_t>& raised) {
+  int dev = 0;
+  int rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc != FLCE_OK) return rc;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (raised.load() & bit) return FLCE_OK;
+  rc = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+                   "cudaFuncSetAttribute(shared memory of a kernel)");
+  if (rc == FLCE_OK) raised.fetch_or(bit);
+  return rc;
+}
+
+// Asynchronous copies of 16 bytes to shared memory; !valid: zeros instead.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // VEC consecutive elements of T in fp32, loaded and stored as one access of
@@ -92,10 +124,6 @@ struct RawVec {
       static_assert(VEC * sizeof(T) == 2, "16, 4 or 2 bytes");
       w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) w[k] = 0u;
   }
   __device__ __forceinline__ void unpack(float (&x)[VEC]) const {
 #pragma unroll

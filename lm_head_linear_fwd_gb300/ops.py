@@ -109,7 +109,8 @@ def _vector(t, name, n, device, dtype=None):
 
 
 def _ids(ids, device):
-    _on(ids, "ids", device)
+    if not isinstance(ids, torch.Tensor) or ids.get_device() != device.index:
+        _on(ids, "ids", device)
     shape = ids.shape
     if ids.dtype is not torch.int64 or len(shape) != 1:
         raise ValueError("ids must be int64 of shape [N]")
@@ -148,9 +149,9 @@ def _status(status, device):
     """The caller's status word or a new one."""
     if status is None:
         return new_status(device)
-    _on(status, "status", device)
-    if status.dtype is not torch.int32 or status.numel() < 1:
-        raise ValueError("status must be an int32 word (new_status)")
+    if not isinstance(status, torch.Tensor) or status.get_device() != device.index or \
+            status.dtype is not torch.int32 or status.numel() < 1:
+        raise ValueError(f"status must be an int32 word on {device} (new_status)")
     return status
 
 
