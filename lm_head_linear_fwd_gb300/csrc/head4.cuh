@@ -9,7 +9,7 @@
 // mantissa of 128: 128 + q, and one fused multiply-add to (q - z) 2^-11, both
 // exact.  The power of two keeps a group's sum (up to 128 * 15 |x|) within fp32
 // for any x.  Its inverse comes last, with the bias: a scale times 2^11 could pass
-// fp32's range.
+// fp32's range.  (Logits below 2^-115 keep their bits down to 2^-138.)
 #pragma once
 
 #include "rows.cuh"
@@ -270,15 +270,15 @@ struct RowStream {
   }
 };
 
-// The bias of row v; the logit of token m and row v from its sum and the bias.
+// The bias of row v; the logit of token m and row v: its sum times `unit`, and the bias.
 __device__ __forceinline__ float head4_bias(const Head4Args& a, int64_t v) {
   if (a.bias == nullptr) return 0.0f;
   return a.x_f32 ? static_cast<const float*>(a.bias)[v]
                  : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(a.bias) + v);
 }
 __device__ __forceinline__ void head4_put(const Head4Args& a, int64_t v, int m, float sum,
-                                          float bias) {
-  const float logit = __fmaf_rn(sum, 2048.0f, bias);  // sum: 2^-11 times the products'
+                                          float unit, float bias) {
+  const float logit = __fmaf_rn(sum, unit, bias);
   const int64_t at = m * a.ldy + v;
   if (a.y_f32)
     static_cast<float*>(a.y)[at] = logit;

@@ -44,6 +44,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   using Rows = RowStream<G32, ST, 32>;
   constexpr int SPW = Rows::SPW, SW = Rows::SW, ZW = Rows::ZW;
   constexpr int R = 2;  // the instruction's 16 rows in a warp's 32
+  // The scales times a power of two that cannot overflow, where the product makes for
+  // better code: 16 tokens on 128256 x 4096 in groups of 128 take 99.3 us with it and
+  // 103.3 without, 32 in groups of 32 219.8 and 222; one in groups of 32 with zero
+  // points 80.3 and 75.9.
+  constexpr float kHalf = NT > 1 ? 0.5f : 1.0f;
   extern __shared__ __align__(128) char smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -153,6 +158,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
                   } else {
                     sl = bf16_lo(s_lo[r]), sh = bf16_lo(s_hi[r]);
                   }
+                  sl *= kHalf;
+                  sh *= kHalf;
 #pragma unroll
                   for (int n = 0; n < NT; ++n) {
                     acc[r][n][0] += part[r][n][0] * sl;
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     }
     if (!real) continue;
     auto put = [&](int64_t v, int m, float sum) {
-      if (v < a.V && m < a.M) head4_put(a, v, m, sum, head4_bias(a, v));
+      if (v < a.V && m < a.M) head4_put(a, v, m, sum, 2048.0f / kHalf, head4_bias(a, v));
     };
 #pragma unroll
     for (int r = 0; r < R; ++r) {

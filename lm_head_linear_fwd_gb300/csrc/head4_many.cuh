@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     if (v >= a.V) continue;
     const float bias = head4_bias(a, v);
     auto put = [&](int m, float sum) {
-      if (m < a.M) head4_put(a, v, m, sum, bias);
+      if (m < a.M) head4_put(a, v, m, sum, 2048.0f, bias);
     };
     if (!a.x_f32) {
 #pragma unroll
