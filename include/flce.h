@@ -456,7 +456,9 @@ FLCE_API size_t embedding_bwd_workspace_bytes(int64_t N, int64_t D, int64_t V);
  * with accumulate_grad_W != 0, rows that ids name are added to and the others
  * left untouched.  Sums run in fp32 over the tokens of an id in a fixed order
  * (two identical calls give identical bits) and are rounded once; adding to a
- * FLCE_BF16 grad_W would round at every call and returns FLCE_ENOSUP.
+ * FLCE_BF16 grad_W would round at every call and returns FLCE_ENOSUP.  The
+ * addition is the memory's own, which takes subnormal numbers (below 2^-126) and
+ * results for 0.
  * Tokens with id == padding_idx contribute nothing (their grad_out is not
  * used); pass -1 for none.  Ids outside [0, V) contribute nothing and set
  * FLCE_ELABEL.  Requires N < 2^31.  ws: embedding_bwd_workspace_bytes bytes,
@@ -473,8 +475,10 @@ FLCE_API int embedding_bwd(const int64_t* ids, const void* grad_out, int dt, int
  *   mean = (1/D) sum_j x_j,  rstd = 1 / sqrt((1/D) sum_j (x_j - mean)^2 + eps)
  *   h_j = (x_j - mean) rstd,  y_j = h_j weight_j + bias_j
  * (rms_norm_*: mean = 0, no bias).  The sum of squares is taken around the
- * mean in a second pass over the row (held on chip), so a mean far from 0
- * costs no digits.  Backward, with u_j = grad_y_j weight_j:
+ * mean in a second pass over the row (held on chip), so a mean far from 0 does
+ * not cancel in it.  The mean itself is one fp32 value: it is off by 2^-24 |mean|
+ * and more, and y by that times rstd.  A row whose mean square passes fp32's range
+ * (|x| from about 2^63 on) gets rstd 0.  Backward, with u_j = grad_y_j weight_j:
  *   grad_x_j = rstd (u_j - (1/D) sum u - h_j (1/D) sum u h)
  *   grad_weight_j = sum over rows of grad_y_j h_j,  grad_bias_j = sum of grad_y_j
  * (rms_norm_*: without the (1/D) sum u term).  All sums in fp32, in a fixed
@@ -527,14 +531,15 @@ FLCE_API int rms_norm_bwd(const void* x, int dt, int64_t N, int64_t D, int64_t l
  *   group   32, 64 or 128 columns
  * The products q x are summed within a group by tensor-core instructions with
  * fp32 accumulation: (q - z) and bf16 x are exact there, and fp32 x is split
- * into three bf16 parts that add up to it exactly.  The groups' sums times
- * their scales add up in fp32, in a fixed order. */
+ * into three bf16 parts that add up to it exactly (where |x| is below 2^-110, up
+ * to 2^-133).  The groups' sums times their scales add up in fp32, in a fixed
+ * order; scales may have any finite value. */
 
 /* x: [M, ldx] of dtype dt; bias: [V] of dtype dt or NULL; y: [M, ldy] of dtype
- * dt_y, which overlaps no input.  M == 0 is valid.  Made for M up to a few tens: the weights are read
- * again for every 32 bf16 (10 fp32) tokens.  A wait inside the kernel that gives
- * up leaves NaN in the logits it was for and sets FLCE_ETIMEOUT in *status
- * (status may be NULL). */
+ * dt_y, which overlaps no input.  M == 0 is valid.  Made for M up to a few tens:
+ * the weights are read again for every 32 bf16 (10 fp32) tokens.  A wait inside
+ * the kernel that gives up leaves NaN in the logits it was for and sets
+ * FLCE_ETIMEOUT in *status (status may be NULL). */
 FLCE_API int head4_logits(const void* x, int dt, int64_t M, int64_t D, int64_t ldx,
                           const uint8_t* packed, int64_t ldp, const void* scales, int dt_s,
                           const uint8_t* zeros, int group, int64_t V, const void* bias, void* y,

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(SortArgs a
 // Bound by the look-ups' instructions on every SM: 8192 tokens take 8 us.  The work
 // grows with N times the bisection's steps, the cluster's sort with N alone but it
 // starts higher: gradients (added) of 8192 x 4096 with this 43.8 us, with the sort
-// 56.2; of 16384 x 1024 33.6 and 37.9; of 32768 x 1024 56.7 and 52.4.
+// 56.2; of 16384 x 1024 33.6 and 37.9; of 32768 x 1024 56.7 and 52.8.
 constexpr int kRankShare = 128;
 constexpr int kRankAhead = 4;  // ids a thread looks up together
 
@@ -491,8 +491,9 @@ struct ReducePlan {
 static int reduce_threads(int64_t D) { return D <= 32 * kReduceLane ? 32 : 128; }
 
 // One wave of blocks (24 warps to an SM) while a chunk stays within kMaxChunk
-// tokens, and no chunk shorter than sqrt(N / 8) tokens: a run over an eighth of
-// all tokens is then joined from as many partial sums as a chunk has tokens.
+// tokens, and no chunk shorter than sqrt(N / 8) tokens while that is within
+// kMaxChunk too: up to 131072 tokens a run over an eighth of them is joined from no
+// more partial sums than a chunk has tokens, beyond that from N / 1024.
 static ReducePlan reduce_plan(int64_t N, int64_t D) {
   const int64_t tile = reduce_threads(D) * kReduceLane;
   const int64_t tiles = (D + tile - 1) / tile;

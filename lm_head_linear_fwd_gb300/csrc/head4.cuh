@@ -60,7 +60,8 @@ __device__ __forceinline__ uint32_t unpack_pair(uint32_t word, uint32_t minus_z)
 // Columns [k0, k0 + chunk) of the tokens to shared memory as bf16, zeros from D on:
 // columns 8 j .. 8 j + 7 of a row to *place(row, j).  An fp32 value becomes three
 // rows: its upper 16 bits, the upper 16 bits of what is left, and the rest (each at
-// most 8 significant bits: exact).
+// most 8 significant bits: exact where the last part's are above 2^-133, so for |x|
+// from 2^-110 on; the bits below are cut).
 template <typename Place>
 __device__ __forceinline__ void stage_tokens(const Head4Args& a, int64_t k0, const Place& place) {
   const int per = static_cast<int>(a.chunk / 8);

@@ -11,10 +11,12 @@
 // columns 32 w .. 32 w + 31, so each pair of instructions stays within 32 columns and
 // any group of 32, 64 or 128 columns can be scaled on its own.
 //
-// One token on 128256 x 4096 with groups of 128 takes 58.8 us (4.6 TB/s of weights),
-// with groups of 32 and zero points 80; two instructions' rows to each of 16 warps
+// One token on 128256 x 4096 with groups of 128 takes 58.5 us (4.6 TB/s of weights),
+// with groups of 32 and zero points 76; two instructions' rows to each of 16 warps
 // (four to each of 8: 61 and 102).  The instruction's rate bounds more columns: 8
-// token columns cost about 45 us there, 16 tokens take 100 us and 32 would take 192.
+// token columns cost about 45 us there, 16 tokens take 99 us and 32 would take 192.
+// At 128 registers 16 columns spill 8 to 40 bytes, 8 with groups of 32 8 to 24, and 32
+// with groups of 32 208 to 216.
 #pragma once
 
 #include "head4.cuh"

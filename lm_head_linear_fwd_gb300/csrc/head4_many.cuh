@@ -9,12 +9,13 @@
 // their sums in order.
 //
 // Bound by the chain of a step (unpack, store, barrier, products, sums), which the
-// other three warpgroups of the SM fill in part: 132 us for 32 tokens on 128256 x
+// other three warpgroups of the SM fill in part: 133 us for 32 tokens on 128256 x
 // 4096 with groups of 128 (2.0 TB/s of weights), 185 us on 151936 x 5120 with groups
-// of 64.  So it waits rarely and stays within 128 registers: steps of 64 columns with
-// two A's took 140 and 211 us, the sums read after the next step's first unpacking
-// (whose registers then spill) 154 and 234, the products issued one step late, with
-// no barrier but an mbarrier, 151 and 252.
+// of 64.  So it waits rarely and keeps to the 128 registers that 512 threads have, but
+// for 12 to 20 bytes that the compiler spills: steps of 64 columns with two A's took
+// 140 and 211 us, the sums read after the next step's first unpacking (which spills
+// much more) 154 and 234, the products issued one step late, with no barrier but an
+// mbarrier, 151 and 252; the wait below without the warp's vote 133 and 199.
 #pragma once
 
 #include "head4.cuh"
