@@ -34,6 +34,7 @@ from .api import _cuda, _dtype_code, new_status
 from .api import _stream as _stream_of
 
 _call = _abi.packed
+_Tensor, _INT32, _INT64 = torch.Tensor, torch.int32, torch.int64
 
 # A call on a few tokens costs less on the device than its checks here, so these
 # ask a tensor for each property once.  The stream's handle comes from the same
@@ -53,7 +54,7 @@ def _addr(t):
 
 def _on(t, name, device):
     """t lies on `device` (a tensor elsewhere has another index, on the host -1)."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device.index:
+    if not isinstance(t, _Tensor) or t.get_device() != device.index:
         _cuda(t, name)
         raise ValueError(f"{name} must be on {device}")
 
@@ -109,10 +110,10 @@ def _vector(t, name, n, device, dtype=None):
 
 
 def _ids(ids, device):
-    if not isinstance(ids, torch.Tensor) or ids.get_device() != device.index:
+    if not isinstance(ids, _Tensor) or ids.get_device() != device.index:
         _on(ids, "ids", device)
     shape = ids.shape
-    if ids.dtype is not torch.int64 or len(shape) != 1:
+    if ids.dtype is not _INT64 or len(shape) != 1:
         raise ValueError("ids must be int64 of shape [N]")
     return ids.contiguous(), shape[0]
 
@@ -139,18 +140,17 @@ def _workspace(ws, device, query, *sizes):
         nbytes = _workspace_bytes(query, device.index, *sizes)
         return (torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes) if nbytes > 0 \
             else (None, 0)
-    _on(ws, "ws", device)
-    if not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    return ws, ws.numel() * ws.element_size()
+    if not isinstance(ws, _Tensor) or ws.get_device() != device.index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
+    return ws, ws.nbytes
 
 
 def _status(status, device):
     """The caller's status word or a new one."""
     if status is None:
         return new_status(device)
-    if not isinstance(status, torch.Tensor) or status.get_device() != device.index or \
-            status.dtype is not torch.int32 or status.numel() < 1:
+    if not isinstance(status, _Tensor) or status.get_device() != device.index or \
+            status.dtype is not _INT32 or status.numel() < 1:
         raise ValueError(f"status must be an int32 word on {device} (new_status)")
     return status
 
