@@ -563,6 +563,119 @@ FLCE_API int head4_quantize(const void* W, int dt, int64_t V, int64_t D, int64_t
                             uint8_t* packed, int64_t ldp, void* scales, int dt_s, uint8_t* zeros,
                             flce_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Matrices in 8 bits, and the norm that writes them                        */
+/* ------------------------------------------------------------------------ */
+/* A matrix [R, K] in 8 bits has
+ *   q       [R, ldq] bytes, e4m3 numbers (1 sign, 4 exponent and 3 significand
+ *           bits, largest 448, NaN 0x7f); ldq >= K, a multiple of 16, base 16-byte
+ *           aligned
+ *   scales  [ceil(R / rows), ceil(K / 128)] f32, contiguous, rows = 1 or 128
+ * and stands for q[r, k] * scales[r / rows, k / 128].  The library's roundings take
+ * the largest magnitude of a block (128 columns of one row, or of 128 rows; fewer at
+ * the ends), a = max(that, 2^-100), and form
+ *   scale = a / 448,   q = e4m3(x * (448 / a)),
+ * each step in fp32 rounded to the nearest, ties to even.  A block with a NaN is NaN
+ * as a whole (scale and numbers); one with an infinity has the scale infinity, and
+ * its finite numbers become 0, the infinite ones NaN. */
+
+/* The RMS norm of a residual stream:
+ *   r = x + residual            (rounded to dt)
+ *   rstd = 1 / sqrt((1/D) sum_j r_j^2 + eps),   y_j = r_j rstd weight_j
+ * x, residual, summed (r), y: [N, D] of dtype dt, row strides ldx, ... >= D, unit
+ * column stride, any alignment of an element.  y is written in dt, in 8 bits (q and
+ * scales, rows = 1; y not rounded to dt before), or both: y or q may be NULL, q and
+ * scales only together.  residual may be NULL (r = x), summed, rstd ([N] f32) and
+ * weight ([D] of dtype wdt, 1) too.  summed may be x or residual itself, and y may
+ * be one of them (then their strides are equal); otherwise outputs overlap neither
+ * inputs nor each other.  Sums in fp32, in a fixed order.  N == 0 is valid. */
+FLCE_API int rms_norm_add_fwd(const void* x, int dt, int64_t N, int64_t D, int64_t ldx,
+                              const void* residual, int64_t ldr, const void* weight, int wdt,
+                              float eps, void* summed, int64_t lds, void* y, int64_t ldy,
+                              uint8_t* q, int64_t ldq, float* scales, float* rstd,
+                              flce_stream_t stream);
+
+/* Gradient of y by r, joined with what comes back along the stream: with
+ * h = r rstd and u = grad_y weight
+ *   grad_x_j = grad_summed_j + rstd (u_j - h_j (1/D) sum u h)     (one rounding)
+ *   grad_weight_j = sum over rows of grad_y_j h_j
+ * grad_x is the gradient of x and of residual alike.  grad_summed may be NULL (0);
+ * grad_x may be grad_y or grad_summed itself; the rest as rms_norm_bwd, workspace
+ * (norm_bwd_workspace_bytes) included.  The 8-bit output has no gradient of its own:
+ * grad_y is taken as that of the unrounded y. */
+FLCE_API int rms_norm_add_bwd(const void* summed, int dt, int64_t N, int64_t D, int64_t lds,
+                              const void* grad_y, int64_t ldgy, const void* grad_summed,
+                              int64_t ldgs, const void* weight, int wdt, const float* rstd,
+                              void* grad_x, int64_t ldgx, float* grad_weight, int accumulate,
+                              void* ws, size_t ws_bytes, flce_stream_t stream);
+
+/* Rounds x [R, ldx] (dtype dt, C columns) to 8 bits: q [R, C] with `rows` (1 or 128)
+ * rows to a scale, and the transpose qt [C, R] with scales_t, `rows` of ITS rows to
+ * a scale (so for rows = 1 its blocks are 128 rows of one column of x).  Either may
+ * be NULL with its scales; x is read once for both.  R == 0 is valid.  Outputs
+ * overlap neither x nor each other. */
+FLCE_API int quantize8(const void* x, int dt, int64_t R, int64_t C, int64_t ldx, int rows,
+                       uint8_t* q, int64_t ldq, float* scales, uint8_t* qt, int64_t ldqt,
+                       float* scales_t, flce_stream_t stream);
+
+/* y [M, N] (dtype dt_y, row stride ldy) = a b^T (+ bias [N], dtype dt_bias, or NULL)
+ * of a [M, K] (rows = 1) and b [N, K] (rows = b_rows, 1 or 128) in 8 bits.  A block's
+ * 128 products are summed by the tensor cores in fp32; these sums times the two
+ * scales, the column's first, add up in fp32 in a fixed order.  accumulate != 0 adds
+ * to y (FLCE_F32 only).  A layer's training pass is three of these:
+ *   y = x8 w8^T,   grad_x = g8 (w8^T)^T,   grad_w = (g8^T) (x8^T)^T
+ * with x, grad_y by rows and w by squares, each with its transpose from quantize8.
+ * M == 0 is valid.  y overlaps no input.  A wait inside the kernel that gives up
+ * leaves NaN in the elements it was for and sets FLCE_ETIMEOUT in *status (may be
+ * NULL). */
+FLCE_API int gemm8(const uint8_t* a, int64_t lda, const float* a_scales, int64_t M,
+                   const uint8_t* b, int64_t ldb, const float* b_scales, int b_rows, int64_t N,
+                   int64_t K, const void* bias, int dt_bias, void* y, int dt_y, int64_t ldy,
+                   int accumulate, int32_t* status, flce_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Beam search on the head's logits                                         */
+/* ------------------------------------------------------------------------ */
+/* B requests have K beams each; beam k of request b is row b K + k of logits
+ * [B K, ld] (dtype dt, V columns) and has the score scores[b K + k] (f32).  Going on
+ * with token v it has
+ *   scores[b K + k] + z[v] - lse,   lse = log sum_j exp(z_j)  of its row z,
+ * and of a request's K V continuations the `num` best are selected, best first: of
+ * one beam in the order of its logits, of several by the sum formed in fp64 (from an
+ * fp32 sum of exponentials), of equal ones the lowest k V + v first.  out_scores,
+ * out_tokens, out_parents: [B, num], the continuation's score rounded to fp32, v and
+ * k.  A logit of -infinity is a token that is not allowed: it has the score
+ * -infinity, and is selected only where nothing better is left.
+ * A beam with finished[b K + k] != 0 ([B K] bytes, or NULL) has ended: its logits are
+ * not used, it goes on with pad_id (in [0, V)) at its own score, and all else has
+ * -infinity.  So has everything of a beam whose score is not finite, or whose logits
+ * have no distribution (a NaN, +infinity, or nothing but -infinity).
+ * K and num at most 64, num <= K V, V <= 2^20, B K ceil(V / 8192) and more below
+ * 2^31.  B == 0 is valid.  Outputs and workspace overlap neither inputs nor each
+ * other.  ws: beam_select_workspace_bytes bytes, 16-byte aligned. */
+FLCE_API size_t beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V, int64_t num);
+FLCE_API int beam_select(const void* logits, int dt, int64_t B, int64_t K, int64_t V, int64_t ld,
+                         const float* scores, const uint8_t* finished, int64_t pad_id,
+                         int64_t num, float* out_scores, int64_t* out_tokens,
+                         int64_t* out_parents, void* ws, size_t ws_bytes, flce_stream_t stream);
+
+/* What a beam carries along (a cache, a history of tokens), by beams: row b K + k
+ * begins at data + (b K + k) row_stride and consists of `outer` runs of `inner` bytes,
+ * outer_stride apart.  All in bytes. */
+typedef struct {
+  void* data;
+  int64_t row_stride, outer, outer_stride, inner;
+} flce_beam_state_t;
+
+/* Puts the rows of n states in the order of parents [B, K] (device, int64), in place:
+ * row b K + k becomes what row b K + parents[b, k] was.  `states` is an array of the
+ * HOST, read before the call returns.  Rows that stay are not touched.  A parent
+ * outside [0, K) leaves its row as it was and sets FLCE_ELABEL in *status.  K at most
+ * 64.  Runs of a state do not overlap, and states do not overlap each other: what the
+ * strides show to overlap is refused (FLCE_ESHAPE, FLCE_EINVAL). */
+FLCE_API int beam_reorder(const flce_beam_state_t* states, int n, int64_t B, int64_t K,
+                          const int64_t* parents, int32_t* status, flce_stream_t stream);
+
 /* ------------------------------------------------- arguments from memory
  *
  * flce_call makes the call that `entry` names with the arguments that stand in
@@ -578,7 +691,12 @@ enum {
   FLCE_CALL_RMS_NORM_FWD = 3,
   FLCE_CALL_LAYER_NORM_BWD = 4,
   FLCE_CALL_RMS_NORM_BWD = 5,
-  FLCE_CALL_HEAD4_LOGITS = 6
+  FLCE_CALL_HEAD4_LOGITS = 6,
+  FLCE_CALL_RMS_NORM_ADD_FWD = 7,
+  FLCE_CALL_RMS_NORM_ADD_BWD = 8,
+  FLCE_CALL_QUANTIZE8 = 9,
+  FLCE_CALL_GEMM8 = 10,
+  FLCE_CALL_BEAM_SELECT = 11
 };
 FLCE_API int flce_call(int entry, const void* args, size_t bytes);
 

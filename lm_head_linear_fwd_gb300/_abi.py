@@ -86,6 +86,17 @@ _SIGNATURES = {
                           _i64, _p, _p]),
     "head4_quantize": (_i, [_p, _i, _i64, _i64, _i64, _i, _p, _i64, _p, _i, _p, _p]),
     "head4_wait_selftest": (_i, [_p, _p, ctypes.c_uint64, _p]),
+    "rms_norm_add_fwd": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i, _f, _p, _i64, _p, _i64,
+                              _p, _i64, _p, _p, _p]),
+    "rms_norm_add_bwd": (_i, [_p, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i, _p, _p, _i64,
+                              _p, _i, _p, _sz, _p]),
+    "quantize8": (_i, [_p, _i, _i64, _i64, _i64, _i, _p, _i64, _p, _p, _i64, _p, _p]),
+    "gemm8": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i, _i64, _i64, _p, _i, _p, _i, _i64, _i, _p,
+                   _p]),
+    "beam_select_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "beam_select": (_i, [_p, _i, _i64, _i64, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _p, _sz,
+                         _p]),
+    "beam_reorder": (_i, [ctypes.c_char_p, _i, _i64, _i64, _p, _p, _p]),
     "flce_call": (_i, [_i, ctypes.c_char_p, _sz]),
     "flce_gemm": (_i, [_i, _i, _i, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i, _p, _p]),
 }
@@ -165,6 +176,11 @@ class packed:
     layer_norm_bwd = staticmethod(_packed("layer_norm_bwd", 4))
     rms_norm_bwd = staticmethod(_packed("rms_norm_bwd", 5))
     head4_logits = staticmethod(_packed("head4_logits", 6))
+    rms_norm_add_fwd = staticmethod(_packed("rms_norm_add_fwd", 7))
+    rms_norm_add_bwd = staticmethod(_packed("rms_norm_add_bwd", 8))
+    quantize8 = staticmethod(_packed("quantize8", 9))
+    gemm8 = staticmethod(_packed("gemm8", 10))
+    beam_select = staticmethod(_packed("beam_select", 11))
 
 
 flce_status_string = _call("flce_status_string")
@@ -207,3 +223,10 @@ rms_norm_bwd = _call("rms_norm_bwd")
 head4_logits = _call("head4_logits")
 head4_quantize = _call("head4_quantize")
 head4_wait_selftest = _call("head4_wait_selftest")
+rms_norm_add_fwd = _call("rms_norm_add_fwd")
+rms_norm_add_bwd = _call("rms_norm_add_bwd")
+quantize8 = _call("quantize8")
+gemm8 = _call("gemm8")
+beam_select_workspace_bytes = _call("beam_select_workspace_bytes")
+beam_select = _call("beam_select")
+beam_reorder = _call("beam_reorder")

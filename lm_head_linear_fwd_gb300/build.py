@@ -19,8 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 # per machine architecture, so that objects built on one host are never linked on another
 LIBDIR = os.path.join(PKG, "_lib", platform.machine())
 LIB = os.path.join(LIBDIR, "libflce.so")
-SOURCES = ["ce_logits.cu", "flce.cu", "embedding.cu", "norm.cu", "head4.cu",
-           "call.cu"]
+SOURCES = ["ce_logits.cu", "flce.cu", "embedding.cu", "norm.cu", "norm_add.cu", "head4.cu",
+           "quantize8.cu", "gemm8.cu", "beam.cu", "call.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + os.path.join(ROOT, "include")]

@@ -1,0 +1,553 @@
+// Beam search on the head's logits: the best continuations over beams and
+// vocabulary, and the beams' states put in their order.
+//
+// A request has K beams.  Beam k with score s_k and logits z_k goes on with token v
+// at s_k + z_k[v] - lse(z_k); the `num` best of its K V continuations are wanted,
+// best first, of equal ones the one with the lowest k V + v.  Within a beam that
+// order is the logits' own, so the selection splits:
+//   beam_rows_kernel    a block takes a chunk of a row, reads it once, and leaves the
+//                       chunk's maximum and sum of exponentials and its `num` best
+//                       tokens, as 64-bit keys: the logit's bits in an order-keeping
+//                       form, then the token's complement, so that keys differ and
+//                       the larger one comes first;
+//   beam_merge_kernel   a block takes a request: every row's lse and best `num` keys
+//                       from its chunks', then the request's from its rows'.
+// Bound by the bytes of the logits, for few rows by the latency of the two launches.
+//
+// beam_reorder_kernel moves rows of caches and histories.  Their order is a map that
+// repeats some beams and drops others, in place: a thread owns 16 bytes of each of a
+// request's rows, copies the rows that move to shared memory, and writes them back.
+// Rows that stay where they are are not touched.  Bound by bytes.
+#include <algorithm>
+
+#include "rows.cuh"
+
+namespace flce {
+
+constexpr int kBeamThreads = 256;
+constexpr int kBeamElems = 32;                          // of a thread
+constexpr int kBeamChunk = kBeamThreads * kBeamElems;   // of a block
+constexpr int kBeamMost = 64;                           // beams of a request, and `num`
+constexpr int64_t kBeamVocab = int64_t(1) << 20;
+constexpr int kBeamMergeThreads = 512;
+
+// Order-keeping bits of a float (not NaN): larger floats, larger numbers.
+__device__ __forceinline__ uint32_t ordered(float z) {
+  const uint32_t u = __float_as_uint(z);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t beam_key(float z, uint32_t token) {
+  // the two zeros are equal
+  return static_cast<uint64_t>(ordered(z + 0.0f)) << 32 | (0xffffffffu - token);
+}
+__device__ __forceinline__ uint32_t key_token(uint64_t key) {
+  return 0xffffffffu - static_cast<uint32_t>(key);
+}
+__device__ __forceinline__ float key_logit(uint64_t key) {
+  return unordered(static_cast<uint32_t>(key >> 32));
+}
+
+struct BeamArgs {
+  const void* logits;
+  int64_t V, ld;
+  const float* scores;      // [B K]
+  const uint8_t* finished;  // [B K] or null
+  int64_t pad;
+  int K, num, chunks;
+  uint64_t* keys;  // [B K, chunks, num]
+  float2* sums;    // [B K, chunks]: maximum, sum of exp(z - maximum)
+  float* out_scores;
+  int64_t* out_tokens;
+  int64_t* out_parents;
+};
+
+// A row whose logits count: its beam goes on and has a score.
+__device__ __forceinline__ bool row_counts(const BeamArgs& a, int64_t row) {
+  const float s = a.scores[row];
+  return !(a.finished != nullptr && a.finished[row] != 0) && s > -INFINITY && s < INFINITY;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
+  constexpr int VEC = 16 / sizeof(T), NV = kBeamElems / VEC;
+  __shared__ uint64_t tops[kBeamThreads];
+  __shared__ uint64_t best[kBeamMost * kBeamElems];
+  __shared__ float red[kBeamThreads / 32];
+  __shared__ uint64_t least_sh;
+  __shared__ int count;
+  const int64_t row = blockIdx.x / a.chunks;
+  const int chunk = static_cast<int>(blockIdx.x - row * a.chunks);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!row_counts(a, row)) return;
+  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+  // chunks begin on 16-byte boundaries, `off` elements before the row for the first
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T);
+  const int64_t c0 = static_cast<int64_t>(chunk) * kBeamChunk - off;
+  float v[kBeamElems];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int64_t j = c0 + (k * kBeamThreads + threadIdx.x) * VEC;
+    float f[VEC];
+    if (j >= 0 && j + VEC <= a.V) {
+      Elem<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z + j)), f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        f[e] = j + e >= 0 && j + e < a.V ? Elem<T>::load(z + j + e) : -INFINITY;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[k * VEC + e] = f[e];
+  }
+  if (threadIdx.x == 0) count = 0;
+  // the maximum, and the thread's largest key
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < kBeamElems; ++i) m = fmaxf(m, v[i]);
+  uint64_t top = 0;  // below every key
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < kBeamElems; ++i) {
+    const int64_t j = c0 + ((i / VEC) * kBeamThreads + threadIdx.x) * VEC + i % VEC;
+    nan |= v[i] != v[i];
+    if (j >= 0 && j < a.V) {
+      const uint64_t key = beam_key(v[i], static_cast<uint32_t>(j));
+      top = key > top ? key : top;
+    }
+  }
+  tops[threadIdx.x] = top;
+  float bm = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+  if (lane == 0) red[warp] = bm;
+  __syncthreads();
+  bm = red[0];
+#pragma unroll
+  for (int w = 1; w < kBeamThreads / 32; ++w) bm = fmaxf(bm, red[w]);
+  __syncthreads();
+  // NaN and +infinity make the sum NaN; a chunk of -infinity has the sum 0
+  float s = 0.0f;
+  if (bm > -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < kBeamElems; ++i) s += ex2((v[i] - bm) * kLog2e);
+  }
+  if (nan) s = __int_as_float(0x7fffffff);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) red[warp] = s;
+  // the num-th largest of the threads' largest keys: at most num threads hold keys
+  // that are not smaller, and the chunk's best num are among these
+  int rank = 0;
+  for (int i = 0; i < kBeamThreads; ++i) rank += tops[i] > top ? 1 : 0;
+  if (rank == a.num - 1) least_sh = top;  // of empty threads (0) any
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0f;
+    for (int w = 0; w < kBeamThreads / 32; ++w) s += red[w];
+    a.sums[row * a.chunks + chunk] = make_float2(bm, s);
+  }
+  // fewer keyed threads than num: all keys count
+  const int keyed = __syncthreads_count(top != 0);
+  const uint64_t least = keyed >= a.num ? least_sh : 1;
+  if (top >= least) {
+#pragma unroll
+    for (int i = 0; i < kBeamElems; ++i) {
+      const int64_t j = c0 + ((i / VEC) * kBeamThreads + threadIdx.x) * VEC + i % VEC;
+      if (j < 0 || j >= a.V) continue;
+      const uint64_t key = beam_key(v[i], static_cast<uint32_t>(j));
+      if (key >= least) best[atomicAdd(&count, 1)] = key;
+    }
+  }
+  __syncthreads();
+  uint64_t* out = a.keys + (row * a.chunks + chunk) * a.num;
+  const int n = count;
+  for (int i = threadIdx.x; i < n; i += kBeamThreads) {
+    const uint64_t key = best[i];
+    int r = 0;
+    for (int k = 0; k < n; ++k) r += best[k] > key ? 1 : 0;
+    if (r < a.num) out[r] = key;
+  }
+  for (int i = n + threadIdx.x; i < a.num; i += kBeamThreads) out[i] = 0;
+}
+
+// How many of the `n` keys, largest first, are larger than `key`.
+__device__ __forceinline__ int larger(const uint64_t* keys, int n, uint64_t key) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (keys[mid] > key)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// The lowest num tokens, all at -infinity, but one that goes first.
+__device__ __forceinline__ uint32_t nth_token(int i, bool first_set, int64_t first) {
+  if (!first_set) return static_cast<uint32_t>(i);
+  if (i == 0) return static_cast<uint32_t>(first);
+  return static_cast<uint32_t>(i - 1 < first ? i - 1 : i);
+}
+
+__global__ void __launch_bounds__(kBeamMergeThreads) beam_merge_kernel(BeamArgs a) {
+  extern __shared__ uint64_t staged[];  // [warps][chunks * num], then the beams' best
+  const int64_t b = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int num = a.num, all = a.chunks * num;
+  const int per = static_cast<int>(min(static_cast<int64_t>(num), a.V));  // of a beam
+  uint64_t* keys = staged + warp * all;
+  double* score = reinterpret_cast<double*>(staged + warps * all);   // [K][num]
+  uint32_t* token = reinterpret_cast<uint32_t*>(score + a.K * num);  // [K][num]
+  for (int k = warp; k < a.K; k += warps) {
+    const int64_t row = b * a.K + k;
+    const float s = a.scores[row];
+    const bool done = a.finished != nullptr && a.finished[row] != 0;
+    double base = -INFINITY;  // score - lse
+    if (row_counts(a, row)) {
+      float m = -INFINITY, sum = 0.0f;
+      for (int c = lane; c < a.chunks; c += 32) m = fmaxf(m, a.sums[row * a.chunks + c].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int c = lane; c < a.chunks; c += 32) {
+        const float2 p = a.sums[row * a.chunks + c];
+        sum += p.x > -INFINITY ? p.y * ex2((p.x - m) * kLog2e) : p.y;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      // a NaN or +infinity among the logits, or nothing but -infinity: no distribution
+      if (m > -INFINITY && m < INFINITY && sum > 0.0f)
+        base = static_cast<double>(s) - (static_cast<double>(m) + log(static_cast<double>(sum)));
+    }
+    const bool live = base > -INFINITY;
+    if (!live) {
+      const bool ended = done && s > -INFINITY && s < INFINITY;
+      for (int i = lane; i < per; i += 32) {
+        score[k * num + i] = ended && i == 0 ? static_cast<double>(s) : -INFINITY;
+        token[k * num + i] = nth_token(i, ended, a.pad);
+      }
+    } else {
+      for (int i = lane; i < all; i += 32) keys[i] = a.keys[row * all + i];
+      __syncwarp();
+      for (int i = lane; i < all; i += 32) {
+        const uint64_t key = keys[i];
+        if (key == 0) continue;  // a short chunk's place
+        const int own = i / num;
+        int rank = i - own * num;
+        for (int c = 0; c < a.chunks && rank < num; ++c)
+          if (c != own) rank += larger(keys + c * num, num, key);
+        if (rank < num) {
+          score[k * num + rank] = base + static_cast<double>(key_logit(key));
+          token[k * num + rank] = key_token(key);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // a beam's continuations come best first: one of all beams' comes after all those
+  // before it in its own, and those of each other beam that are better
+  for (int i = threadIdx.x; i < a.K * per; i += blockDim.x) {
+    const int k = i / per, p = i - k * per;
+    const double s = score[k * num + p];
+    int rank = p;
+    for (int o = 0; o < a.K && rank < num; ++o) {
+      if (o == k) continue;
+      int lo = 0, hi = per;  // of equal ones the lower beam's come first
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        const double t = score[o * num + mid];
+        if (o < k ? t >= s : t > s)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      rank += lo;
+    }
+    if (rank >= num) continue;
+    a.out_scores[b * num + rank] = static_cast<float>(s);
+    a.out_tokens[b * num + rank] = token[k * num + p];
+    a.out_parents[b * num + rank] = k;
+  }
+}
+
+// ---------------------------------------------------------------- reordering
+
+constexpr int kReorderThreads = 128;
+constexpr int kReorderStates = 64;  // of a launch
+
+struct ReorderState {
+  char* data;
+  int64_t row_stride, outer_stride, units;  // bytes; units of one row
+  int64_t inner;                            // units of an inner run
+  int64_t first;                            // the state's first block
+};
+
+struct ReorderArgs {
+  ReorderState state[kReorderStates];
+  int states, K;
+  int64_t B;
+  const int64_t* parents;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// U: a unit, the largest power of two up to 16 that all addresses are multiples of.
+template <typename U>
+__global__ void __launch_bounds__(kReorderThreads)
+    beam_reorder_kernel(const __grid_constant__ ReorderArgs a) {
+  extern __shared__ uint4 moved_raw[];
+  U* moved = reinterpret_cast<U*>(moved_raw);  // [K][threads]
+  __shared__ int from[kBeamMost];
+  int t = 0;
+  while (t + 1 < a.states && static_cast<int64_t>(blockIdx.x) >= a.state[t + 1].first) ++t;
+  const ReorderState& st = a.state[t];
+  const int64_t block = blockIdx.x - st.first;
+  const int64_t per_row = (st.units + kReorderThreads - 1) / kReorderThreads;  // blocks
+  const int64_t b = block / per_row;
+  const int64_t u = block % per_row * kReorderThreads + threadIdx.x;
+  for (int k = threadIdx.x; k < a.K; k += kReorderThreads) {
+    int64_t p = a.parents[b * a.K + k];
+    if (p < 0 || p >= a.K) {  // no such beam: the row stays as it is
+      set_status(a.status, FLCE_ELABEL);
+      p = k;
+    }
+    from[k] = static_cast<int>(p);
+  }
+  __syncthreads();
+  if (u >= st.units) return;
+  const int64_t outer = u / st.inner;
+  char* p = st.data + b * a.K * st.row_stride + outer * st.outer_stride +
+            (u - outer * st.inner) * static_cast<int64_t>(sizeof(U));
+  for (int k = 0; k < a.K; ++k) {
+    if (from[k] == k) continue;
+    const char* src = p + from[k] * st.row_stride;
+    U* to = moved + k * kReorderThreads + threadIdx.x;
+    if constexpr (sizeof(U) == 16)
+      cp_async16(smem_u32(to), src);
+    else if constexpr (sizeof(U) == 8)
+      cp_async8(smem_u32(to), src);
+    else if constexpr (sizeof(U) == 4)
+      cp_async4(smem_u32(to), src);
+    else
+      *to = *reinterpret_cast<const U*>(src);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  for (int k = 0; k < a.K; ++k)
+    if (from[k] != k)
+      *reinterpret_cast<U*>(p + k * st.row_stride) = moved[k * kReorderThreads + threadIdx.x];
+}
+
+// ------------------------------------------------------------------------ host
+
+static int64_t beam_chunks(int64_t V) {
+  // a row may begin inside a 16-byte block: its first chunk is up to 7 elements short
+  return (V + 7 + kBeamChunk - 1) / kBeamChunk;
+}
+
+static bool beam_sizes(int64_t B, int64_t K, int64_t V, int64_t num) {
+  return B >= 0 && B <= 0x7fffffff / kBeamMost && K >= 1 && K <= kBeamMost && V >= 1 &&
+         V <= kBeamVocab && num >= 1 && num <= kBeamMost && num <= K * V &&
+         B * K * beam_chunks(V) <= 0x7fffffff;
+}
+
+template <typename U>
+static int launch_reorder(const ReorderArgs& a, int64_t blocks, cudaStream_t s) {
+  static std::atomic<uint64_t> raised{0};
+  const int rc = raise_smem(beam_reorder_kernel<U>, kBeamMost * kReorderThreads * 16, raised);
+  if (rc != FLCE_OK) return rc;
+  beam_reorder_kernel<U><<<static_cast<unsigned>(blocks), kReorderThreads,
+                           a.K * kReorderThreads * sizeof(U), s>>>(a);
+  return launch_status("beam_reorder_kernel launch");
+}
+
+// The largest power of two up to 16 that a state's address, runs and strides are
+// multiples of.
+static int reorder_unit(const flce_beam_state_t& t, int64_t R) {
+  uint64_t bits = reinterpret_cast<uintptr_t>(t.data) | static_cast<uint64_t>(t.inner) | 16u;
+  if (R > 1) bits |= static_cast<uint64_t>(t.row_stride);
+  if (t.outer > 1) bits |= static_cast<uint64_t>(t.outer_stride);
+  return static_cast<int>(bits & (~bits + 1));
+}
+
+static int64_t reorder_blocks(const flce_beam_state_t& t, int64_t B, int unit) {
+  const int64_t units = t.outer * (t.inner / unit);
+  const int64_t per_row = (units + kReorderThreads - 1) / kReorderThreads;
+  return per_row > 0x7fffffff ? per_row : per_row * B;
+}
+
+// A state's bytes and more: whole rows from their first byte to their last,
+static Span whole_rows(const flce_beam_state_t& t, int64_t R) {
+  return Span(t.data, R, (t.outer - 1) * t.outer_stride + t.inner, t.row_stride, 1);
+}
+
+// or lines of `inner` bytes one pitch apart, where both strides allow it.  States that
+// are apart in either way are apart.
+static Span lines(const flce_beam_state_t& t, int64_t R) {
+  if (t.outer == 1) return Span(t.data, R, t.inner, t.row_stride, 1);
+  if (R == 1) return Span(t.data, t.outer, t.inner, t.outer_stride, 1);
+  if (t.row_stride % t.outer_stride == 0)
+    return Span(t.data, (R - 1) * (t.row_stride / t.outer_stride) + t.outer, t.inner,
+                t.outer_stride, 1);
+  if (t.outer_stride % t.row_stride == 0)
+    return Span(t.data, (t.outer - 1) * (t.outer_stride / t.row_stride) + R, t.inner,
+                t.row_stride, 1);
+  const int64_t end = (R - 1) * t.row_stride + (t.outer - 1) * t.outer_stride + t.inner;
+  return Span(t.data, 1, end, end, 1);
+}
+
+static bool meet(const flce_beam_state_t& a, const flce_beam_state_t& b, int64_t R) {
+  if (a.outer == 0 || a.inner == 0 || b.outer == 0 || b.inner == 0) return false;
+  return overlap(whole_rows(a, R), whole_rows(b, R)) && overlap(lines(a, R), lines(b, R));
+}
+
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" size_t beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V, int64_t num) {
+  if (!beam_sizes(B, K, V, num) || B == 0) return 0;
+  const size_t lists = static_cast<size_t>(B * K * beam_chunks(V));
+  return round_up(lists * (num * sizeof(uint64_t) + sizeof(float2)), 256);
+}
+
+extern "C" int beam_select(const void* logits, int dt, int64_t B, int64_t K, int64_t V, int64_t ld,
+                           const float* scores, const uint8_t* finished, int64_t pad_id,
+                           int64_t num, float* out_scores, int64_t* out_tokens,
+                           int64_t* out_parents, void* ws, size_t ws_bytes,
+                           flce_stream_t stream) {
+  if (!valid_dtype(dt)) return FLCE_EDTYPE;
+  if (!beam_sizes(B, K, V, num)) return FLCE_ESHAPE;
+  if (finished != nullptr && (pad_id < 0 || pad_id >= V)) return FLCE_EINVAL;
+  const int rc = check_matrix(logits, dt, B * K, V, ld);
+  if (rc != FLCE_OK) return rc;
+  if (B == 0) return FLCE_OK;
+  if (scores == nullptr || out_scores == nullptr || out_tokens == nullptr ||
+      out_parents == nullptr)
+    return FLCE_EINVAL;
+  if (!aligned(scores, 4) || !aligned(out_scores, 4) || !aligned(out_tokens, 8) ||
+      !aligned(out_parents, 8) || !aligned(ws, 16))
+    return FLCE_EALIGN;
+  if (ws == nullptr || ws_bytes < beam_select_workspace_bytes(B, K, V, num))
+    return FLCE_EWORKSPACE;
+  const int64_t R = B * K, n = B * num;
+  const Span in[3] = {Span(logits, R, V, ld, dtype_size(dt)), Span(scores, 1, R, R, 4),
+                      Span(finished, 1, R, R, 1)};
+  const Span out[4] = {Span(out_scores, 1, n, n, 4), Span(out_tokens, 1, n, n, 8),
+                       Span(out_parents, 1, n, n, 8),
+                       Span(ws, 1, static_cast<int64_t>(ws_bytes), 0, 1)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 3; ++j)
+      if (overlap(out[i], in[j])) return FLCE_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return FLCE_EINVAL;
+  }
+  BeamArgs a{};
+  a.logits = logits, a.V = V, a.ld = ld, a.scores = scores, a.finished = finished;
+  a.pad = pad_id, a.K = static_cast<int>(K), a.num = static_cast<int>(num);
+  a.chunks = static_cast<int>(beam_chunks(V));
+  a.keys = static_cast<uint64_t*>(ws);
+  a.sums = reinterpret_cast<float2*>(a.keys + R * a.chunks * num);
+  a.out_scores = out_scores, a.out_tokens = out_tokens, a.out_parents = out_parents;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(a.chunks * R);
+  if (dt == FLCE_BF16)
+    beam_rows_kernel<__nv_bfloat16><<<grid, kBeamThreads, 0, s>>>(a);
+  else
+    beam_rows_kernel<float><<<grid, kBeamThreads, 0, s>>>(a);
+  // a warp for each beam, where their keys fit shared memory together
+  const int64_t list = static_cast<int64_t>(a.chunks) * num * 8, best = K * num * 12;
+  constexpr int64_t kMost = 200 * 1024;  // the most: 129 chunks of 64, 4096 best, 113 KB
+  const int warps = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({kBeamMergeThreads / 32, K, (kMost - best) / list})));
+  static std::atomic<uint64_t> raised{0};
+  const int rc2 = raise_smem(beam_merge_kernel, kMost, raised);
+  if (rc2 != FLCE_OK) return rc2;
+  beam_merge_kernel<<<static_cast<unsigned>(B), 32 * warps, warps * list + best, s>>>(a);
+  return launch_status("beam_merge_kernel launch");
+}
+
+extern "C" int beam_reorder(const flce_beam_state_t* states, int n, int64_t B, int64_t K,
+                            const int64_t* parents, int32_t* status, flce_stream_t stream) {
+  if (n < 0 || B < 0 || K < 1 || K > kBeamMost || B > 0x7fffffff / kBeamMost) return FLCE_ESHAPE;
+  if (n > 0 && states == nullptr) return FLCE_EINVAL;
+  if (n > 0 && B > 0 && (parents == nullptr || status == nullptr)) return FLCE_EINVAL;
+  if (!aligned(parents, 8) || !aligned(status, 4)) return FLCE_EALIGN;
+  const int64_t R = B * K;
+  constexpr int64_t kFar = int64_t(1) << 60;
+  for (int i = 0; i < n; ++i) {
+    const flce_beam_state_t& t = states[i];
+    if (t.outer < 0 || t.inner < 0 || t.row_stride < 0 || t.outer_stride < 0) return FLCE_ESHAPE;
+    if (t.outer == 0 || t.inner == 0 || R == 0) continue;
+    if (t.inner > kFar / t.outer || t.outer_stride > kFar / t.outer || t.row_stride > kFar / R)
+      return FLCE_ESHAPE;
+    if (t.data == nullptr) return FLCE_EINVAL;
+    // runs that do not meet: one row's within the row's stride, or all rows' within one
+    // step of the outer stride
+    const int64_t row = (t.outer - 1) * t.outer_stride + t.inner;
+    const bool steps = t.outer == 1 || t.outer_stride >= t.inner;
+    const bool rows = R == 1 || t.row_stride >= row ||
+                      (t.row_stride >= t.inner &&
+                       t.outer_stride >= (R - 1) * t.row_stride + t.inner);
+    if (!steps || !rows) return FLCE_ESHAPE;
+    if (reorder_blocks(t, B, reorder_unit(t, R)) > 0x7fffffff) return FLCE_ESHAPE;
+  }
+  if (R == 0) return FLCE_OK;
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if (meet(states[i], states[j], R)) return FLCE_EINVAL;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // one launch for the states of each unit
+  for (int unit = 16; unit > 0; unit /= 2) {
+    ReorderArgs a{};
+    a.K = static_cast<int>(K), a.B = B, a.parents = parents, a.status = status;
+    int64_t blocks = 0;
+    auto launch = [&]() {
+      int rc = FLCE_OK;
+      if (a.states > 0)
+        rc = unit == 16  ? launch_reorder<uint4>(a, blocks, s)
+             : unit == 8 ? launch_reorder<uint2>(a, blocks, s)
+             : unit == 4 ? launch_reorder<uint32_t>(a, blocks, s)
+             : unit == 2 ? launch_reorder<uint16_t>(a, blocks, s)
+                         : launch_reorder<uint8_t>(a, blocks, s);
+      a.states = 0;
+      blocks = 0;
+      return rc;
+    };
+    for (int i = 0; i < n; ++i) {
+      const flce_beam_state_t& t = states[i];
+      if (t.outer == 0 || t.inner == 0) continue;
+      if (reorder_unit(t, R) != unit) continue;
+      ReorderState& d = a.state[a.states];
+      d.data = static_cast<char*>(t.data);
+      d.row_stride = t.row_stride, d.outer_stride = t.outer_stride;
+      d.inner = t.inner / unit;
+      d.units = t.outer * d.inner;
+      const int64_t need = reorder_blocks(t, B, unit);
+      if (a.states > 0 && blocks + need > 0x7fffffff) {
+        const ReorderState keep = d;
+        const int rc = launch();
+        if (rc != FLCE_OK) return rc;
+        a.state[0] = keep;
+      }
+      a.state[a.states++].first = blocks;
+      blocks += need;
+      if (a.states == kReorderStates) {
+        const int rc = launch();
+        if (rc != FLCE_OK) return rc;
+      }
+    }
+    const int rc = launch();
+    if (rc != FLCE_OK) return rc;
+  }
+  return FLCE_OK;
+}

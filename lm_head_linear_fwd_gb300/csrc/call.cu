@@ -56,6 +56,11 @@ extern "C" int flce_call(int entry, const void* args, size_t bytes) {
     case FLCE_CALL_LAYER_NORM_BWD: return spread(layer_norm_bwd, args, bytes);
     case FLCE_CALL_RMS_NORM_BWD: return spread(rms_norm_bwd, args, bytes);
     case FLCE_CALL_HEAD4_LOGITS: return spread(head4_logits, args, bytes);
+    case FLCE_CALL_RMS_NORM_ADD_FWD: return spread(rms_norm_add_fwd, args, bytes);
+    case FLCE_CALL_RMS_NORM_ADD_BWD: return spread(rms_norm_add_bwd, args, bytes);
+    case FLCE_CALL_QUANTIZE8: return spread(quantize8, args, bytes);
+    case FLCE_CALL_GEMM8: return spread(gemm8, args, bytes);
+    case FLCE_CALL_BEAM_SELECT: return spread(beam_select, args, bytes);
     default: return FLCE_ENOSUP;
   }
 }

@@ -82,6 +82,8 @@ def _row_stride(t, name, rows, cols):
 
 def _rows_of(t):
     """t as the calls take it: unit column stride, rows that do not overlap."""
+    if t.numel() == 0:  # counts as contiguous whatever its strides
+        return t.new_empty(t.shape)
     ok = (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])
     return t if ok else t.contiguous()
 
