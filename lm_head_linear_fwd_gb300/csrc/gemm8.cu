@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "gemm8.cuh"
+#include "gemm8_pair.cuh"
 
 namespace flce {
 
@@ -238,10 +239,7 @@ __global__ void __launch_bounds__(kG8Threads, 1)
       }
       if (g.split > 1) break;  // one tile per cluster: its shares are added up below
       if (n >= g.N) continue;
-      const float bias =
-          g.bias == nullptr ? 0.0f
-          : g.bias_f32      ? static_cast<const float*>(g.bias)[n]
-                            : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(g.bias) + n);
+      const float bias = bias_at(g, n);
 #pragma unroll
       for (int j = 0; j < BN; ++j) {
         if (m0 + j >= g.M) break;
@@ -293,22 +291,24 @@ static int with_context() {
   return rc != FLCE_OK ? rc : cuda_status(cudaSetDevice(dev), "cudaSetDevice");
 }
 
-// A map of [rows, cols] bytes in boxes of 128 bytes of `box` rows, 128-byte swizzle,
+// A map of a [rows, cols] matrix in boxes of 128 bytes of `box` rows, 128-byte swizzle,
 // zeros outside.
-static int map8(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box) {
+static int map8(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box,
+                CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8, int es = 1) {
   static const EncodeFn encode = driver_entry<EncodeFn>("cuTensorMapEncodeTiled");
   if (encode == nullptr) {
     record_cuda_error(cudaErrorUnknown, "cuTensorMapEncodeTiled entry point");
     return FLCE_ECUDA;
   }
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld)};
-  const cuuint32_t boxes[2] = {128, static_cast<cuuint32_t>(box)}, one[2] = {1, 1};
-  if (encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, stride, boxes, one,
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld * es)};
+  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box)};
+  const cuuint32_t one[2] = {1, 1};
+  if (encode(m, type, 2, const_cast<void*>(p), dims, stride, boxes, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
-    record_cuda_error(cudaErrorUnknown, "cuTensorMapEncodeTiled of a matrix in 8 bits");
+    record_cuda_error(cudaErrorUnknown, "cuTensorMapEncodeTiled of a product's matrix");
     return FLCE_ECUDA;
   }
   return FLCE_OK;
@@ -330,6 +330,57 @@ static int launch_gemm8(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_
   const int64_t grid = std::min<int64_t>(g.tiles_m * g.tiles_n, sm_count());
   gemm8_kernel<BN><<<static_cast<unsigned>(grid), kG8Threads, G::kSmemBytes, s>>>(mb, ma, g);
   return launch_status("gemm8_kernel launch");
+}
+
+// A lone CTA cannot run half of a pair: as many pairs as can be resident at once.
+template <bool kCols>
+static int launch_gemm8_pair(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_t* b,
+                             int64_t ldb, int64_t K, cudaStream_t s) {
+  using G = Gemm8Pair;
+  auto* kernel = gemm8_pair_kernel<kCols>;
+  CUtensorMap ma, mb, my;
+  int rc = map8(&ma, a, g.M, K, lda, 128);
+  if (rc == FLCE_OK) rc = map8(&mb, b, g.N, K, ldb, 128);
+  const int es = g.y_f32 ? 4 : 2;
+  const bool tma_store = aligned(g.y, 16) && g.ldy * es % 16 == 0;
+  my = ma;  // not used without tma_store
+  if (rc == FLCE_OK && tma_store)
+    rc = map8(&my, g.y, g.M, g.N, g.ldy, 32,
+              g.y_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, es);
+  static std::atomic<uint64_t> raised{0};
+  if (rc == FLCE_OK) rc = raise_smem(kernel, G::kSmemBytes, raised);
+  if (rc != FLCE_OK) return rc;
+  g.tiles_m = (g.M + G::kTile - 1) / G::kTile;
+  g.tiles_n = (g.N + G::kTile - 1) / G::kTile;
+  const int64_t tiles = g.tiles_m * g.tiles_n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(G::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = G::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static std::atomic<int> resident[64];
+  int dev = 0;
+  rc = cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc != FLCE_OK) return rc;
+  int pairs = resident[dev & 63].load();
+  if (pairs <= 0) {
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(std::max(1, sm_count() / 2)), 1, 1);
+    rc = cuda_status(cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg),
+                     "cudaOccupancyMaxActiveClusters");
+    if (rc != FLCE_OK) return rc;
+    if (pairs < 1) return FLCE_ENOSUP;
+    resident[dev & 63].store(pairs);
+  }
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)), 1, 1);
+  const int group_m = static_cast<int>(std::min<int64_t>(8, g.tiles_m));
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, ma, mb, my, g, group_m, tma_store ? 1 : 0),
+                     "cudaLaunchKernelEx(gemm8_pair_kernel)");
 }
 
 }  // namespace flce
@@ -363,6 +414,7 @@ extern "C" int gemm8(const uint8_t* a, int64_t lda, const float* a_scales, int64
       overlap(out, Span(bias, 1, N, N, dtype_size(dt_bias))))
     return FLCE_EINVAL;
   if (M == 0) return FLCE_OK;
+  if (blocks8(M) > 0x7fffffff / blocks8(N)) return FLCE_ESHAPE;  // tiles are counted in 32 bits
   rc = with_context();
   if (rc != FLCE_OK) return rc;
   Gemm8Args g{};
@@ -374,5 +426,7 @@ extern "C" int gemm8(const uint8_t* a, int64_t lda, const float* a_scales, int64
   if (M <= 16) return launch_gemm8<16>(g, a, lda, b, ldb, K, s);
   if (M <= 32) return launch_gemm8<32>(g, a, lda, b, ldb, K, s);
   if (M <= 64) return launch_gemm8<64>(g, a, lda, b, ldb, K, s);
-  return launch_gemm8<128>(g, a, lda, b, ldb, K, s);
+  if (M <= 128) return launch_gemm8<128>(g, a, lda, b, ldb, K, s);
+  return b_rows == 1 ? launch_gemm8_pair<true>(g, a, lda, b, ldb, K, s)
+                     : launch_gemm8_pair<false>(g, a, lda, b, ldb, K, s);
 }

@@ -64,4 +64,14 @@ struct Gemm8Args {
   int split;        // CTAs of a cluster, which share a tile's blocks
 };
 
+__device__ __forceinline__ float2 both_nan() {
+  return make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+}
+
+__device__ __forceinline__ float bias_at(const Gemm8Args& g, int64_t n) {
+  if (g.bias == nullptr || n >= g.N) return 0.0f;
+  return g.bias_f32 ? static_cast<const float*>(g.bias)[n]
+                    : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(g.bias) + n);
+}
+
 }  // namespace flce
