@@ -2,15 +2,25 @@
 //
 // The pair's two SMs form one tile with tcgen05.mma.cta_group::2: each loads its 128
 // rows of a and 128 of the tile's 256 rows of b, and has 128 rows of the sums in its
-// tensor memory, a block's in one half of the 512 columns while the next block's are
-// formed in the other.  Eight warps add them up, a thread 128 columns of one row, so
-// that a's scale is one number per thread, and b's, where it is for 128 rows, one per
-// warp: one multiply-add per element and block.  Two more warps load the scales, a few
-// blocks ahead, to shared memory.
+// tensor memory.  Eight warps add them up, a thread 128 columns of one row, so that
+// a's scale is one number per thread, and b's, where it is for 128 rows, one per warp:
+// one multiply-add per element and block.  The two halves of the columns are apart: a
+// thread of its own issues each half's products, into one of the half's two places in
+// tensor memory while its four warps read the other, so that one half's waits fall
+// into the other's additions.  A warp loads the scales, a few blocks ahead, to shared
+// memory.
+//
+// Bound by the way of a block's sums from the tensor cores through the registers: of
+// about 1000 cycles per block the products take 512 and the additions 256 (packed
+// fp32 at half rate); the rest are the waits between them, which two warps to a
+// scheduler (their sums fill the registers) hide in part.  8192 x 4096 x 16384, scales
+// of b for 128 rows: 446 us, 2.46 PFLOP/s; for each row, twice the arithmetic: 780 us.
+// The scales loaded by the adding threads took 723 us (they spill); sixteen warps of 64
+// columns 548 and 755 us; all 256 columns issued by one thread 445 and 823 us.
 //
 // Barriers as in the pair kernel of tc_gemm.cuh:
-//   full[s]   leader: both CTAs' copies have landed     empty[s]  both: stage was read
-//   sum[i]    both: a block's sums are there            read[i]   leader: 16 warps have
+//   full[s]   leader: both CTAs' copies have landed     empty[s]  both: both halves' were read
+//   sum[i]    both: a half block's sums are there       read[i]   leader: its 8 warps have
 //                                                       read them
 //   scaled[r] both: kAhead blocks' scales are there     used[r]   both: they were used
 #pragma once
@@ -28,12 +38,12 @@ struct Gemm8Pair {
   static constexpr int kTile = 256;     // rows of a, and of b, of a pair's tile
   static constexpr int kStageA = 128 * 128;
   static constexpr int kStageBytes = 2 * kStageA;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 4;
   static constexpr int kAhead = 4;  // blocks whose scales are loaded together
   static constexpr int kRing = 3;   // of these
   static constexpr int kScales = 128 + 256;  // a block's: of the rows, and of the columns
   static constexpr int kScaleBytes = kRing * kAhead * kScales * 4;
-  static constexpr int kStaging = 8 * 4096;
+  static constexpr int kStaging = 8 * 2 * 4096;
   static constexpr int kSmemBytes = kStages * kStageBytes + kStaging + kScaleBytes + 1024;
 };
 
@@ -47,34 +57,45 @@ __device__ __forceinline__ void mma_8bit_pair(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
-// 32 columns of this thread's lane, to be waited for.
-__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 columns of fp32 of this thread's lane of tensor memory, as pairs.
+__device__ __forceinline__ void tmem_ld16_pairs(uint32_t taddr, uint64_t (&v)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "{\n\t.reg .b32 t<16>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {t0, t1};\n\t"
+      "mov.b64 %1, {t2, t3};\n\t"
+      "mov.b64 %2, {t4, t5};\n\t"
+      "mov.b64 %3, {t6, t7};\n\t"
+      "mov.b64 %4, {t8, t9};\n\t"
+      "mov.b64 %5, {t10, t11};\n\t"
+      "mov.b64 %6, {t12, t13};\n\t"
+      "mov.b64 %7, {t14, t15};\n\t"
+      "}"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]),
+        "=l"(v[7])
       : "r"(taddr)
       : "memory");
 }
-// Waits for all loads of this thread; r are those of the last one (so that no use of
-// them comes before).
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])::"memory");
+// Packed fp32 arithmetic on pairs.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
-
-__device__ __forceinline__ float2 pair_of(const uint32_t (&r)[32], int p) {
-  return make_float2(__uint_as_float(r[2 * p]), __uint_as_float(r[2 * p + 1]));
+__device__ __forceinline__ float2 both_of(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void fma_pair(uint64_t a, uint64_t b, uint64_t& c) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
 
 // Arrive on a barrier of another CTA of the cluster for tensor memory that was read:
@@ -84,24 +105,33 @@ __device__ __forceinline__ void mbar_arrive_read(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// The scales of four blocks from k on of a row (null: 0), each to its block's place.
-__device__ __forceinline__ void stage_scales(const float* row, int k, int blocks, bool wide,
-                                             float* to) {
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (row != nullptr) {
+// The scales of four blocks from k on, of 128 rows from `first` on: each to its block's
+// place.  All loads are under way before the first is waited for.
+__device__ __forceinline__ void stage_scales(const float* scales, int64_t first, int64_t rows,
+                                             int k, int blocks, bool wide, int lane, float* to) {
+  float4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // past the last row the last one's: their sums are not stored
+    const float* row = scales + min(first + 32 * i + lane, rows - 1) * blocks;
     if (wide) {  // all four are there, on a 16-byte boundary
-      v = *reinterpret_cast<const float4*>(row + k);
+      v[i] = *reinterpret_cast<const float4*>(row + k);
     } else {
-      v.x = row[k];
-      if (k + 1 < blocks) v.y = row[k + 1];
-      if (k + 2 < blocks) v.z = row[k + 2];
-      if (k + 3 < blocks) v.w = row[k + 3];
+      const int last = blocks - 1;
+      v[i].x = row[k];
+      v[i].y = row[min(k + 1, last)];
+      v[i].z = row[min(k + 2, last)];
+      v[i].w = row[min(k + 3, last)];
     }
   }
-  to[0] = v.x;
-  to[Gemm8Pair::kScales] = v.y;
-  to[2 * Gemm8Pair::kScales] = v.z;
-  to[3 * Gemm8Pair::kScales] = v.w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float* at = to + 32 * i + lane;
+    at[0] = v[i].x;
+    at[Gemm8Pair::kScales] = v[i].y;
+    at[2 * Gemm8Pair::kScales] = v[i].z;
+    at[3 * Gemm8Pair::kScales] = v[i].w;
+  }
 }
 
 // kCols: b has a scale for each of its rows (the tile's columns); else one for 128.
@@ -114,7 +144,7 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
   using G = Gemm8Pair;
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full_bar[S], empty_bar[S], sum_bar[2], read_bar[2], drain_bar;
+  __shared__ uint64_t full_bar[S], empty_bar[S], sum_bar[4], read_bar[4], drain_bar[2];
   __shared__ uint64_t scaled_bar[G::kRing], used_bar[G::kRing];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -129,17 +159,18 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full_bar[i], 1);
-      mbar_init(&empty_bar[i], 1);
+      mbar_init(&empty_bar[i], 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sum_bar[i], 1);
-      mbar_init(&read_bar[i], 16);
+      mbar_init(&read_bar[i], 8);
     }
     for (int i = 0; i < G::kRing; ++i) {
-      mbar_init(&scaled_bar[i], 2);
+      mbar_init(&scaled_bar[i], 1);
       mbar_init(&used_bar[i], 8);
     }
-    mbar_init(&drain_bar, 1);
+    mbar_init(&drain_bar[0], 1);
+    mbar_init(&drain_bar[1], 1);
     // checked builds: everything fits the launch's shared memory
     abort_sh = smem_in_range(0, G::kSmemBytes, g.status) ? 0 : 1;
     fence_barrier_init();
@@ -176,7 +207,7 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
         int mt, nt;
         tile_coords(t, nm, nn, group_m, mt, nt);
         const int arow = mt * G::kTile + static_cast<int>(rank) * 128;
-        const int brow = nt * G::kTile + static_cast<int>(rank) * 128;
+        const int brow = nt * G::kTile + static_cast<int>(rank) * 64;
         for (int k = 0; k < g.blocks; ++k) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag)) {
             ok = false;
@@ -187,6 +218,7 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
           const uint32_t bar = full_leader + stage * 8u;
           tma_load_2d_pair(to, &map_a, bar, k * 128, arow);
           tma_load_2d_pair(to + G::kStageA, &map_b, bar, k * 128, brow);
+          tma_load_2d_pair(to + G::kStageA + G::kStageA / 2, &map_b, bar, k * 128, brow + 128);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -201,28 +233,30 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
         }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
     if (leader && lane == 0) {
-      // products: the sums of one block after the other
-      constexpr uint32_t idesc = make_idesc(0, 256, G::kTile, false, false);  // 0: e4m3
+      // products of one half of the tile's columns: the sums of one block after the other
+      const int h = warp - 1;
+      constexpr uint32_t idesc = make_idesc(0, 256, 128, false, false);  // 0: e4m3
       uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         for (int k = 0; k < g.blocks; ++k) {
-          if (!mbar_wait(&read_bar[buf], buf_phase ^ 1u, abort_flag) ||
+          if (!mbar_wait(&read_bar[2 * h + buf], buf_phase ^ 1u, abort_flag) ||
               !mbar_wait(&full_bar[stage], phase, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sa = smem_u32(smem + stage * G::kStageBytes);
-          const uint32_t sb = sa + G::kStageA;
+          const uint32_t sb = sa + G::kStageA + h * (G::kStageA / 2);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_8bit_pair(tmem_base + buf * G::kTile, smem_desc_sw128(sa + j * 32, 16, 1024),
+            mma_8bit_pair(tmem_base + h * G::kTile + buf * 128,
+                          smem_desc_sw128(sa + j * 32, 16, 1024),
                           smem_desc_sw128(sb + j * 32, 16, 1024), idesc, j > 0 ? 1u : 0u);
           mma_commit_pair(&empty_bar[stage], 0x3);
-          mma_commit_pair(&sum_bar[buf], 0x3);
+          mma_commit_pair(&sum_bar[2 * h + buf], 0x3);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -232,13 +266,13 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
         }
       }
       if (!ok) fail();
-      mma_commit_pair(&drain_bar, 0x1);
+      mma_commit_pair(&drain_bar[h], 0x1);
       const uint64_t t0 = global_ns();
-      while (!mbar_try_wait(smem_u32(&drain_bar), 0) && global_ns() - t0 < kWaitLimitNs) {
+      while (!mbar_try_wait(smem_u32(&drain_bar[h]), 0) && global_ns() - t0 < kWaitLimitNs) {
       }
     }
   } else if (warp < 4) {
-    // scales: warp 2 those of the rows, warp 3 those of the columns
+    // scales
     const bool wide = g.blocks % G::kAhead == 0 &&
                       ((reinterpret_cast<uintptr_t>(g.a_scales) |
                         reinterpret_cast<uintptr_t>(g.b_scales)) & 15) == 0;
@@ -257,20 +291,15 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
           break;
         }
         float* to = scale_ring + slot * G::kAhead * G::kScales;
-        if (warp == 2) {
-#pragma unroll
-          for (int i = lane; i < 128; i += 32)
-            stage_scales(m0 + i < g.M ? g.a_scales + (m0 + i) * g.blocks : nullptr, k, g.blocks,
-                         wide, to + i);
-        } else if (kCols) {
-#pragma unroll
-          for (int i = lane; i < 256; i += 32)
-            stage_scales(n0 + i < g.N ? g.b_scales + (n0 + i) * g.blocks : nullptr, k, g.blocks,
-                         wide, to + 128 + i);
-        } else if (lane < 2) {
-          const int64_t n = n0 + lane * 128;
-          stage_scales(n < g.N ? g.b_scales + n / kBlock8 * g.blocks : nullptr, k, g.blocks, wide,
-                       to + 128 + lane);
+        stage_scales(g.a_scales, m0, g.M, k, g.blocks, wide, lane, to);
+        if (kCols) {
+          stage_scales(g.b_scales, n0, g.N, k, g.blocks, wide, lane, to + 128);
+          stage_scales(g.b_scales, n0 + 128, g.N, k, g.blocks, wide, lane, to + 256);
+        } else if (lane < 2 * G::kAhead) {
+          const int64_t n = min(n0 / kBlock8 + lane % 2, (g.N - 1) / kBlock8);
+          const int at = lane / 2;
+          to[at * G::kScales + 128 + lane % 2] =
+              g.b_scales[n * g.blocks + min(k + at, g.blocks - 1)];
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&scaled_bar[slot]);
@@ -285,67 +314,80 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
     // sums: a thread has 128 columns of one row
     const int quad = warp & 3;         // the tensor memory lanes this warp may access
     const int half = (warp - 4) >> 2;  // its half of the columns
-    const uint32_t lanes =
-        tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * 128);
-    uint8_t* slab = smem + S * G::kStageBytes + (warp - 4) * 4096;
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                           static_cast<uint32_t>(half * G::kTile);
+    uint8_t* slabs = smem + S * G::kStageBytes + (warp - 4) * 8192;
     uint32_t buf = 0, buf_phase = 0, slot = 0, slot_phase = 0;
+    int next_slab = 0;
     for (int t = first; t < tiles; t += step) {
       int mt, nt;
       tile_coords(t, nm, nn, group_m, mt, nt);
-      float2 acc[64];
+      uint64_t sums[64];  // pairs of columns
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
-      bool good = true;
+      for (int j = 0; j < 64; ++j) sums[j] = 0;
+      // the next block's scale is asked for while this one's columns are added
+      bool good = mbar_wait(&scaled_bar[slot], slot_phase, abort_flag);
+      const float* scales = scale_ring + slot * G::kAhead * G::kScales;
+      float row_s = scales[quad * 32 + lane], col_s = kCols ? 1.0f : scales[128 + half];
       for (int k = 0; k < g.blocks; ++k) {
         const int at = k & (G::kAhead - 1);
-        if (at == 0) good &= mbar_wait(&scaled_bar[slot], slot_phase, abort_flag);
-        const float* scales = scale_ring + (slot * G::kAhead + at) * G::kScales;
-        float s = scales[quad * 32 + lane];
-        if (!kCols) s = __fmul_rn(s, scales[128 + half]);
-        const float4* c4 = reinterpret_cast<const float4*>(scales + 128 + half * 128);
-        good &= mbar_wait(&sum_bar[buf], buf_phase, abort_flag);
+        const bool last = k + 1 == g.blocks, slot_done = last || at == G::kAhead - 1;
+        const float s = kCols ? row_s : __fmul_rn(row_s, col_s);
+        const uint64_t s2 = pair_of(s, s);
+        const ulonglong2* c2 = reinterpret_cast<const ulonglong2*>(scales + 128 + half * 128);
+        good &= mbar_wait(&sum_bar[2 * half + buf], buf_phase, abort_flag);
         __syncwarp();
         tc_fence_after();
-        const uint32_t from = lanes + buf * G::kTile;
-        uint32_t r[2][32];
-        tmem_ld32_start(from, r[0]);
+        const uint32_t from = lanes + buf * 128;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          tmem_ld32_wait(r[j & 1]);
-          if (j < 3) {
-            tmem_ld32_start(from + 32 * (j + 1), r[(j + 1) & 1]);
-          } else {
+        for (int j = 0; j < 8; ++j) {
+          ulonglong2 c[4];
+          if (kCols) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) c[p] = c2[j * 4 + p];
+          }
+          uint64_t v[8];
+          tmem_ld16_pairs(from + 16 * j, v);
+          if (j == 3 && !last && !slot_done) {
+            row_s = scales[G::kScales + quad * 32 + lane];
+            if (!kCols) col_s = scales[G::kScales + 128 + half];
+          }
+          if (j == 7) {
             // the last columns are here: the next block but one may be formed
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_read(read_leader + buf * 8u);
+            if (lane == 0) mbar_arrive_read(read_leader + (2 * half + buf) * 8u);
           }
 #pragma unroll
-          for (int p = 0; p < 16; p += 2) {
-            float2 a = pair_of(r[j & 1], p), b = pair_of(r[j & 1], p + 1);
-            if (kCols) {
-              const float4 c = c4[j * 8 + p / 2];
-              a = __fmul2_rn(a, make_float2(c.x, c.y));
-              b = __fmul2_rn(b, make_float2(c.z, c.w));
-            }
-            acc[j * 16 + p] = __ffma2_rn(a, make_float2(s, s), acc[j * 16 + p]);
-            acc[j * 16 + p + 1] = __ffma2_rn(b, make_float2(s, s), acc[j * 16 + p + 1]);
+          for (int p = 0; p < 8; ++p) {
+            if (kCols) v[p] = mul_pair(v[p], p & 1 ? c[p / 2].y : c[p / 2].x);
+            fma_pair(v[p], s2, sums[j * 8 + p]);
           }
         }
+        buf_phase ^= buf;
         buf ^= 1u;
-        if (buf == 0) buf_phase ^= 1u;
-        if (at == G::kAhead - 1 || k == g.blocks - 1) {
+        scales += G::kScales;
+        if (slot_done) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&used_bar[slot]);
           if (++slot == G::kRing) {
             slot = 0;
             slot_phase ^= 1u;
           }
+          if (!last) {
+            good &= mbar_wait(&scaled_bar[slot], slot_phase, abort_flag);
+            scales = scale_ring + slot * G::kAhead * G::kScales;
+            row_s = scales[quad * 32 + lane];
+            if (!kCols) col_s = scales[128 + half];
+          }
         }
       }
       const int64_t m_first = static_cast<int64_t>(mt) * G::kTile + rank * 128 + quad * 32;
       const int64_t n0 = static_cast<int64_t>(nt) * G::kTile + half * 128;
       if (!good) fail();
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = both_of(sums[j]);
       if (!good) {  // a wait gave up: its elements are not a number
 #pragma unroll
         for (int j = 0; j < 64; ++j) acc[j] = both_nan();
@@ -365,9 +407,9 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
         if (!g.y_f32 && c >= 2) break;
         const int64_t n = n0 + c * slab_cols;
         if (n >= g.N || m_first >= g.M) break;
-        if (tma_store) {
-          if (lane == 0) bulk_wait_read_all();  // the last store has read the slab
-        }
+        uint8_t* slab = slabs + next_slab * 4096;
+        next_slab ^= 1;
+        if (tma_store && lane == 0) bulk_wait_read_le1();  // the slab's last store has read it
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
