@@ -11,7 +11,6 @@
 
 namespace flce {
 
-constexpr int kG8Threads = 192;  // copies, products, and four warps that add up
 constexpr int kG8Rows = 128;     // rows of weights of a tile
 constexpr int kG8Ahead = 8;      // blocks whose scales are loaded together
 
@@ -24,6 +23,12 @@ struct Gemm8Geo {
   static constexpr int kTmemCols = BN == 16 ? 64 : BN == 32 ? 128 : 256;
   static constexpr int kScaleBytes = 2 * kG8Ahead * BN * 4;
   static constexpr int kSmemBytes = kStages * kStageBytes + kScaleBytes + 1024;
+  // Warps that add up: each of two sets of four has half of the columns where they are
+  // many (with one set 128 x 4096 x 4096 took 31 us)
+  static constexpr int kSets = BN >= 64 ? 2 : 1;
+  static constexpr int kCols = BN / kSets;  // of a thread
+  static constexpr int kAdders = 128 * kSets;
+  static constexpr int kThreads = 64 + kAdders;  // and copies, and products
   static constexpr int kLoad = BN == 16 ? 16 : 32;  // columns read back at a time
 };
 
@@ -35,8 +40,12 @@ __device__ __forceinline__ void load_scales(const float* row, int k, int end,
   for (int i = 0; i < kG8Ahead; ++i) s[i] = row != nullptr && k + i < end ? row[k + i] : 0.0f;
 }
 
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 template <int BN>
-__global__ void __launch_bounds__(kG8Threads, 1)
+__global__ void __launch_bounds__(Gemm8Geo<BN>::kThreads, 1)
     gemm8_kernel(const __grid_constant__ CUtensorMap map_b,
                  const __grid_constant__ CUtensorMap map_a, const Gemm8Args g) {
   using G = Gemm8Geo<BN>;
@@ -48,7 +57,7 @@ __global__ void __launch_bounds__(kG8Threads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* col_scales = reinterpret_cast<float*>(smem + S * G::kStageBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   volatile int* abort_flag = &abort_sh;
 
   if (threadIdx.x == 0) {
@@ -58,7 +67,7 @@ __global__ void __launch_bounds__(kG8Threads, 1)
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&sum_bar[i], 1);
-      mbar_init(&read_bar[i], 4);
+      mbar_init(&read_bar[i], 4 * G::kSets);
     }
     mbar_init(&drain_bar, 1);
     // checked builds: the ring and the scales fit the launch's shared memory
@@ -75,7 +84,6 @@ __global__ void __launch_bounds__(kG8Threads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (g.split > 1) cluster_sync();  // before another CTA's shared memory is written
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
   // this CTA's share of a tile's blocks, and its tiles
@@ -131,65 +139,81 @@ __global__ void __launch_bounds__(kG8Threads, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // products: the sums of one block after the other
-      constexpr uint32_t idesc = make_idesc(0, kG8Rows, BN, false, false);  // 0: e4m3
-      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
-      bool ok = true;
-      for (int64_t t = first; t < tiles && ok; t += step) {
-        for (int k = k0; k < k1; ++k) {
-          if (!mbar_wait(&read_bar[buf], buf_phase ^ 1u, abort_flag) ||
-              !mbar_wait(&full_bar[stage], phase, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * G::kStageBytes);
-          const uint32_t sb = sa + G::kStageA;
+    // products: the sums of one block after the other
+    constexpr uint32_t idesc = make_idesc(0, kG8Rows, BN, false, false);  // 0: e4m3
+    const uint64_t desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+    bool ok = true;
+    for (int64_t t = first; t < tiles && ok; t += step) {
+      for (int k = k0; k < k1; ++k) {
+        ok = mbar_wait(&read_bar[buf], buf_phase ^ 1u, abort_flag) &&
+             mbar_wait(&full_bar[stage], phase, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t da = desc + stage * (G::kStageBytes / 16), db = da + G::kStageA / 16;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_8bit(tmem_base + buf * BN, smem_desc_sw128(sa + j * 32, 16, 1024),
-                     smem_desc_sw128(sb + j * 32, 16, 1024), idesc, j > 0 ? 1u : 0u);
+            mma_8bit(tmem_base + buf * BN, da + 2 * j, db + 2 * j, idesc, j > 0 ? 1u : 0u);
           mma_commit(&empty_bar[stage]);
           mma_commit(&sum_bar[buf]);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (++buf == kBufs) {
-            buf = 0;
-            buf_phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++buf == kBufs) {
+          buf = 0;
+          buf_phase ^= 1u;
         }
       }
-      if (!ok) fail();
-      // wait (bounded) until every product issued above has finished
-      mma_commit(&drain_bar);
-      const uint64_t t0 = global_ns();
-      while (!mbar_try_wait(smem_u32(&drain_bar), 0) && global_ns() - t0 < kWaitLimitNs) {
-      }
     }
+    if (!ok && lane == 0) fail();
+    // wait (bounded) until every product issued above has finished
+    if (elect_one()) mma_commit(&drain_bar);
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(smem_u32(&drain_bar), 0) && global_ns() - t0 < kWaitLimitNs) {
+    }
+    __syncwarp();
   } else {
-    // sums: a thread has one row of weights
+    // sums: a thread has kCols columns (tokens) of one row of weights
     const int quad = warp & 3;  // the tensor memory lanes this warp may access
+    const int c0 = (warp - 2) / 4 * G::kCols;
     const int row = quad * 32 + lane, t0 = threadIdx.x - 64;
-    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t lanes =
+        tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c0);
     uint32_t buf = 0, buf_phase = 0;
+    int half = 0;
+    float acc[G::kCols];
+    int64_t m0 = 0, n = 0;
+    // y[m0 + j, n] of the thread's row
+    auto store = [&](int j, float v) {
+      if (n >= g.N || m0 + j >= g.M) return;
+      v += bias_at(g, n);
+      const int64_t at = (m0 + j) * g.ldy + n;
+      if (g.y_f32) {
+        float* y = static_cast<float*>(g.y) + at;
+        *y = g.accumulate ? *y + v : v;
+      } else {
+        Elem<__nv_bfloat16>::store(static_cast<__nv_bfloat16*>(g.y) + at, v);
+      }
+    };
     for (int64_t t = first; t < tiles; t += step) {
-      const int64_t m0 = t % g.tiles_m * BN, n0 = t / g.tiles_m * kG8Rows;
-      const int64_t n = n0 + row;
+      m0 = t % g.tiles_m * BN;
+      n = t / g.tiles_m * kG8Rows + row;
       const float* row_scale =
           n < g.N ? g.b_scales + (g.b_rows == 1 ? n : n / kBlock8) * g.blocks : nullptr;
       const float* col_scale =
           t0 < BN && m0 + t0 < g.M ? g.a_scales + (m0 + t0) * g.blocks : nullptr;
-      float acc[BN];
 #pragma unroll
-      for (int j = 0; j < BN; ++j) acc[j] = 0.0f;
+      for (int j = 0; j < G::kCols; ++j) acc[j] = 0.0f;
       float rs[kG8Ahead], cs[kG8Ahead], rs_next[kG8Ahead];
       load_scales(row_scale, k0, k1, rs_next);
       load_scales(col_scale, k0, k1, cs);
       bool good = true;
-      for (int k = k0, half = 0; k < k1; k += kG8Ahead, half ^= 1) {
+      for (int k = k0; k < k1; k += kG8Ahead, half ^= 1) {
         float* shared_scales = col_scales + half * kG8Ahead * BN;
         if (t0 < BN) {
 #pragma unroll
@@ -199,20 +223,16 @@ __global__ void __launch_bounds__(kG8Threads, 1)
         for (int i = 0; i < kG8Ahead; ++i) rs[i] = rs_next[i];
         load_scales(row_scale, k + kG8Ahead, k1, rs_next);
         load_scales(col_scale, k + kG8Ahead, k1, cs);
-        named_barrier(1, 128);
+        named_barrier(1, G::kAdders);
 #pragma unroll
         for (int i = 0; i < kG8Ahead; ++i) {
           if (k + i >= k1) break;
-          int ok = 1;
-          if (lane == 0) ok = mbar_wait(&sum_bar[buf], buf_phase, abort_flag) ? 1 : 0;
-          if (!__shfl_sync(0xffffffffu, ok, 0)) {
-            if (lane == 0) fail();
-            good = false;
-          }
+          good &= mbar_wait(&sum_bar[buf], buf_phase, abort_flag);
+          __syncwarp();
           tc_fence_after();
-          const float4* s4 = reinterpret_cast<const float4*>(shared_scales + i * BN);
+          const float4* s4 = reinterpret_cast<const float4*>(shared_scales + i * BN + c0);
 #pragma unroll
-          for (int j = 0; j < BN; j += G::kLoad) {
+          for (int j = 0; j < G::kCols; j += G::kLoad) {
             float v[G::kLoad];
             tmem_ld(lanes + buf * BN + j, v);
 #pragma unroll
@@ -233,25 +253,42 @@ __global__ void __launch_bounds__(kG8Threads, 1)
           }
         }
       }
-      if (!good) {  // a wait gave up: its logits are not a number
+      if (!good) {  // a wait gave up: its elements are not a number
+        fail();
 #pragma unroll
-        for (int j = 0; j < BN; ++j) acc[j] = __int_as_float(0x7fffffff);
+        for (int j = 0; j < G::kCols; ++j) acc[j] = __int_as_float(0x7fffffff);
       }
-      if (g.split > 1) break;  // one tile per cluster: its shares are added up below
-      if (n >= g.N) continue;
-      const float bias = bias_at(g, n);
+      if (g.split == 1) {
 #pragma unroll
-      for (int j = 0; j < BN; ++j) {
-        if (m0 + j >= g.M) break;
-        const int64_t at = (m0 + j) * g.ldy + n;
-        if (g.y_f32) {
-          float* y = static_cast<float*>(g.y) + at;
-          *y = g.accumulate ? *y + (acc[j] + bias) : acc[j] + bias;
-        } else {
-          Elem<__nv_bfloat16>::store(static_cast<__nv_bfloat16*>(g.y) + at, acc[j] + bias);
-        }
+        for (int j = 0; j < G::kCols; ++j) store(c0 + j, acc[j]);
       }
     }
+    if (g.split > 1) {
+      // One tile per cluster: each CTA adds up all shares of its part of the columns, in
+      // the order of the ranks.  The ring is free in every CTA (its blocks' sums are
+      // read), and takes the shares as [from][column][row].
+      const int part = BN / g.split;
+      cluster_sync();
+      const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>((rank * part * kG8Rows + row) * 4);
+#pragma unroll
+      for (int j = 0; j < G::kCols; ++j) {
+        const int c = c0 + j;
+        st_cluster_f32(mapa_shared(mine + static_cast<uint32_t>(c % part * kG8Rows * 4),
+                                   static_cast<uint32_t>(c / part)), acc[j]);
+      }
+      cluster_sync();
+      const float* shares = reinterpret_cast<const float*>(smem);
+      for (int c = (warp - 2) / 4; c < part; c += G::kSets) {
+        float v = 0.0f;
+        for (int r = 0; r < g.split; ++r) v += shares[(r * part + c) * kG8Rows + row];
+        store(rank * part + c, v);
+      }
+    }
+  }
+  if (g.split > 1 && warp < 2) {
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
   }
 
   tc_fence_before();
@@ -326,10 +363,30 @@ static int launch_gemm8(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_
   if (rc != FLCE_OK) return rc;
   g.tiles_m = (g.M + BN - 1) / BN;
   g.tiles_n = (g.N + kG8Rows - 1) / kG8Rows;
+  const int64_t tiles = g.tiles_m * g.tiles_n;
+  // Few tiles: a cluster of CTAs to each, while there are SMs and each has two blocks
+  // (1 x 4096 x 4096: 16.6 us alone, XX in clusters of four)
   g.split = 1;
-  const int64_t grid = std::min<int64_t>(g.tiles_m * g.tiles_n, sm_count());
-  gemm8_kernel<BN><<<static_cast<unsigned>(grid), kG8Threads, G::kSmemBytes, s>>>(mb, ma, g);
-  return launch_status("gemm8_kernel launch");
+  while (g.split < 8 && tiles * g.split * 2 <= sm_count() && g.blocks >= 4 * g.split) g.split *= 2;
+  if (g.split == 1) {
+    gemm8_kernel<BN><<<static_cast<unsigned>(std::min<int64_t>(tiles, sm_count())), G::kThreads,
+                       G::kSmemBytes, s>>>(mb, ma, g);
+    return launch_status("gemm8_kernel launch");
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(g.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.split), 1, 1);
+  cfg.blockDim = dim3(G::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = G::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, gemm8_kernel<BN>, mb, ma, g),
+                     "cudaLaunchKernelEx(gemm8_kernel)");
 }
 
 // A lone CTA cannot run half of a pair: as many pairs as can be resident at once.

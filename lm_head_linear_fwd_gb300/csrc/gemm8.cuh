@@ -26,6 +26,25 @@ __device__ __forceinline__ void mma_8bit(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
+// One lane of a warp whose lanes are all here.  The products are issued by a warp that
+// goes through its loop as a whole, so that descriptors and addresses stay in the
+// registers that a warp shares, where the instruction wants them: with one lane in
+// the loop four products and their two commits took 450 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// This thread's warp, known to be the same for all its lanes.
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+}
+
 // K columns of fp32 of this thread's lane of tensor memory (16 or 32).
 template <int K>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[K]) {

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
   __shared__ int abort_sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   float* scale_ring = reinterpret_cast<float*>(smem + S * G::kStageBytes + G::kStaging);
@@ -234,29 +234,31 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
       }
     }
   } else if (warp <= 2) {
-    if (leader && lane == 0) {
+    if (leader) {
       // products of one half of the tile's columns: the sums of one block after the other
       const int h = warp - 1;
       constexpr uint32_t idesc = make_idesc(0, 256, 128, false, false);  // 0: e4m3
+      const uint64_t desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
       uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         for (int k = 0; k < g.blocks; ++k) {
-          if (!mbar_wait(&read_bar[2 * h + buf], buf_phase ^ 1u, abort_flag) ||
-              !mbar_wait(&full_bar[stage], phase, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = mbar_wait(&read_bar[2 * h + buf], buf_phase ^ 1u, abort_flag) &&
+               mbar_wait(&full_bar[stage], phase, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * G::kStageBytes);
-          const uint32_t sb = sa + G::kStageA + h * (G::kStageA / 2);
+          if (elect_one()) {
+            const uint64_t da = desc + stage * (G::kStageBytes / 16);
+            const uint64_t db = da + (G::kStageA + h * (G::kStageA / 2)) / 16;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_8bit_pair(tmem_base + h * G::kTile + buf * 128,
-                          smem_desc_sw128(sa + j * 32, 16, 1024),
-                          smem_desc_sw128(sb + j * 32, 16, 1024), idesc, j > 0 ? 1u : 0u);
-          mma_commit_pair(&empty_bar[stage], 0x3);
-          mma_commit_pair(&sum_bar[2 * h + buf], 0x3);
+            for (int j = 0; j < 4; ++j)
+              mma_8bit_pair(tmem_base + h * G::kTile + buf * 128, da + 2 * j, db + 2 * j, idesc,
+                            j > 0 ? 1u : 0u);
+            mma_commit_pair(&empty_bar[stage], 0x3);
+            mma_commit_pair(&sum_bar[2 * h + buf], 0x3);
+          }
+          __syncwarp();
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -265,11 +267,12 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
           if (buf == 0) buf_phase ^= 1u;
         }
       }
-      if (!ok) fail();
-      mma_commit_pair(&drain_bar[h], 0x1);
+      if (!ok && lane == 0) fail();
+      if (elect_one()) mma_commit_pair(&drain_bar[h], 0x1);
       const uint64_t t0 = global_ns();
       while (!mbar_try_wait(smem_u32(&drain_bar[h]), 0) && global_ns() - t0 < kWaitLimitNs) {
       }
+      __syncwarp();
     }
   } else if (warp < 4) {
     // scales
