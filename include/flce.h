@@ -650,9 +650,9 @@ FLCE_API int gemm8(const uint8_t* a, int64_t lda, const float* a_scales, int64_t
  * not used, it goes on with pad_id (in [0, V)) at its own score, and all else has
  * -infinity.  So has everything of a beam whose score is not finite, or whose logits
  * have no distribution (a NaN, +infinity, or nothing but -infinity).
- * K and num at most 64, num <= K V, V <= 2^20, B K ceil(V / 8192) and more below
- * 2^31.  B == 0 is valid.  Outputs and workspace overlap neither inputs nor each
- * other.  ws: beam_select_workspace_bytes bytes, 16-byte aligned. */
+ * K and num at most 64, num <= K V, V <= 2^20, B K ceil((V + 7) / 2048) below 2^31.  B == 0 is valid.  Outputs and workspace overlap neither inputs nor each
+ * other.  ws: beam_select_workspace_bytes bytes (on the current device), 16-byte
+ * aligned. */
 FLCE_API size_t beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V, int64_t num);
 FLCE_API int beam_select(const void* logits, int dt, int64_t B, int64_t K, int64_t V, int64_t ld,
                          const float* scores, const uint8_t* finished, int64_t pad_id,
@@ -670,8 +670,8 @@ typedef struct {
 /* Puts the rows of n states in the order of parents [B, K] (device, int64), in place:
  * row b K + k becomes what row b K + parents[b, k] was.  `states` is an array of the
  * HOST, read before the call returns.  Rows that stay are not touched.  A parent
- * outside [0, K) leaves its row as it was and sets FLCE_ELABEL in *status.  K at most
- * 64.  Runs of a state do not overlap, and states do not overlap each other: what the
+ * outside [0, K) leaves its row as it was and sets FLCE_ELABEL in *status (may be
+ * NULL).  K at most 64.  Runs of a state do not overlap, and states do not overlap each other: what the
  * strides show to overlap is refused (FLCE_ESHAPE, FLCE_EINVAL). */
 FLCE_API int beam_reorder(const flce_beam_state_t* states, int n, int64_t B, int64_t K,
                           const int64_t* parents, int32_t* status, flce_stream_t stream);

@@ -97,27 +97,33 @@ def beam_reorder_(states, parents, *, status=None) -> None:
     whose rows have at most one gap in their order in memory.  A parent outside
     [0, K) leaves its row as it was and sets FLCE_ELABEL in ``status``
     (new_status), if given."""
-    _on_gpu = isinstance(parents, torch.Tensor) and parents.is_cuda
-    if not _on_gpu or parents.dtype is not torch.int64 or parents.dim() != 2 or \
+    if not isinstance(parents, torch.Tensor) or not parents.is_cuda or \
+            parents.dtype is not torch.int64 or parents.dim() != 2 or \
             not parents.is_contiguous():
         raise ValueError("parents must be a contiguous int64 CUDA tensor [B, K]")
     dev = parents.device
+    index = dev.index
     B, K = parents.shape
-    rows = []
+    R = B * K
+    rows, last, runs = [], None, None  # caches mostly come in one shape
     for i, t in enumerate(states):
-        _on(t, f"states[{i}]", dev)
-        shape = t.shape
-        if len(shape) < 1 or shape[0] != B * K:
-            raise ValueError(f"states[{i}] must have {B * K} rows")
-        if t.numel() == 0:
-            continue
-        runs = _runs(shape, t.stride(), t.element_size())
-        if runs is None:
-            raise ValueError(f"states[{i}]: more than one gap in a row's order in memory")
-        rows.append(struct.pack("=Qqqqq", t.data_ptr(), *runs))
+        if not isinstance(t, torch.Tensor) or t.get_device() != index:
+            _on(t, f"states[{i}]", dev)
+        layout = (t.shape, t.stride(), t.dtype)
+        if layout != last:
+            if len(layout[0]) < 1 or layout[0][0] != R:
+                raise ValueError(f"states[{i}] must have {R} rows")
+            runs = _runs(*layout[:2], t.element_size()) if t.numel() > 0 else ()
+            if runs is None:
+                raise ValueError(f"states[{i}]: more than one gap in a row's order in memory")
+            last = layout
+        if runs:
+            rows += (t.data_ptr(), *runs)
     if not rows:
         return
-    status = _status(status, dev)
-    rc = _abi.beam_reorder(b"".join(rows), len(rows), B, K, parents.data_ptr(),
-                           status.data_ptr(), _stream(dev))
+    if status is not None:
+        _status(status, dev)
+    rc = _abi.beam_reorder(struct.pack("=" + "Qqqqq" * (len(rows) // 5), *rows), len(rows) // 5, B,
+                           K, parents.data_ptr(), None if status is None else status.data_ptr(),
+                           _stream(dev))
     _abi.check(rc, "beam_reorder")

@@ -25,9 +25,9 @@
 namespace flce {
 
 constexpr int kBeamThreads = 256;
-constexpr int kBeamElems = 32;                          // of a thread
-constexpr int kBeamChunk = kBeamThreads * kBeamElems;   // of a block
-constexpr int kBeamMost = 64;                           // beams of a request, and `num`
+constexpr int kBeamLong = 32, kBeamShort = 8;  // elements of a thread
+constexpr int kBeamMost = 64;                  // beams of a request, and `num`
+constexpr int kBeamFew = 16;                   // `num` up to which threads go by fours
 constexpr int64_t kBeamVocab = int64_t(1) << 20;
 constexpr int kBeamMergeThreads = 512;
 
@@ -70,12 +70,18 @@ __device__ __forceinline__ bool row_counts(const BeamArgs& a, int64_t row) {
   return !(a.finished != nullptr && a.finished[row] != 0) && s > -INFINITY && s < INFINITY;
 }
 
-template <typename T>
+// ELEMS elements to a thread.  The block's threads, four together where `num` is at
+// most kBeamFew, are groups; the num-th largest of the groups' largest keys is a bound
+// that the chunk's best num keys reach, and at most num groups have keys that do.
+// Bound by the latency of a block's few steps, where the blocks of an SM overlap: XX.
+template <typename T, int ELEMS>
 __global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
-  constexpr int VEC = 16 / sizeof(T), NV = kBeamElems / VEC;
+  constexpr int VEC = 16 / sizeof(T), NV = ELEMS / VEC;
+  constexpr int kWarps = kBeamThreads / 32;
   __shared__ uint64_t tops[kBeamThreads];
-  __shared__ uint64_t best[kBeamMost * kBeamElems];
-  __shared__ float red[kBeamThreads / 32];
+  __shared__ uint64_t best[kBeamMost * ELEMS > kBeamFew * 4 * ELEMS ? kBeamMost * ELEMS
+                                                                     : kBeamFew * 4 * ELEMS];
+  __shared__ float2 red[kWarps];
   __shared__ uint64_t least_sh;
   __shared__ int count;
   const int64_t row = blockIdx.x / a.chunks;
@@ -85,13 +91,16 @@ __global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   // chunks begin on 16-byte boundaries, `off` elements before the row for the first
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T);
-  const int64_t c0 = static_cast<int64_t>(chunk) * kBeamChunk - off;
-  float v[kBeamElems];
+  const int64_t c0 = static_cast<int64_t>(chunk) * (kBeamThreads * ELEMS) - off;
+  const int64_t first = c0 + threadIdx.x * VEC;  // the thread's first, then VEC * threads on
+  const int64_t step = kBeamThreads * VEC;
+  const bool inside = c0 >= 0 && c0 + kBeamThreads * ELEMS <= a.V;
+  float v[ELEMS];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int64_t j = c0 + (k * kBeamThreads + threadIdx.x) * VEC;
+    const int64_t j = first + k * step;
     float f[VEC];
-    if (j >= 0 && j + VEC <= a.V) {
+    if (inside || (j >= 0 && j + VEC <= a.V)) {
       Elem<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z + j)), f);
     } else {
 #pragma unroll
@@ -102,60 +111,73 @@ __global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
     for (int e = 0; e < VEC; ++e) v[k * VEC + e] = f[e];
   }
   if (threadIdx.x == 0) count = 0;
-  // the maximum, and the thread's largest key
   float m = v[0];
 #pragma unroll
-  for (int i = 1; i < kBeamElems; ++i) m = fmaxf(m, v[i]);
-  uint64_t top = 0;  // below every key
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < kBeamElems; ++i) {
-    const int64_t j = c0 + ((i / VEC) * kBeamThreads + threadIdx.x) * VEC + i % VEC;
-    nan |= v[i] != v[i];
-    if (j >= 0 && j < a.V) {
-      const uint64_t key = beam_key(v[i], static_cast<uint32_t>(j));
-      top = key > top ? key : top;
-    }
-  }
-  tops[threadIdx.x] = top;
-  float bm = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-  if (lane == 0) red[warp] = bm;
-  __syncthreads();
-  bm = red[0];
-#pragma unroll
-  for (int w = 1; w < kBeamThreads / 32; ++w) bm = fmaxf(bm, red[w]);
-  __syncthreads();
-  // NaN and +infinity make the sum NaN; a chunk of -infinity has the sum 0
+  for (int i = 1; i < ELEMS; ++i) m = fmaxf(m, v[i]);
+  // the sum of exponentials: NaN and +infinity make it NaN, nothing but -infinity 0
   float s = 0.0f;
-  if (bm > -INFINITY) {
+  if (m > -INFINITY) {
 #pragma unroll
-    for (int i = 0; i < kBeamElems; ++i) s += ex2((v[i] - bm) * kLog2e);
+    for (int i = 0; i < ELEMS; ++i) s += ex2((v[i] - m) * kLog2e);
+  } else {
+#pragma unroll
+    for (int i = 0; i < ELEMS; ++i)
+      if (v[i] != v[i]) s = v[i];
   }
-  if (nan) s = __int_as_float(0x7fffffff);
+  float wm = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+  if (m > -INFINITY) s *= ex2((m - wm) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) red[warp] = s;
-  // the num-th largest of the threads' largest keys: at most num threads hold keys
-  // that are not smaller, and the chunk's best num are among these
-  int rank = 0;
-  for (int i = 0; i < kBeamThreads; ++i) rank += tops[i] > top ? 1 : 0;
-  if (rank == a.num - 1) least_sh = top;  // of empty threads (0) any
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0.0f;
-    for (int w = 0; w < kBeamThreads / 32; ++w) s += red[w];
-    a.sums[row * a.chunks + chunk] = make_float2(bm, s);
-  }
-  // fewer keyed threads than num: all keys count
-  const int keyed = __syncthreads_count(top != 0);
-  const uint64_t least = keyed >= a.num ? least_sh : 1;
-  if (top >= least) {
+  if (lane == 0) red[warp] = make_float2(wm, s);
+  // the thread's largest key (0, below every key, without an element): the largest
+  // logit, of equal ones the first
+  uint64_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kBeamElems; ++i) {
-      const int64_t j = c0 + ((i / VEC) * kBeamThreads + threadIdx.x) * VEC + i % VEC;
-      if (j < 0 || j >= a.V) continue;
+  for (int i = ELEMS - 1; i >= 0; --i) {
+    const int64_t j = first + (i / VEC) * step + i % VEC;
+    if (v[i] == m && (inside || (j >= 0 && j < a.V)))
+      top = beam_key(v[i], static_cast<uint32_t>(j));
+  }
+  const bool by_four = a.num <= kBeamFew;
+  if (by_four) {
+#pragma unroll
+    for (int o = 1; o < 4; o *= 2) {
+      const uint64_t other = __shfl_xor_sync(0xffffffffu, top, o);
+      top = other > top ? other : top;
+    }
+    if ((threadIdx.x & 3) == 0) tops[threadIdx.x / 4] = top;
+  } else {
+    tops[threadIdx.x] = top;
+  }
+  __syncthreads();
+  const int groups = by_four ? kBeamThreads / 4 : kBeamThreads;
+  if (threadIdx.x < groups) {
+    const uint64_t mine = tops[threadIdx.x];
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < groups; ++i) rank += tops[i] > mine ? 1 : 0;
+    // (fewer groups with an element than num: 0, which every key reaches)
+    if (rank < a.num && mine == 0) least_sh = 0;
+    if (rank == a.num - 1 && mine != 0) least_sh = mine;
+  }
+  if (threadIdx.x == kBeamThreads - 1) {
+    float bm = red[0].x, bs = 0.0f;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, red[w].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      bs += red[w].x > -INFINITY ? red[w].y * ex2((red[w].x - bm) * kLog2e) : red[w].y;
+    a.sums[row * a.chunks + chunk] = make_float2(bm, bs);
+  }
+  __syncthreads();
+  const uint64_t least = least_sh;
+  if (top >= least && top != 0) {
+#pragma unroll
+    for (int i = 0; i < ELEMS; ++i) {
+      const int64_t j = first + (i / VEC) * step + i % VEC;
+      if (!inside && (j < 0 || j >= a.V)) continue;
       const uint64_t key = beam_key(v[i], static_cast<uint32_t>(j));
       if (key >= least) best[atomicAdd(&count, 1)] = key;
     }
@@ -170,19 +192,6 @@ __global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
     if (r < a.num) out[r] = key;
   }
   for (int i = n + threadIdx.x; i < a.num; i += kBeamThreads) out[i] = 0;
-}
-
-// How many of the `n` keys, largest first, are larger than `key`.
-__device__ __forceinline__ int larger(const uint64_t* keys, int n, uint64_t key) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (keys[mid] > key)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  return lo;
 }
 
 // The lowest num tokens, all at -infinity, but one that goes first.
@@ -229,15 +238,31 @@ __global__ void __launch_bounds__(kBeamMergeThreads) beam_merge_kernel(BeamArgs 
         token[k * num + i] = nth_token(i, ended, a.pad);
       }
     } else {
-      for (int i = lane; i < all; i += 32) keys[i] = a.keys[row * all + i];
+      // a chunk's last key is a bound: its num keys reach it.  The keys that reach the
+      // largest bound are moved together, and counted off against each other.
+      const uint64_t* from = a.keys + row * all;
+      uint64_t least = 1;  // (a short chunk's places hold 0)
+      for (int c = lane; c < a.chunks; c += 32) {
+        const uint64_t last = from[c * num + num - 1];
+        least = last > least ? last : least;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, least, o);
+        least = other > least ? other : least;
+      }
+      int n = 0;
+      for (int i = lane; i - lane < all; i += 32) {
+        const uint64_t key = i < all ? from[i] : 0;
+        const unsigned in = __ballot_sync(0xffffffffu, key >= least);
+        if (key >= least) keys[n + __popc(in & ((1u << lane) - 1))] = key;
+        n += __popc(in);
+      }
       __syncwarp();
-      for (int i = lane; i < all; i += 32) {
+      for (int i = lane; i < n; i += 32) {
         const uint64_t key = keys[i];
-        if (key == 0) continue;  // a short chunk's place
-        const int own = i / num;
-        int rank = i - own * num;
-        for (int c = 0; c < a.chunks && rank < num; ++c)
-          if (c != own) rank += larger(keys + c * num, num, key);
+        int rank = 0;
+        for (int o = 0; o < n; ++o) rank += keys[o] > key ? 1 : 0;
         if (rank < num) {
           score[k * num + rank] = base + static_cast<double>(key_logit(key));
           token[k * num + rank] = key_token(key);
@@ -349,15 +374,22 @@ __global__ void __launch_bounds__(kReorderThreads)
 
 // ------------------------------------------------------------------------ host
 
-static int64_t beam_chunks(int64_t V) {
+// Elements of a thread: long chunks where they fill the SMs (XX), else short ones.
+static int beam_elems(int64_t R, int64_t V) {
+  const bool fill = R * (V / (kBeamThreads * kBeamLong)) >= 2 * sm_count();
+  return fill || V > kBeamVocab / 2 ? kBeamLong : kBeamShort;  // (the merge holds a row's keys)
+}
+
+static int64_t beam_chunks(int64_t V, int elems) {
   // a row may begin inside a 16-byte block: its first chunk is up to 7 elements short
-  return (V + 7 + kBeamChunk - 1) / kBeamChunk;
+  const int64_t chunk = kBeamThreads * elems;
+  return (V + 7 + chunk - 1) / chunk;
 }
 
 static bool beam_sizes(int64_t B, int64_t K, int64_t V, int64_t num) {
   return B >= 0 && B <= 0x7fffffff / kBeamMost && K >= 1 && K <= kBeamMost && V >= 1 &&
          V <= kBeamVocab && num >= 1 && num <= kBeamMost && num <= K * V &&
-         B * K * beam_chunks(V) <= 0x7fffffff;
+         B * K * beam_chunks(V, kBeamShort) <= 0x7fffffff;
 }
 
 template <typename U>
@@ -416,7 +448,7 @@ using namespace flce;
 
 extern "C" size_t beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V, int64_t num) {
   if (!beam_sizes(B, K, V, num) || B == 0) return 0;
-  const size_t lists = static_cast<size_t>(B * K * beam_chunks(V));
+  const size_t lists = static_cast<size_t>(B * K * beam_chunks(V, beam_elems(B * K, V)));
   return round_up(lists * (num * sizeof(uint64_t) + sizeof(float2)), 256);
 }
 
@@ -454,19 +486,21 @@ extern "C" int beam_select(const void* logits, int dt, int64_t B, int64_t K, int
   BeamArgs a{};
   a.logits = logits, a.V = V, a.ld = ld, a.scores = scores, a.finished = finished;
   a.pad = pad_id, a.K = static_cast<int>(K), a.num = static_cast<int>(num);
-  a.chunks = static_cast<int>(beam_chunks(V));
+  const int elems = beam_elems(R, V);
+  a.chunks = static_cast<int>(beam_chunks(V, elems));
   a.keys = static_cast<uint64_t*>(ws);
   a.sums = reinterpret_cast<float2*>(a.keys + R * a.chunks * num);
   a.out_scores = out_scores, a.out_tokens = out_tokens, a.out_parents = out_parents;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(a.chunks * R);
-  if (dt == FLCE_BF16)
-    beam_rows_kernel<__nv_bfloat16><<<grid, kBeamThreads, 0, s>>>(a);
-  else
-    beam_rows_kernel<float><<<grid, kBeamThreads, 0, s>>>(a);
+  auto* rows = dt == FLCE_BF16 ? elems == kBeamLong ? beam_rows_kernel<__nv_bfloat16, kBeamLong>
+                                                    : beam_rows_kernel<__nv_bfloat16, kBeamShort>
+               : elems == kBeamLong ? beam_rows_kernel<float, kBeamLong>
+                                    : beam_rows_kernel<float, kBeamShort>;
+  rows<<<grid, kBeamThreads, 0, s>>>(a);
   // a warp for each beam, where their keys fit shared memory together
   const int64_t list = static_cast<int64_t>(a.chunks) * num * 8, best = K * num * 12;
-  constexpr int64_t kMost = 200 * 1024;  // the most: 129 chunks of 64, 4096 best, 113 KB
+  constexpr int64_t kMost = 200 * 1024;  // at least 257 chunks of 64 and 4096 best: 176 KB
   const int warps = static_cast<int>(
       std::max<int64_t>(1, std::min<int64_t>({kBeamMergeThreads / 32, K, (kMost - best) / list})));
   static std::atomic<uint64_t> raised{0};
@@ -480,7 +514,7 @@ extern "C" int beam_reorder(const flce_beam_state_t* states, int n, int64_t B, i
                             const int64_t* parents, int32_t* status, flce_stream_t stream) {
   if (n < 0 || B < 0 || K < 1 || K > kBeamMost || B > 0x7fffffff / kBeamMost) return FLCE_ESHAPE;
   if (n > 0 && states == nullptr) return FLCE_EINVAL;
-  if (n > 0 && B > 0 && (parents == nullptr || status == nullptr)) return FLCE_EINVAL;
+  if (n > 0 && B > 0 && parents == nullptr) return FLCE_EINVAL;
   if (!aligned(parents, 8) || !aligned(status, 4)) return FLCE_EALIGN;
   const int64_t R = B * K;
   constexpr int64_t kFar = int64_t(1) << 60;

@@ -140,7 +140,8 @@ def test_beam_reorder(abi):
                                 status, None)
     good = (A, 64, 1, 0, 64)
     assert call(good) == call((A, 64, 2, 32, 20)) == call((A, 8, 2, 64, 8)) == ECUDA
-    assert call(good, parents=None) == call(good, status=None) == call((0, 64, 1, 0, 64)) == EINVAL
+    assert call(good, parents=None) == call((0, 64, 1, 0, 64)) == EINVAL
+    assert call(good, status=None) == ECUDA
     assert call(good, parents=B + 4) == call(good, status=C + 2) == EALIGN
     assert call(good, K=0) == call(good, K=65) == call(good, B_=-1) == call(good, n=-1) == ESHAPE
     for bad in ((A, 63, 1, 0, 64), (A, 64, 2, 10, 20), (A, 64, 2, 32, -1), (A, -64, 1, 0, 64),
