@@ -75,7 +75,7 @@ __device__ __forceinline__ bool row_counts(const BeamArgs& a, int64_t row) {
 // that the chunk's best num keys reach, and at most num groups have keys that do.
 // Bound by the latency of a block's few steps, where the blocks of an SM overlap: XX.
 template <typename T, int ELEMS>
-__global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) {
   constexpr int VEC = 16 / sizeof(T), NV = ELEMS / VEC;
   constexpr int kWarps = kBeamThreads / 32;
   __shared__ uint64_t tops[kBeamThreads];
@@ -91,24 +91,26 @@ __global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   // chunks begin on 16-byte boundaries, `off` elements before the row for the first
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T);
-  const int64_t c0 = static_cast<int64_t>(chunk) * (kBeamThreads * ELEMS) - off;
-  const int64_t first = c0 + threadIdx.x * VEC;  // the thread's first, then VEC * threads on
-  const int64_t step = kBeamThreads * VEC;
-  const bool inside = c0 >= 0 && c0 + kBeamThreads * ELEMS <= a.V;
+  const int V = static_cast<int>(a.V);
+  const int c0 = chunk * (kBeamThreads * ELEMS) - off;
+  constexpr int step = kBeamThreads * VEC;
+  const int first = c0 + static_cast<int>(threadIdx.x) * VEC;  // the thread's, then step on
+  const bool inside = c0 >= 0 && c0 + kBeamThreads * ELEMS <= V;
   float v[ELEMS];
+  if (inside) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int64_t j = first + k * step;
-    float f[VEC];
-    if (inside || (j >= 0 && j + VEC <= a.V)) {
-      Elem<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z + j)), f);
-    } else {
+    for (int k = 0; k < NV; ++k) {
+      float f[VEC];
+      Elem<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z + first + k * step)), f);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        f[e] = j + e >= 0 && j + e < a.V ? Elem<T>::load(z + j + e) : -INFINITY;
+      for (int e = 0; e < VEC; ++e) v[k * VEC + e] = f[e];
     }
+  } else {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[k * VEC + e] = f[e];
+    for (int i = 0; i < ELEMS; ++i) {
+      const int j = first + i / VEC * step + i % VEC;
+      v[i] = j >= 0 && j < V ? Elem<T>::load(z + j) : -INFINITY;
+    }
   }
   if (threadIdx.x == 0) count = 0;
   float m = v[0];
@@ -133,13 +135,13 @@ __global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
   if (lane == 0) red[warp] = make_float2(wm, s);
   // the thread's largest key (0, below every key, without an element): the largest
   // logit, of equal ones the first
-  uint64_t top = 0;
+  int at = -1;
 #pragma unroll
   for (int i = ELEMS - 1; i >= 0; --i) {
-    const int64_t j = first + (i / VEC) * step + i % VEC;
-    if (v[i] == m && (inside || (j >= 0 && j < a.V)))
-      top = beam_key(v[i], static_cast<uint32_t>(j));
+    const int j = first + i / VEC * step + i % VEC;
+    if (v[i] == m && (inside || (j >= 0 && j < V))) at = j;
   }
+  uint64_t top = at >= 0 ? beam_key(m, static_cast<uint32_t>(at)) : 0;
   const bool by_four = a.num <= kBeamFew;
   if (by_four) {
 #pragma unroll
@@ -174,10 +176,12 @@ __global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
   __syncthreads();
   const uint64_t least = least_sh;
   if (top >= least && top != 0) {
+    const float z_least = least != 0 ? key_logit(least) : -INFINITY;
 #pragma unroll
     for (int i = 0; i < ELEMS; ++i) {
-      const int64_t j = first + (i / VEC) * step + i % VEC;
-      if (!inside && (j < 0 || j >= a.V)) continue;
+      if (!(v[i] >= z_least)) continue;
+      const int j = first + i / VEC * step + i % VEC;
+      if (!inside && (j < 0 || j >= V)) continue;
       const uint64_t key = beam_key(v[i], static_cast<uint32_t>(j));
       if (key >= least) best[atomicAdd(&count, 1)] = key;
     }
@@ -192,6 +196,15 @@ __global__ void __launch_bounds__(kBeamThreads) beam_rows_kernel(BeamArgs a) {
     if (r < a.num) out[r] = key;
   }
   for (int i = n + threadIdx.x; i < a.num; i += kBeamThreads) out[i] = 0;
+}
+
+// log(x) for x >= 1, off by an fp32 step of a number below 1, however large x is
+// (double-precision log takes longer than all else here).
+__device__ __forceinline__ double log_of_sum(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const int e = static_cast<int>(u >> 23) - 127;
+  return static_cast<double>(e) * 0.69314718055994531 +
+         static_cast<double>(logf(__uint_as_float((u & 0x7fffffu) | 0x3f800000u)));
 }
 
 // The lowest num tokens, all at -infinity, but one that goes first.
@@ -215,20 +228,33 @@ __global__ void __launch_bounds__(kBeamMergeThreads) beam_merge_kernel(BeamArgs 
     const float s = a.scores[row];
     const bool done = a.finished != nullptr && a.finished[row] != 0;
     double base = -INFINITY;  // score - lse
+    const uint64_t* from = a.keys + row * all;
+    uint64_t least = 1;  // (a short chunk's places hold 0)
     if (row_counts(a, row)) {
       float m = -INFINITY, sum = 0.0f;
-      for (int c = lane; c < a.chunks; c += 32) m = fmaxf(m, a.sums[row * a.chunks + c].x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       for (int c = lane; c < a.chunks; c += 32) {
         const float2 p = a.sums[row * a.chunks + c];
-        sum += p.x > -INFINITY ? p.y * ex2((p.x - m) * kLog2e) : p.y;
+        // a chunk's last key is a bound: its num keys reach it
+        const uint64_t last = from[c * num + num - 1];
+        least = last > least ? last : least;
+        const float to = fmaxf(m, p.x);
+        if (m > -INFINITY) sum *= ex2((m - to) * kLog2e);
+        sum += p.x > -INFINITY ? p.y * ex2((p.x - to) * kLog2e) : p.y;
+        m = to;
       }
+      float wm = m;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+      if (m > -INFINITY) sum *= ex2((m - wm) * kLog2e);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, least, o);
+        least = other > least ? other : least;
+      }
       // a NaN or +infinity among the logits, or nothing but -infinity: no distribution
-      if (m > -INFINITY && m < INFINITY && sum > 0.0f)
-        base = static_cast<double>(s) - (static_cast<double>(m) + log(static_cast<double>(sum)));
+      if (wm > -INFINITY && wm < INFINITY && sum >= 1.0f && sum < INFINITY)
+        base = static_cast<double>(s) - (static_cast<double>(wm) + log_of_sum(sum));
     }
     const bool live = base > -INFINITY;
     if (!live) {
@@ -238,19 +264,8 @@ __global__ void __launch_bounds__(kBeamMergeThreads) beam_merge_kernel(BeamArgs 
         token[k * num + i] = nth_token(i, ended, a.pad);
       }
     } else {
-      // a chunk's last key is a bound: its num keys reach it.  The keys that reach the
-      // largest bound are moved together, and counted off against each other.
-      const uint64_t* from = a.keys + row * all;
-      uint64_t least = 1;  // (a short chunk's places hold 0)
-      for (int c = lane; c < a.chunks; c += 32) {
-        const uint64_t last = from[c * num + num - 1];
-        least = last > least ? last : least;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t other = __shfl_xor_sync(0xffffffffu, least, o);
-        least = other > least ? other : least;
-      }
+      // the keys that reach the largest bound are moved together, and counted off
+      // against each other
       int n = 0;
       for (int i = lane; i - lane < all; i += 32) {
         const uint64_t key = i < all ? from[i] : 0;
