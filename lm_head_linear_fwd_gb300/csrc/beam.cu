@@ -136,10 +136,17 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) 
   // the thread's largest key (0, below every key, without an element): the largest
   // logit, of equal ones the first
   int at = -1;
+  if (inside) {
 #pragma unroll
-  for (int i = ELEMS - 1; i >= 0; --i) {
-    const int j = first + i / VEC * step + i % VEC;
-    if (v[i] == m && (inside || (j >= 0 && j < V))) at = j;
+    for (int i = ELEMS - 1; i >= 0; --i)
+      if (v[i] == m) at = i / VEC * step + i % VEC;
+    if (at >= 0) at += first;  // (all NaN: none)
+  } else {
+#pragma unroll
+    for (int i = ELEMS - 1; i >= 0; --i) {
+      const int j = first + i / VEC * step + i % VEC;
+      if (v[i] == m && j >= 0 && j < V) at = j;
+    }
   }
   uint64_t top = at >= 0 ? beam_key(m, static_cast<uint32_t>(at)) : 0;
   const bool by_four = a.num <= kBeamFew;
@@ -154,12 +161,18 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) 
     tops[threadIdx.x] = top;
   }
   __syncthreads();
-  const int groups = by_four ? kBeamThreads / 4 : kBeamThreads;
-  if (threadIdx.x < groups) {
-    const uint64_t mine = tops[threadIdx.x];
+  {
+    // a group's rank: how many are larger.  By four each of its threads looks at a quarter.
+    const uint64_t mine = by_four ? top : tops[threadIdx.x];
+    const int looked = by_four ? kBeamThreads / 16 : kBeamThreads;
+    const uint64_t* at_tops = tops + (by_four ? (threadIdx.x & 3) * looked : 0);
     int rank = 0;
 #pragma unroll 8
-    for (int i = 0; i < groups; ++i) rank += tops[i] > mine ? 1 : 0;
+    for (int i = 0; i < looked; ++i) rank += at_tops[i] > mine ? 1 : 0;
+    if (by_four) {
+      rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+      rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    }
     // (fewer groups with an element than num: 0, which every key reaches)
     if (rank < a.num && mine == 0) least_sh = 0;
     if (rank == a.num - 1 && mine != 0) least_sh = mine;
@@ -177,13 +190,18 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) 
   const uint64_t least = least_sh;
   if (top >= least && top != 0) {
     const float z_least = least != 0 ? key_logit(least) : -INFINITY;
+    uint32_t reach = 0;  // elements that may
 #pragma unroll
-    for (int i = 0; i < ELEMS; ++i) {
-      if (!(v[i] >= z_least)) continue;
+    for (int i = 0; i < ELEMS; ++i) reach |= v[i] >= z_least ? 1u << i : 0u;
+    while (reach != 0) {
+      const int i = __ffs(reach) - 1;
+      reach &= reach - 1;
+      float x = v[0];
+#pragma unroll
+      for (int q = 1; q < ELEMS; ++q) x = q == i ? v[q] : x;
       const int j = first + i / VEC * step + i % VEC;
-      if (!inside && (j < 0 || j >= V)) continue;
-      const uint64_t key = beam_key(v[i], static_cast<uint32_t>(j));
-      if (key >= least) best[atomicAdd(&count, 1)] = key;
+      const uint64_t key = beam_key(x, static_cast<uint32_t>(j));
+      if (key >= least && j >= 0 && j < V) best[atomicAdd(&count, 1)] = key;
     }
   }
   __syncthreads();
