@@ -7,6 +7,7 @@
 // same teams: vector k of thread l of a team is k * team + l.  A block of 128
 // columns is thus one vector of each of 16 neighbouring lanes (bf16; 32 for fp32),
 // which find its largest magnitude by shuffles; a team has at least that many.
+// Rows that begin inside 16-byte blocks have a kernel of their own.
 // r is rounded to its type before it is squared: the norm is that of the row which
 // the stream keeps and the backward pass reads.
 #include "eight.cuh"
@@ -39,151 +40,265 @@ __device__ __forceinline__ float rounded(float x) {
   return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(x)) : x;
 }
 
-template <typename T, bool kWhole, int kElems, int kRows, bool kQuant>
+// The largest of each of NV values over a group of L lanes: afterwards lane i of the
+// group has that of value i / (L / NV).  Halves of the values are exchanged, so that
+// NV values take about NV + log2(L / NV) shuffles, not NV log2(L).
+template <int NV, int L>
+__device__ __forceinline__ float group_max_of(float (&m)[NV]) {
+  const int lane = threadIdx.x & (L - 1);
+  int o = L / 2;
+#pragma unroll
+  for (int n = NV / 2; n > 0; n /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? m[i] : m[i + n], keep = upper ? m[i + n] : m[i];
+      m[i] = max_nan(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  return group_max_nan<L / NV>(m[0]);
+}
+
+// Rows on 16-byte boundaries.  65536 x 5120 bf16: 362 us with y in 8 bits, 416 in bf16
+// (both 6.5 TB/s); 8192 x 4096 to 8 bits 42 us.  With two rows at a time of 16 elements
+// per thread, as in norm_fwd_kernel, and two divisions per block and lane: 412, 415, 49.
+template <typename T, int kElems, bool kQuant>
 __global__ void __launch_bounds__(kFwdThreads<T>) norm_add_fwd_kernel(NormAddArgs a) {
-  extern __shared__ float4 weights[];  // weight, then the rows' copies
+  extern __shared__ float4 weights[];  // weight, then the row's copies
   constexpr int kPlaces = kRedPlaces<kFwdThreads<T>>;
   __shared__ __align__(16) float2 red[2 * kPlaces];
-  using Copy = RowCopy<T, kWhole, kElems>;
+  using Copy = RowCopy<T, true, kElems>;
   constexpr int VEC = Copy::VEC, NV = Copy::NV, P = VEC / 2;
   constexpr int kLanes = kBlock8 / VEC;  // that hold a block of 128 columns
   const int D = static_cast<int>(a.D);
-  const int nvec = (D + VEC - 1) / VEC;
+  const int nvec = D / VEC;
   const Team team(a.team, nvec, red, kPlaces);
   const int64_t all = static_cast<int64_t>(gridDim.x) * a.teams;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * a.teams + team.id;  // then row + all, ...
   int rows = rows_from(row, all, a.N);  // of this team, and of the warp's first one
   int turns = a.team < 32 ? __shfl_sync(0xffffffffu, rows, 0) : rows;
   const bool add = a.residual != nullptr;
-  RowPtr<T, kWhole> x(a.x, row, a.ldx, all, team.l), res(a.residual, row, a.ldr, all, team.l);
-  RowPtr<T, kWhole> sum(a.summed, row, a.lds, all, team.l), y(a.y, row, a.ldy, all, team.l);
+  RowPtr<T, true> x(a.x, row, a.ldx, all, team.l), res(a.residual, row, a.ldr, all, team.l);
+  RowPtr<T, true> sum(a.summed, row, a.lds, all, team.l), y(a.y, row, a.ldy, all, team.l);
   const int blocks = (D + kBlock8 - 1) / kBlock8;
   uint8_t* q = kQuant ? a.q + row * a.ldq : nullptr;
   float* scales = kQuant ? a.scales + row * blocks : nullptr;
   float* rstd_out = a.rstd != nullptr ? a.rstd + row : nullptr;
   char* places = reinterpret_cast<char*>(weights + nvec * (VEC / 4));
-  const int row_bytes = Copy::bytes(blockDim.x, a.team);
-  const Copy copy[2] = {Copy(places, team), Copy(places + (kRows - 1) * row_bytes, team)};
-  const Copy rcopy[2] = {Copy(places + kRows * row_bytes, team),
-                         Copy(places + (2 * kRows - 1) * row_bytes, team)};
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    copy[r].clear(false, team);
-    rcopy[r].clear(!add, team);
-    if (r < rows) {
-      copy[r].start(x.p + r * x.step, D, team);
-      if (add) rcopy[r].start(res.p + r * res.step, D, team);
-    }
+  const Copy copy(places, team), rcopy(places + Copy::bytes(blockDim.x, a.team), team);
+  copy.clear(false, team);
+  rcopy.clear(!add, team);
+  if (rows > 0) {
+    copy.start(x.p, D, team);
+    if (add) rcopy.start(res.p, D, team);
   }
   cp_async_commit();
   stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
   bool staged = false;  // the block's weights are there: needed late in the first row
   const float inv_n = 1.0f / static_cast<float>(D);
-  for (int parity = 0; turns > 0; turns -= kRows, rows -= kRows, parity ^= 1) {
-    float2 f[kRows][NV][P];
+  for (int parity = 0; turns > 0; --turns, --rows, parity ^= 1) {
+    float2 f[NV][P];
     cp_async_wait<0>();
-    if (!kWhole) __syncwarp();  // the right neighbour's blocks
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    {
       float2 g[NV][P];
-      copy[r].read(x.p + r * x.step, D, team, f[r]);
-      rcopy[r].read(res.p + r * res.step, D, team, g);
+      copy.read(x.p, D, team, f);
+      rcopy.read(res.p, D, team, g);
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-          const float2 s = __fadd2_rn(f[r][k][e], g[k][e]);
-          f[r][k][e] = make_float2(rounded<T>(s.x), rounded<T>(s.y));
+          const float2 s = __fadd2_rn(f[k][e], g[k][e]);
+          f[k][e] = make_float2(rounded<T>(s.x), rounded<T>(s.y));
         }
     }
-    x.p += kRows * x.step;
-    res.p += kRows * res.step;
-    __syncwarp();
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (kRows + r < rows) {
-        copy[r].start(x.p + r * x.step, D, team);
-        if (add) rcopy[r].start(res.p + r * res.step, D, team);
-      }
-    cp_async_commit();
-    float rstd[2] = {};
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      float2 s[P];  // a chain of additions for each place in a vector
-#pragma unroll
-      for (int e = 0; e < P; ++e) s[e] = both(0.0f);
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-#pragma unroll
-        for (int e = 0; e < P; ++e) s[e] = __ffma2_rn(f[r][k][e], f[r][k][e], s[e]);
-        if (a.summed != nullptr)
-          store_vector<T, kWhole>(sum.p + r * sum.step, k, r < rows, D, team, f[r][k]);
-      }
-      rstd[r] = sum_pairs(s);
+    x.p += x.step;
+    res.p += res.step;
+    if (rows > 1) {
+      copy.start(x.p, D, team);
+      if (add) rcopy.start(res.p, D, team);
     }
-    sum.p += kRows * sum.step;
-    team.sum(rstd[0], rstd[1], parity);
+    cp_async_commit();
+    float2 s[P];  // a chain of additions for each place in a vector
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) rstd[r] = rsqrtf(__fmaf_rn(rstd[r], inv_n, a.eps));
+    for (int e = 0; e < P; ++e) s[e] = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) s[e] = __ffma2_rn(f[k][e], f[k][e], s[e]);
+      if (a.summed != nullptr) store_vector<T, true>(sum.p, k, rows > 0, D, team, f[k]);
+    }
+    sum.p += sum.step;
+    float rstd = sum_pairs(s), unused = 0.0f;
+    team.sum(rstd, unused, parity);
+    rstd = rsqrtf(__fmaf_rn(rstd, inv_n, a.eps));
     if (!staged) __syncthreads();
     staged = true;
+    float m[NV];  // the vectors' largest magnitudes
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float2 w[P];
       weight_vec<VEC>(weights, nvec, min(team.at(k), nvec - 1), w);
+      m[k] = 0.0f;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        float m = 0.0f;
+      for (int e = 0; e < P; ++e) {
+        f[k][e] = __fmul2_rn(__fmul2_rn(f[k][e], both(rstd)), w[e]);
+        if (kQuant) m[k] = max_nan(m[k], max_nan(fabsf(f[k][e].x), fabsf(f[k][e].y)));
+      }
+      if (a.y != nullptr) store_vector<T, true>(y.p, k, rows > 0, D, team, f[k]);
+    }
+    y.p += y.step;
+    if constexpr (kQuant) {
+      // a lane divides for one block: the even ones form its `times`, the odd ones its scale
+      constexpr int kPer = kLanes / NV;
+      const float largest = max_nan(group_max_of<NV, kLanes>(m), kLeast8);
+      const bool odd = (threadIdx.x & 1) != 0;
+      const float mine = __fdiv_rn(odd ? largest : kMax8, odd ? kMax8 : largest);
+      const int in_group = threadIdx.x & (kLanes - 1);
+      const int block = (in_group / kPer * team.size + team.l - in_group) / kLanes;
+      if (in_group % kPer == 1 && rows > 0 && block < blocks) scales[block] = mine;
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const float2 v = __fmul2_rn(__fmul2_rn(f[r][k][e], both(rstd[r])), w[e]);
-          f[r][k][e] = v;
-          if (kQuant) m = max_nan(m, max_nan(fabsf(v.x), fabsf(v.y)));
-        }
-        if (a.y != nullptr)
-          store_vector<T, kWhole>(y.p + r * y.step, k, r < rows, D, team, f[r][k]);
-        if (!kQuant) continue;
-        const Scale8 s(group_max_nan<kLanes>(m));
-        const int j = team.at(k) * VEC;
-        if (r >= rows || j >= D) continue;
-        const int64_t at = r * all;
-        if ((team.l & (kLanes - 1)) == 0) scales[at * blocks + j / kBlock8] = s.scale;
+      for (int k = 0; k < NV; ++k) {
+        const float times =
+            __shfl_sync(0xffffffffu, mine, (threadIdx.x & 31 & ~(kLanes - 1)) + k * kPer);
         uint32_t packed[VEC / 4];
 #pragma unroll
         for (int e = 0; e < P; e += 2) {
-          const float2 u = __fmul2_rn(f[r][k][e], both(s.times));
-          const float2 v = __fmul2_rn(f[r][k][e + 1], both(s.times));
+          const float2 u = __fmul2_rn(f[k][e], both(times));
+          const float2 v = __fmul2_rn(f[k][e + 1], both(times));
           packed[e / 2] = pack_e4m3x4(u.x, u.y, v.x, v.y);
         }
-        uint8_t* to = q + at * a.ldq + j;
-        if (j + VEC <= D) {
+        uint8_t* to = q + team.at(k) * VEC;
+        if (rows > 0 && k < team.mine) {
           if constexpr (VEC == 8)
             *reinterpret_cast<uint2*>(to) = make_uint2(packed[0], packed[1]);
           else
             *reinterpret_cast<uint32_t*>(to) = packed[0];
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (j + e < D) to[e] = static_cast<uint8_t>(packed[e / 4] >> (e % 4 * 8));
         }
       }
-    }
-    y.p += kRows * y.step;
-    if (kQuant) {
-      q += kRows * all * a.ldq;
-      scales += kRows * all * blocks;
+      q += all * a.ldq;
+      scales += all * blocks;
     }
     if (rstd_out != nullptr) {
-      if (team.l == 0) {
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-          if (r < rows) rstd_out[r * all] = rstd[r];
-      }
-      rstd_out += kRows * all;
+      if (team.l == 0 && rows > 0) *rstd_out = rstd;
+      rstd_out += all;
     }
   }
   if (!staged) __syncthreads();  // warps without a row
   cp_async_wait<0>();
+}
+
+// Rows that begin anywhere: element by element, 32 neighbouring ones to a warp's access.
+// A warp has blocks of 128 columns, kAnyBlocks of them at most, in registers; `team`
+// warps have a row.  Bound by those accesses and by what registers leave of an SM's
+// warps: 8191 x 1601 bf16 29 us, to 8 bits 37, fp32 44; four blocks to a warp 33, 48
+// and 67 us, one 32, 42 and 43; whole 16-byte blocks shifted together, as in
+// norm_fwd_kernel, 52, 55 and 75.
+constexpr int kAnyThreads = 512;
+
+template <typename T, int kAnyBlocks, bool kQuant>
+__global__ void __launch_bounds__(kAnyThreads, 2) norm_add_fwd_any_kernel(NormAddArgs a) {
+  __shared__ float red[2][kAnyThreads / 32];
+  __shared__ uint32_t bytes[kQuant ? kAnyThreads / 32 : 1][kBlock8 / 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / a.team, w = warp - team * a.team;
+  const int D = static_cast<int>(a.D), blocks = (D + kBlock8 - 1) / kBlock8;
+  float wt[kAnyBlocks][4];  // the same columns of every row
+#pragma unroll
+  for (int b = 0; b < kAnyBlocks; ++b)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = (w + b * a.team) * kBlock8 + e * 32 + lane;
+      wt[b][e] = j < D ? weight_at(a.weight, a.w_f32, j, 1.0f) : 0.0f;
+    }
+  const int64_t all = static_cast<int64_t>(gridDim.x) * a.teams;
+  const float inv_n = 1.0f / static_cast<float>(D);
+  int parity = 0;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * a.teams + team; i < a.N;
+       i += all, parity ^= 1) {
+    const T* x = static_cast<const T*>(a.x) + i * a.ldx;
+    const T* res = a.residual != nullptr ? static_cast<const T*>(a.residual) + i * a.ldr : nullptr;
+    T* sum = a.summed != nullptr ? static_cast<T*>(a.summed) + i * a.lds : nullptr;
+    T* y = a.y != nullptr ? static_cast<T*>(a.y) + i * a.ldy : nullptr;
+    float f[kAnyBlocks][4];
+#pragma unroll
+    for (int b = 0; b < kAnyBlocks; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = (w + b * a.team) * kBlock8 + e * 32 + lane;
+        f[b][e] = j < D ? Elem<T>::load(x + j) : 0.0f;
+      }
+    if (res != nullptr) {
+#pragma unroll
+      for (int b = 0; b < kAnyBlocks; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = (w + b * a.team) * kBlock8 + e * 32 + lane;
+          if (j < D) f[b][e] = rounded<T>(f[b][e] + Elem<T>::load(res + j));
+        }
+    }
+    float s[4] = {};
+#pragma unroll
+    for (int b = 0; b < kAnyBlocks; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = (w + b * a.team) * kBlock8 + e * 32 + lane;
+        s[e] = __fmaf_rn(f[b][e], f[b][e], s[e]);
+        if (sum != nullptr && j < D) Elem<T>::store(sum + j, f[b][e]);
+      }
+    float total = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (a.team > 1) {
+      if (lane == 0) red[parity][warp] = total;
+      named_barrier(1 + team, a.team * 32);
+      total = 0.0f;
+      for (int k = 0; k < a.team; ++k) total += red[parity][team * a.team + k];
+    }
+    const float rstd = rsqrtf(__fmaf_rn(total, inv_n, a.eps));
+    float m[kAnyBlocks];
+#pragma unroll
+    for (int b = 0; b < kAnyBlocks; ++b) {
+      m[b] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = (w + b * a.team) * kBlock8 + e * 32 + lane;
+        f[b][e] = f[b][e] * rstd * wt[b][e];
+        if (y != nullptr && j < D) Elem<T>::store(y + j, f[b][e]);
+        if (kQuant) m[b] = max_nan(m[b], fabsf(f[b][e]));
+      }
+    }
+    if constexpr (kQuant) {
+      // a lane divides for one block, as above
+      constexpr int kPer = 32 / kAnyBlocks;
+      const float largest = max_nan(group_max_of<kAnyBlocks, 32>(m), kLeast8);
+      const bool odd = (lane & 1) != 0;
+      const float mine = __fdiv_rn(odd ? largest : kMax8, odd ? kMax8 : largest);
+      const int mine_block = w + lane / kPer * a.team;
+      if (lane % kPer == 1 && mine_block < blocks) a.scales[i * blocks + mine_block] = mine;
+      uint8_t* q = a.q + i * a.ldq;
+      uint8_t* own = reinterpret_cast<uint8_t*>(bytes[warp]);
+#pragma unroll
+      for (int b = 0; b < kAnyBlocks; ++b) {
+        const float times = __shfl_sync(0xffffffffu, mine, b * kPer);
+        const int j = (w + b * a.team) * kBlock8 + lane * 4;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const uint32_t two =
+              pack_e4m3x2(__fmul_rn(f[b][e], times), __fmul_rn(f[b][e + 1], times));
+          own[e * 32 + lane] = static_cast<uint8_t>(two);
+          own[e * 32 + 32 + lane] = static_cast<uint8_t>(two >> 8);
+        }
+        __syncwarp();
+        if (j + 4 <= D) {
+          *reinterpret_cast<uint32_t*>(q + j) = bytes[warp][lane];
+        } else {
+          for (int e = 0; j + e < D; ++e) q[j + e] = own[lane * 4 + e];
+        }
+      }
+    }
+    if (lane == 0 && w == 0 && a.rstd != nullptr) a.rstd[i] = rstd;
+  }
 }
 
 // Rows too wide to hold: one block per row, which is read again for the norm (the
@@ -243,10 +358,11 @@ __global__ void __launch_bounds__(kLongThreads) norm_add_fwd_long_kernel(NormAdd
 }
 
 // Launches norm_add_fwd_kernel; returns 1 (nothing launched) when a row does not fit.
-template <typename T, bool kWhole, int kElems, int kRows, bool kQuant>
-static int launch_norm_add_k(NormAddArgs a, cudaStream_t s) {
+template <typename T, bool kQuant>
+static int launch_norm_add_whole(NormAddArgs a, cudaStream_t s) {
+  constexpr int kElems = kFwdLaneLong;
   if (a.D > int64_t(kFwdThreads<T>) * kElems) return 1;
-  auto* kernel = norm_add_fwd_kernel<T, kWhole, kElems, kRows, kQuant>;
+  auto* kernel = norm_add_fwd_kernel<T, kElems, kQuant>;
   static std::atomic<uint64_t> raised{0};
   const int rc = raise_smem(kernel, kSmemMost, raised);
   if (rc != FLCE_OK) return rc;
@@ -256,8 +372,7 @@ static int launch_norm_add_k(NormAddArgs a, cudaStream_t s) {
   a.team = p.team;
   a.teams = p.teams;
   const int threads = p.team * p.teams;
-  const size_t smem =
-      weight_bytes(a.D) + 2 * kRows * RowCopy<T, kWhole, kElems>::bytes(threads, p.team);
+  const size_t smem = weight_bytes(a.D) + 2 * RowCopy<T, true, kElems>::bytes(threads, p.team);
   if (smem > kSmemMost) return 1;
   kernel<<<static_cast<unsigned>(p.blocks), threads, smem, s>>>(a);
   return launch_status("norm_add_fwd_kernel launch");
@@ -266,15 +381,26 @@ static int launch_norm_add_k(NormAddArgs a, cudaStream_t s) {
 template <typename T, bool kQuant>
 static int launch_norm_add(NormAddArgs a, int dt, cudaStream_t s) {
   auto aligned_rows = [dt](const void* p, int64_t ld) { return p == nullptr || whole(dt, p, ld); };
-  const bool w = aligned_rows(a.x, a.ldx) && aligned_rows(a.residual, a.ldr) &&
-                 aligned_rows(a.summed, a.lds) && aligned_rows(a.y, a.ldy) &&
-                 whole(dt, nullptr, a.D);
-  int rc = w ? launch_norm_add_k<T, true, kFwdLane, 2, kQuant>(a, s)
-             : launch_norm_add_k<T, false, kFwdLane, 2, kQuant>(a, s);
-  if (rc == 1)
-    rc = w ? launch_norm_add_k<T, true, kFwdLaneLong, 1, kQuant>(a, s)
-           : launch_norm_add_k<T, false, kFwdLaneLong, 1, kQuant>(a, s);
-  if (rc != 1) return rc;
+  if (aligned_rows(a.x, a.ldx) && aligned_rows(a.residual, a.ldr) &&
+      aligned_rows(a.summed, a.lds) && aligned_rows(a.y, a.ldy) && whole(dt, nullptr, a.D)) {
+    const int rc = launch_norm_add_whole<T, kQuant>(a, s);
+    if (rc != 1) return rc;
+  }
+  // two blocks of 128 columns to a warp, or four
+  for (int per = 2; per <= 4; per += 2) {
+    const int64_t warps = (blocks8(a.D) + per - 1) / per;  // of a row
+    if (warps > kAnyThreads / 32) continue;
+    a.team = static_cast<int>(warps);
+    a.teams = std::max(1, 8 / a.team);
+    const int threads = 32 * a.team * a.teams;
+    // as many blocks as there is room for, rows in turn
+    const int64_t grid =
+        std::min<int64_t>((a.N + a.teams - 1) / a.teams, sm_count() * (1024 / threads));
+    auto* kernel =
+        per == 2 ? norm_add_fwd_any_kernel<T, 2, kQuant> : norm_add_fwd_any_kernel<T, 4, kQuant>;
+    kernel<<<static_cast<unsigned>(grid), threads, 0, s>>>(a);
+    return launch_status("norm_add_fwd_any_kernel launch");
+  }
   const int grid = static_cast<int>(std::min<int64_t>(a.N, sm_count() * 8));
   norm_add_fwd_long_kernel<T><<<grid, kLongThreads, 0, s>>>(a);
   return launch_status("norm_add_fwd_long_kernel launch");
