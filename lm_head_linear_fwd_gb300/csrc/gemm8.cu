@@ -1,9 +1,12 @@
-// The product of matrices in 8 bits: kernels and calls (gemm8.cuh has the formula).
+// The product of matrices in 8 bits: the kernel for few tokens and the calls (gemm8.cuh
+// has the formula, gemm8_pair.cuh the kernel for many).
 //
 // The weights are the 128 rows of the instruction's first operand and the tokens its
 // columns, 16 to 128 of them: for a few tokens the weights stream once through a deep
 // ring, and what is formed per thread is a row of weights, so that neighbouring
-// lanes write neighbouring elements of y.
+// lanes write neighbouring elements of y.  Bound by the weights' bytes and a start of
+// some 8 us: 1 x 4096 x 128256 85 us (6.2 TB/s), 32 x 5120 x 151936 132 us (6.0).
+// Issuing several blocks' copies together, for longer runs of a row, changed nothing.
 #include <algorithm>
 
 #include "gemm8.cuh"
@@ -351,6 +354,34 @@ static int map8(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64
   return FLCE_OK;
 }
 
+// Few tiles: a cluster of CTAs to each, while there are SMs and each has two blocks (1 x
+// 4096 x 4096: 16.6 us with a CTA to each of the 32 tiles, 7.2 in a captured graph with
+// four).
+static int split_of(int64_t tiles, int64_t blocks) {
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= sm_count() && blocks >= 4 * split) split *= 2;
+  return split;
+}
+
+// Tokens of a tile (0: a tile of gemm8_pair_kernel).  Up to 64 tokens one tile has them
+// all, and the weights are read once.  More than that go by 64 where this makes one
+// round of the SMs at most, and else to the pairs (M x N x 4096 in captured graphs: 200
+// x 4096 15 us, on pairs 20; 300 x 4096 27 and 20; 128 x 16384 27 and 21), but where
+// the pairs' second multiplication for scales of single rows costs more than half a
+// tile of zeros (128 x 128256: 174 us with tiles of 128 tokens, 187 on pairs).  Smaller
+// tiles where all these CTAs fill less than half of the SMs (77 x 768 x 1601: 6.4 us by
+// 16, 7.7 by 32, 8.9 by 64).
+static int tile_tokens(int64_t M, int64_t N, int64_t blocks, int b_rows) {
+  const int64_t tiles_n = (N + kG8Rows - 1) / kG8Rows, sms = sm_count();
+  int bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  if (M > 64 && (M + 63) / 64 * tiles_n > sms) return b_rows == 1 && M <= 128 ? 128 : 0;
+  for (; bn > 16; bn /= 2) {
+    const int64_t tiles = (M + bn - 1) / bn * tiles_n;
+    if (2 * tiles * split_of(tiles, blocks) >= sms) break;
+  }
+  return bn;
+}
+
 template <int BN>
 static int launch_gemm8(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb,
                         int64_t K, cudaStream_t s) {
@@ -364,10 +395,7 @@ static int launch_gemm8(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_
   g.tiles_m = (g.M + BN - 1) / BN;
   g.tiles_n = (g.N + kG8Rows - 1) / kG8Rows;
   const int64_t tiles = g.tiles_m * g.tiles_n;
-  // Few tiles: a cluster of CTAs to each, while there are SMs and each has two blocks
-  // (1 x 4096 x 4096: 16.6 us alone, XX in clusters of four)
-  g.split = 1;
-  while (g.split < 8 && tiles * g.split * 2 <= sm_count() && g.blocks >= 4 * g.split) g.split *= 2;
+  g.split = split_of(tiles, g.blocks);
   if (g.split == 1) {
     gemm8_kernel<BN><<<static_cast<unsigned>(std::min<int64_t>(tiles, sm_count())), G::kThreads,
                        G::kSmemBytes, s>>>(mb, ma, g);
@@ -480,10 +508,13 @@ extern "C" int gemm8(const uint8_t* a, int64_t lda, const float* a_scales, int64
   g.bias = bias, g.bias_f32 = dt_bias == FLCE_F32;
   g.y = y, g.ldy = ldy, g.y_f32 = dt_y == FLCE_F32, g.accumulate = accumulate, g.status = status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (M <= 16) return launch_gemm8<16>(g, a, lda, b, ldb, K, s);
-  if (M <= 32) return launch_gemm8<32>(g, a, lda, b, ldb, K, s);
-  if (M <= 64) return launch_gemm8<64>(g, a, lda, b, ldb, K, s);
-  if (M <= 128) return launch_gemm8<128>(g, a, lda, b, ldb, K, s);
-  return b_rows == 1 ? launch_gemm8_pair<true>(g, a, lda, b, ldb, K, s)
-                     : launch_gemm8_pair<false>(g, a, lda, b, ldb, K, s);
+  switch (tile_tokens(M, N, blocks, b_rows)) {
+    case 16: return launch_gemm8<16>(g, a, lda, b, ldb, K, s);
+    case 32: return launch_gemm8<32>(g, a, lda, b, ldb, K, s);
+    case 64: return launch_gemm8<64>(g, a, lda, b, ldb, K, s);
+    case 128: return launch_gemm8<128>(g, a, lda, b, ldb, K, s);
+    default:
+      return b_rows == 1 ? launch_gemm8_pair<true>(g, a, lda, b, ldb, K, s)
+                         : launch_gemm8_pair<false>(g, a, lda, b, ldb, K, s);
+  }
 }
