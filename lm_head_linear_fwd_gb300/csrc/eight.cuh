@@ -32,6 +32,25 @@ __device__ __forceinline__ float group_max_nan(float m) {
   return m;
 }
 
+// The largest of each of NV values over a group of L lanes: afterwards lane i of the
+// group has that of value i / (L / NV).  Halves of the values are exchanged, so that
+// NV values take about NV + log2(L / NV) shuffles, not NV log2(L).
+template <int NV, int L>
+__device__ __forceinline__ float group_max_of(float (&m)[NV]) {
+  const int lane = threadIdx.x & (L - 1);
+  int o = L / 2;
+#pragma unroll
+  for (int n = NV / 2; n > 0; n /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? m[i] : m[i + n], keep = upper ? m[i + n] : m[i];
+      m[i] = max_nan(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  return group_max_nan<L / NV>(m[0]);
+}
+
 struct Scale8 {
   float scale, times;
   __device__ __forceinline__ explicit Scale8(float largest) {

@@ -344,11 +344,6 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
         const uint32_t from = lanes + buf * 128;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          ulonglong2 c[4];
-          if (kCols) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) c[p] = c2[j * 4 + p];
-          }
           uint64_t v[8];
           tmem_ld16_pairs(from + 16 * j, v);
           if (j == 3 && !last && !slot_done) {
@@ -363,7 +358,7 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
           }
 #pragma unroll
           for (int p = 0; p < 8; ++p) {
-            if (kCols) v[p] = mul_pair(v[p], p & 1 ? c[p / 2].y : c[p / 2].x);
+            if (kCols) v[p] = mul_pair(v[p], reinterpret_cast<const uint64_t*>(c2)[j * 8 + p]);
             fma_pair(v[p], s2, sums[j * 8 + p]);
           }
         }

@@ -40,25 +40,6 @@ __device__ __forceinline__ float rounded(float x) {
   return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(x)) : x;
 }
 
-// The largest of each of NV values over a group of L lanes: afterwards lane i of the
-// group has that of value i / (L / NV).  Halves of the values are exchanged, so that
-// NV values take about NV + log2(L / NV) shuffles, not NV log2(L).
-template <int NV, int L>
-__device__ __forceinline__ float group_max_of(float (&m)[NV]) {
-  const int lane = threadIdx.x & (L - 1);
-  int o = L / 2;
-#pragma unroll
-  for (int n = NV / 2; n > 0; n /= 2, o /= 2) {
-    const bool upper = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float give = upper ? m[i] : m[i + n], keep = upper ? m[i + n] : m[i];
-      m[i] = max_nan(keep, __shfl_xor_sync(0xffffffffu, give, o));
-    }
-  }
-  return group_max_nan<L / NV>(m[0]);
-}
-
 // Rows on 16-byte boundaries.  65536 x 5120 bf16: 362 us with y in 8 bits, 416 in bf16
 // (both 6.5 TB/s); 8192 x 4096 to 8 bits 42 us.  With two rows at a time of 16 elements
 // per thread, as in norm_fwd_kernel, and two divisions per block and lane: 412, 415, 49.

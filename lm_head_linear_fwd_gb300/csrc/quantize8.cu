@@ -99,26 +99,39 @@ __global__ void __launch_bounds__(kQThreads) quantize8_kernel(Quantize8Args a) {
   }
 
   // by rows
-  if (a.q != nullptr || (kT && !kSquare)) {
+  float row_times = block_times;  // !kSquare: of row i in lane i * kPer of the row's lanes
+  constexpr int kRows = kRuns * 8, kPer = kLanes / kRows;
+  if (!kSquare) {
+    float m[kRows];
 #pragma unroll
-    for (int i = 0; i < kRuns * 8; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       float v[VEC];
       raw[i].unpack(v);
-      float times = block_times;
-      if (!kSquare) {
-        float m = 0.0f;
+      m[i] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          m = max_nan(m, fabsf(v[e]));
-          if (kT) down[e] = max_nan(down[e], fabsf(v[e]));
-        }
-        if (a.q != nullptr) {
-          const Scale8 s(group_max_nan<kLanes>(m));
-          times = s.times;
-          if (lane % kLanes == 0 && first + i < rows) a.scales[(r0 + first + i) * bc + tc] = s.scale;
-        }
+      for (int e = 0; e < VEC; ++e) {
+        m[i] = max_nan(m[i], fabsf(v[e]));
+        if (kT) down[e] = max_nan(down[e], fabsf(v[e]));
       }
-      if (a.q == nullptr || first + i >= rows) continue;
+    }
+    if (a.q != nullptr) {
+      // a lane divides for one row: the even ones form its `times`, the odd ones its scale
+      const float largest = max_nan(group_max_of<kRows, kLanes>(m), kLeast8);
+      const bool odd = (lane & 1) != 0;
+      row_times = __fdiv_rn(odd ? largest : kMax8, odd ? kMax8 : largest);
+      const int r = first + lane % kLanes / kPer;
+      if (odd && r < rows) a.scales[(r0 + r) * bc + tc] = row_times;
+    }
+  }
+  if (a.q != nullptr) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float times =
+          kSquare ? block_times
+                  : __shfl_sync(0xffffffffu, row_times, (lane & ~(kLanes - 1)) + i * kPer);
+      if (first + i >= rows) continue;
+      float v[VEC];
+      raw[i].unpack(v);
       uint32_t packed[VEC / 4];
 #pragma unroll
       for (int e = 0; e < VEC; e += 4)
@@ -138,57 +151,64 @@ __global__ void __launch_bounds__(kQThreads) quantize8_kernel(Quantize8Args a) {
       }
     }
   }
-  if (!kT) return;
-
-  // transposed
-  float times[VEC];
+  if constexpr (kT) {
+    // transposed
+    float times[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) times[e] = block_times;
-  if (!kSquare) {
+    for (int e = 0; e < VEC; ++e) times[e] = block_times;
+    if (!kSquare) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) tops[first / (8 * kRuns)][col + e] = down[e];
-    __syncthreads();
-    for (int c = threadIdx.x; c < kBlock8; c += kQThreads) {
-      float m = 0.0f;
+      for (int e = 0; e < VEC; ++e) tops[first / (8 * kRuns)][col + e] = down[e];
+      __syncthreads();
+      {
+        // two threads to a column: one forms its `times`, the other its scale
+        static_assert(kQThreads == 2 * kBlock8, "a pair of threads to a column");
+        const int c = threadIdx.x / 2;
+        const bool odd = (threadIdx.x & 1) != 0;
+        float m = kLeast8;
 #pragma unroll
-      for (int w = 0; w < 16 / kRuns; ++w) m = max_nan(m, tops[w][c]);
-      const Scale8 s(m);
-      if (c < cols) a.scales_t[(c0 + c) * ((a.R + kBlock8 - 1) / kBlock8) + tr] = s.scale;
-      tops[0][c] = s.times;
+        for (int w = 0; w < 16 / kRuns; ++w) m = max_nan(m, tops[w][c]);
+        const float mine = __fdiv_rn(odd ? m : kMax8, odd ? kMax8 : m);
+        __syncwarp();  // the pair has read its column
+        if (!odd)
+          tops[0][c] = mine;
+        else if (c < cols)
+          a.scales_t[(c0 + c) * ((a.R + kBlock8 - 1) / kBlock8) + tr] = mine;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) times[e] = tops[0][col + e];
+    }
+#pragma unroll
+    for (int run = 0; run < kRuns; ++run) {
+      float v[8][VEC];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) raw[run * 8 + i].unpack(v[i]);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[h] = pack_e4m3x4(__fmul_rn(v[4 * h][e], times[e]), __fmul_rn(v[4 * h + 1][e], times[e]),
+                             __fmul_rn(v[4 * h + 2][e], times[e]),
+                             __fmul_rn(v[4 * h + 3][e], times[e]));
+        bytes[unit8<VEC>(col + e, first / 8 + run)] = make_uint2(w[0], w[1]);
+      }
     }
     __syncthreads();
+    for (int i = threadIdx.x; i < kBlock8 * 8; i += kQThreads) {
+      const int c = i / 8, u = i % 8 * 2;  // two units: 16 rows
+      if (c >= cols || u * 8 >= rows) continue;
+      const uint2 lo = bytes[unit8<VEC>(c, u)], hi = bytes[unit8<VEC>(c, u + 1)];
+      uint8_t* to = a.qt + (c0 + c) * a.ldqt + r0 + u * 8;
+      if (u * 8 + 16 <= rows) {
+        *reinterpret_cast<uint4*>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) times[e] = tops[0][col + e];
-  }
-#pragma unroll
-  for (int run = 0; run < kRuns; ++run) {
-    float v[8][VEC];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) raw[run * 8 + i].unpack(v[i]);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      uint32_t w[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[h] = pack_e4m3x4(__fmul_rn(v[4 * h][e], times[e]), __fmul_rn(v[4 * h + 1][e], times[e]),
-                           __fmul_rn(v[4 * h + 2][e], times[e]),
-                           __fmul_rn(v[4 * h + 3][e], times[e]));
-      bytes[unit8<VEC>(col + e, first / 8 + run)] = make_uint2(w[0], w[1]);
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kBlock8 * 8; i += kQThreads) {
-    const int c = i / 8, u = i % 8 * 2;  // two units: 16 rows
-    if (c >= cols || u * 8 >= rows) continue;
-    const uint2 lo = bytes[unit8<VEC>(c, u)], hi = bytes[unit8<VEC>(c, u + 1)];
-    uint8_t* to = a.qt + (c0 + c) * a.ldqt + r0 + u * 8;
-    if (u * 8 + 16 <= rows) {
-      *reinterpret_cast<uint4*>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    } else {
-      const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (u * 8 + k < rows) to[k] = static_cast<uint8_t>(w[k / 4] >> (k % 4 * 8));
+        for (int k = 0; k < 16; ++k)
+          if (u * 8 + k < rows) to[k] = static_cast<uint8_t>(w[k / 4] >> (k % 4 * 8));
+      }
     }
   }
 }
