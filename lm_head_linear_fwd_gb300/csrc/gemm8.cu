@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(Gemm8Geo<BN>::kThreads, 1)
       // read), and takes the shares as [from][column][row].
       const int part = BN / g.split;
       cluster_sync();
-      const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>((rank * part * kG8Rows + row) * 4);
+      const uint32_t mine =
+          smem_u32(smem) + static_cast<uint32_t>((rank * part * kG8Rows + row) * 4);
 #pragma unroll
       for (int j = 0; j < G::kCols; ++j) {
         const int c = c0 + j;
@@ -421,7 +422,7 @@ static int launch_gemm8(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_
 template <bool kCols>
 static int launch_gemm8_pair(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_t* b,
                              int64_t ldb, int64_t K, cudaStream_t s) {
-  using G = Gemm8Pair;
+  using G = Gemm8Pair<kCols>;
   auto* kernel = gemm8_pair_kernel<kCols>;
   CUtensorMap ma, mb, my;
   int rc = map8(&ma, a, g.M, K, lda, 128);

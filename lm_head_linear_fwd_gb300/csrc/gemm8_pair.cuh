@@ -11,12 +11,13 @@
 // memory.
 //
 // Bound by the way of a block's sums from the tensor cores through the registers: of
-// about 1000 cycles per block the products take 512 and the additions 256 (packed
-// fp32 at half rate); the rest are the waits between them, which two warps to a
-// scheduler (their sums fill the registers) hide in part.  8192 x 4096 x 16384, scales
-// of b for 128 rows: 446 us, 2.46 PFLOP/s; for each row, twice the arithmetic: 780 us.
-// The scales loaded by the adding threads took 723 us (they spill); sixteen warps of 64
-// columns 548 and 755 us; all 256 columns issued by one thread 445 and 823 us.
+// about 800 cycles per block the products take 512 and the additions 256 (packed fp32
+// at half rate); the rest are the waits between them, which two warps to a scheduler
+// (their sums fill the registers) hide in part.  8192 x 4096 x 16384, scales of b for
+// 128 rows: 368 us, 3.0 PFLOP/s; for each row, twice the arithmetic, 675 us.  The
+// scales loaded by the adding threads took 723 us (they spill), handed over for four
+// blocks at a time 385 us; tensor memory read without a load ahead 438; one lane in the
+// issuing warp's loop 446; sixteen adding warps of 64 columns 414 and 754.
 //
 // Barriers as in the pair kernel of tc_gemm.cuh:
 //   full[s]   leader: both CTAs' copies have landed     empty[s]  both: both halves' were read
@@ -30,6 +31,8 @@
 
 namespace flce {
 
+// kCols: b has a scale for each of its rows (the tile's columns); else one for 128.
+template <bool kCols>
 struct Gemm8Pair {
   // A warpgroup for copies and products, two that add up.  The registers of 384 threads
   // at launch, 168 each (65536 / 384, down to a multiple of eight), are dealt anew: 56
@@ -39,9 +42,9 @@ struct Gemm8Pair {
   static constexpr int kStageA = 128 * 128;
   static constexpr int kStageBytes = 2 * kStageA;
   static constexpr int kStages = 4;
-  static constexpr int kAhead = 4;  // blocks whose scales are loaded together
-  static constexpr int kRing = 3;   // of these
-  static constexpr int kScales = 128 + 256;  // a block's: of the rows, and of the columns
+  static constexpr int kAhead = kCols ? 4 : 8;  // blocks whose scales are handed over together
+  static constexpr int kRing = kCols ? 3 : 2;   // of these
+  static constexpr int kScales = 128 + (kCols ? 256 : 4);  // a block's: rows, then columns
   static constexpr int kScaleBytes = kRing * kAhead * kScales * 4;
   static constexpr int kStaging = 8 * 2 * 4096;
   static constexpr int kSmemBytes = kStages * kStageBytes + kStaging + kScaleBytes + 1024;
@@ -57,25 +60,34 @@ __device__ __forceinline__ void mma_8bit_pair(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
-// 16 columns of fp32 of this thread's lane of tensor memory, as pairs.
-__device__ __forceinline__ void tmem_ld16_pairs(uint32_t taddr, uint64_t (&v)[8]) {
+// 16 columns of fp32 of this thread's lane of tensor memory, to be waited for; and the
+// wait for all loads of this thread, which gives the last one's values as pairs.
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "{\n\t.reg .b32 t<16>;\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{t0, t1, t2, t3, t4, t5, t6, t7, t8, t9, t10, t11, t12, t13, t14, t15}, [%8];\n\t"
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(const uint32_t (&r)[16], uint64_t (&v)[8]) {
+  asm volatile(
       "tcgen05.wait::ld.sync.aligned;\n\t"
-      "mov.b64 %0, {t0, t1};\n\t"
-      "mov.b64 %1, {t2, t3};\n\t"
-      "mov.b64 %2, {t4, t5};\n\t"
-      "mov.b64 %3, {t6, t7};\n\t"
-      "mov.b64 %4, {t8, t9};\n\t"
-      "mov.b64 %5, {t10, t11};\n\t"
-      "mov.b64 %6, {t12, t13};\n\t"
-      "mov.b64 %7, {t14, t15};\n\t"
-      "}"
+      "mov.b64 %0, {%8, %9};\n\t"
+      "mov.b64 %1, {%10, %11};\n\t"
+      "mov.b64 %2, {%12, %13};\n\t"
+      "mov.b64 %3, {%14, %15};\n\t"
+      "mov.b64 %4, {%16, %17};\n\t"
+      "mov.b64 %5, {%18, %19};\n\t"
+      "mov.b64 %6, {%20, %21};\n\t"
+      "mov.b64 %7, {%22, %23};\n\t"
       : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]), "=l"(v[6]),
         "=l"(v[7])
-      : "r"(taddr)
+      : "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
       : "memory");
 }
 // Packed fp32 arithmetic on pairs.
@@ -106,7 +118,8 @@ __device__ __forceinline__ void mbar_arrive_read(uint32_t cluster_addr) {
 }
 
 // The scales of four blocks from k on, of 128 rows from `first` on: each to its block's
-// place.  All loads are under way before the first is waited for.
+// place, kScales further.  All loads are under way before the first is waited for.
+template <int kScales>
 __device__ __forceinline__ void stage_scales(const float* scales, int64_t first, int64_t rows,
                                              int k, int blocks, bool wide, int lane, float* to) {
   float4 v[4];
@@ -128,20 +141,19 @@ __device__ __forceinline__ void stage_scales(const float* scales, int64_t first,
   for (int i = 0; i < 4; ++i) {
     float* at = to + 32 * i + lane;
     at[0] = v[i].x;
-    at[Gemm8Pair::kScales] = v[i].y;
-    at[2 * Gemm8Pair::kScales] = v[i].z;
-    at[3 * Gemm8Pair::kScales] = v[i].w;
+    at[kScales] = v[i].y;
+    at[2 * kScales] = v[i].z;
+    at[3 * kScales] = v[i].w;
   }
 }
 
-// kCols: b has a scale for each of its rows (the tile's columns); else one for 128.
 template <bool kCols>
-__global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
+__global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
     gemm8_pair_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ CUtensorMap map_y, const Gemm8Args g,
                       const int group_m, const int tma_store) {
-  using G = Gemm8Pair;
+  using G = Gemm8Pair<kCols>;
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full_bar[S], empty_bar[S], sum_bar[4], read_bar[4], drain_bar[2];
@@ -276,7 +288,7 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
     }
   } else if (warp < 4) {
     // scales
-    const bool wide = g.blocks % G::kAhead == 0 &&
+    const bool wide = g.blocks % 4 == 0 &&
                       ((reinterpret_cast<uintptr_t>(g.a_scales) |
                         reinterpret_cast<uintptr_t>(g.b_scales)) & 15) == 0;
     uint32_t slot = 0, phase = 0;
@@ -294,11 +306,15 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
           break;
         }
         float* to = scale_ring + slot * G::kAhead * G::kScales;
-        stage_scales(g.a_scales, m0, g.M, k, g.blocks, wide, lane, to);
-        if (kCols) {
-          stage_scales(g.b_scales, n0, g.N, k, g.blocks, wide, lane, to + 128);
-          stage_scales(g.b_scales, n0 + 128, g.N, k, g.blocks, wide, lane, to + 256);
-        } else if (lane < 2 * G::kAhead) {
+        for (int c = k; c < min(k + G::kAhead, g.blocks); c += 4) {
+          float* at = to + (c - k) * G::kScales;
+          stage_scales<G::kScales>(g.a_scales, m0, g.M, c, g.blocks, wide, lane, at);
+          if (kCols) {
+            stage_scales<G::kScales>(g.b_scales, n0, g.N, c, g.blocks, wide, lane, at + 128);
+            stage_scales<G::kScales>(g.b_scales, n0 + 128, g.N, c, g.blocks, wide, lane, at + 256);
+          }
+        }
+        if (!kCols && lane < 2 * G::kAhead) {
           const int64_t n = min(n0 / kBlock8 + lane % 2, (g.N - 1) / kBlock8);
           const int at = lane / 2;
           to[at * G::kScales + 128 + lane % 2] =
@@ -337,29 +353,36 @@ __global__ void __launch_bounds__(Gemm8Pair::kThreads, 1)
         const bool last = k + 1 == g.blocks, slot_done = last || at == G::kAhead - 1;
         const float s = kCols ? row_s : __fmul_rn(row_s, col_s);
         const uint64_t s2 = pair_of(s, s);
-        const ulonglong2* c2 = reinterpret_cast<const ulonglong2*>(scales + 128 + half * 128);
+        const uint64_t* c2 = reinterpret_cast<const uint64_t*>(scales + 128 + half * 128);
         good &= mbar_wait(&sum_bar[2 * half + buf], buf_phase, abort_flag);
         __syncwarp();
         tc_fence_after();
         const uint32_t from = lanes + buf * 128;
+        // !kCols: kLoad columns are on their way while those before them are added (kCols
+        // has no registers for that: 729 against 675 us)
+        constexpr int kLoad = 16, kLast = 128 / kLoad - 1;
+        uint32_t r[2][kLoad];
+        if (!kCols) tmem_ld_start(from, r[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint64_t v[8];
-          tmem_ld16_pairs(from + 16 * j, v);
-          if (j == 3 && !last && !slot_done) {
+        for (int j = 0; j <= kLast; ++j) {
+          uint64_t v[kLoad / 2];
+          if (kCols) tmem_ld_start(from + kLoad * j, r[j & 1]);
+          tmem_ld_wait(r[j & 1], v);
+          if (!kCols && j < kLast) tmem_ld_start(from + kLoad * (j + 1), r[(j + 1) & 1]);
+          if (j == kLast / 2 && !last && !slot_done) {
             row_s = scales[G::kScales + quad * 32 + lane];
             if (!kCols) col_s = scales[G::kScales + 128 + half];
           }
-          if (j == 7) {
+          if (j == kLast) {
             // the last columns are here: the next block but one may be formed
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_read(read_leader + (2 * half + buf) * 8u);
           }
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            if (kCols) v[p] = mul_pair(v[p], reinterpret_cast<const uint64_t*>(c2)[j * 8 + p]);
-            fma_pair(v[p], s2, sums[j * 8 + p]);
+          for (int p = 0; p < kLoad / 2; ++p) {
+            if (kCols) v[p] = mul_pair(v[p], c2[j * (kLoad / 2) + p]);
+            fma_pair(v[p], s2, sums[j * (kLoad / 2) + p]);
           }
         }
         buf_phase ^= buf;
