@@ -902,9 +902,11 @@ static int launch_norm_bwd(NormBwdArgs a, int dt, cudaStream_t s) {
   return launch_status("norm_bwd launch");
 }
 
+// other: a launch to be tried first, which returns 1 where it does not apply.
 template <bool kCenter, bool kAdd>
 static int norm_bwd(NormBwdArgs a, int dt, int wdt, void* ws, size_t ws_bytes,
-                    flce_stream_t stream) {
+                    flce_stream_t stream,
+                    int (*other)(NormBwdArgs, int, cudaStream_t) = nullptr) {
   if (!valid_dtype(dt) || !valid_dtype(wdt)) return FLCE_EDTYPE;
   if (a.accumulate != 0 && a.accumulate != 1) return FLCE_EINVAL;
   if (a.N < 0 || a.D < 1) return FLCE_ESHAPE;
@@ -937,6 +939,10 @@ static int norm_bwd(NormBwdArgs a, int dt, int wdt, void* ws, size_t ws_bytes,
   a.part = cols ? static_cast<float*>(ws) : nullptr;
   a.w_f32 = wdt == FLCE_F32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (other != nullptr && a.N > 0) {
+    const int done = other(a, dt, s);
+    if (done != 1) return done;
+  }
   return dt == FLCE_BF16 ? launch_norm_bwd<__nv_bfloat16, kCenter, kAdd>(a, dt, s)
                          : launch_norm_bwd<float, kCenter, kAdd>(a, dt, s);
 }

@@ -147,7 +147,10 @@ def test_backward(lh, N, D, dtype, wdtype, pad, shift):
     gw = torch.full((D,), 0.25, device="cuda")
     lh.rms_norm_add_bwd(r, gy, gs, rstd, w, grad_x=wide[:, 2:2 + D], grad_weight=gw,
                         accumulate=True)
-    assert torch.equal(wide[:, 2:2 + D], o.grad_x) and torch.equal(gw, 0.25 + o.grad_weight)
+    # (rows that begin elsewhere are added up in another order)
+    R.close(wide[:, 2:2 + D], want, bx + 2 * R.U * (dx.abs() + R.d(gs).abs()) +
+            (R.half(dtype) * (want.abs() + bx) * 1.01 if dtype == BF else 0), "grad_x, wide")
+    R.close(gw, dw[0] + 0.25, dw[1] + R.U * (dw[0].abs() + 0.5), "grad_weight, added")
     assert (wide[:, :2] == 7).all() and (wide[:, 2 + D:] == 7).all()
     plain = lh.rms_norm_bwd(r, gy, rstd, w)
     p = lh.rms_norm_add_bwd(r, gy, None, rstd, w)
