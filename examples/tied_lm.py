@@ -6,7 +6,8 @@ package's operators: ``python examples/tied_lm.py [--steps N] [--vocab V] [--wid
 
 Training writes its own backward: the head's gradient of the table (flce_bwd) and
 the lookup's (embedding_bwd) are summed in one fp32 buffer.  Decoding reads the table
-in 4 bits (head4_quantize, head4_logits), one captured graph per token.  The tokens
+in 4 bits (head4_quantize, head4_logits), one captured graph per token, or, with several
+beams to a sequence, in 8 (quantize8, gemm8, beam_select, beam_reorder_).  The tokens
 follow a random permutation, so what there is to learn is the permutation.
 """
 import argparse
@@ -109,6 +110,33 @@ class Decoder:
         return torch.stack(out)
 
 
+class BeamDecoder:
+    """B sequences of K beams each, from the table in 8 bits; the beams' histories are
+    what moves with them."""
+
+    def __init__(self, model, B, K, length):
+        self.model, self.B, self.K = model, B, K
+        device = model.p["W"].device
+        self.head = lh.quantize8(model.p["W"], 128)
+        self.history = torch.zeros(B * K, length, dtype=torch.int64, device=device)
+        # the first step has one beam to go on from
+        self.start = torch.full((B, K), float("-inf"), device=device)
+        self.start[:, 0] = 0.0
+
+    def run(self, first):
+        """The best history of each sequence after `first` [B], and its score."""
+        model, K = self.model, self.K
+        ids, scores = first.repeat_interleave(K), self.start.flatten()
+        for t in range(self.history.shape[1]):
+            h = lh.quantize8(model.hidden(ids)[-1].y)
+            best = lh.beam_select(lh.gemm8(h, self.head, status=model.status), scores, K)
+            lh.beam_reorder_([self.history[:, :t]] if t else [], best.parents,
+                             status=model.status)
+            ids, scores = best.tokens.flatten(), best.scores.flatten()
+            self.history[:, t] = ids
+        return self.history.view(self.B, K, -1)[:, 0].clone(), best.scores[:, 0]
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=100)
@@ -134,8 +162,11 @@ def main(argv=None):
         first = follows[first]
         want.append(first)
     right = (got == torch.stack(want)).float().mean().item()
+    beams = BeamDecoder(model, 4, 3, 16).run(torch.arange(4, device=device))[0]
     lh.check_status(model.status)
     print(f"decoded from 4 bits: {100 * right:.0f}% of 64 tokens right")
+    same = (beams.t() == torch.stack(want)).float().mean().item()
+    print(f"with 3 beams from 8 bits: {100 * same:.0f}%")
     return [x.item() for x in losses], right
 
 
