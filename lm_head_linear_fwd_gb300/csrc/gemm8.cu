@@ -428,7 +428,8 @@ static int launch_gemm8_pair(Gemm8Args g, const uint8_t* a, int64_t lda, const u
   int rc = map8(&ma, a, g.M, K, lda, 128);
   if (rc == FLCE_OK) rc = map8(&mb, b, g.N, K, ldb, 64);
   const int es = g.y_f32 ? 4 : 2;
-  const bool tma_store = aligned(g.y, 16) && g.ldy * es % 16 == 0;
+  const bool tma_store =
+      aligned(g.y, 16) && g.ldy * es % 16 == 0 && g.ldy * es < (int64_t(1) << 40);
   my = ma;  // not used without tma_store
   if (rc == FLCE_OK && tma_store)
     rc = map8(&my, g.y, g.M, g.N, g.ldy, 32,

@@ -430,6 +430,8 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
         if (n >= g.N || m_first >= g.M) break;
         uint8_t* slab = slabs + next_slab * 4096;
         next_slab ^= 1;
+        // a copy writes whole 16-byte units, also past the last column
+        const bool copy = tma_store && n + slab_cols <= g.N;
         if (tma_store && lane == 0) bulk_wait_read_le1();  // the slab's last store has read it
         __syncwarp();
 #pragma unroll
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
           }
           *reinterpret_cast<uint4*>(slab + lane * 128 + ((j ^ (lane & 7)) << 4)) = u;
         }
-        if (tma_store) {
+        if (copy) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -459,7 +461,8 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
             bulk_commit();
           }
         } else {
-          // rows that a copy cannot start in: element by element, lanes along a row
+          // element by element, lanes along a row
+          if (tma_store && lane == 0) bulk_commit();  // the slabs' stores are counted
           __syncwarp();
           const int rows = static_cast<int>(min(int64_t(32), g.M - m_first));
           const int width = static_cast<int>(min(static_cast<int64_t>(slab_cols), g.N - n));

@@ -101,7 +101,10 @@ def _operand(lh, R0, K, rows, seed, wild=False):
 SIZES = [(1, 1, 1), (1, 128, 128), (1, 300, 257), (2, 129, 1000), (5, 1000, 96), (16, 768, 768),
          (17, 513, 300), (33, 200, 2048), (64, 130, 129), (77, 768, 1601), (100, 2000, 640),
          (128, 128, 4096), (129, 257, 128), (250, 300, 384), (300, 1000, 1601), (513, 640, 100),
-         (1000, 1024, 512), (1, 8000, 64), (3, 64, 9000), (700, 130, 3000)]
+         (1000, 1024, 512), (1, 8000, 64), (3, 64, 9000), (700, 130, 3000),
+         # more tiles than SMs, clusters of each size and tile, both kernels above 64 tokens
+         (3, 30000, 300), (40, 20500, 130), (50, 8192, 512), (20, 4096, 2048), (100, 10000, 200),
+         (70, 10240, 384), (2000, 2600, 400)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -120,10 +123,18 @@ def test_gemm(lh, M, N, K, rows):
         assert torch.equal(wide[:, 2:2 + N], y)
         assert (wide[:, :2] == 7).all() and (wide[:, 2 + N:] == 7).all()
         lh.check_status(st)
+        # rows of whole 16-byte blocks, which the last columns do not fill
+        wide = torch.full((M, E.ceil(N, 8) * 8 + 8), 7.0, dtype=dtype, device="cuda")
+        lh.gemm8(a, b, bias, out=wide[:, :N])
+        assert torch.equal(wide[:, :N], y) and (wide[:, N:] == 7).all()
     base = torch.randn(M, N, generator=g).mul_(1e4).cuda()
     out = base.clone()
     lh.gemm8(a, b, bias, out=out, accumulate=True)
     R.close(out, *E.gemm(a, b, bias, base, F32), "accumulate")
+    wide = torch.full((M, E.ceil(N, 8) * 8 + 8), 7.0, device="cuda")
+    wide[:, :N] = base
+    lh.gemm8(a, b, bias, out=wide[:, :N], accumulate=True)
+    assert torch.equal(wide[:, :N], out) and (wide[:, N:] == 7).all()
 
 
 def test_gemm_scales(lh):
