@@ -18,7 +18,9 @@
  * accumulate = 1 adds to the existing C (beta = 1), 0 overwrites it.
  *
  * All pointers are device pointers, 16-byte aligned; lda*sizeof(dt) and
- * ldb*sizeof(dt) must be multiples of 16 and ldc a multiple of 4.  The call is
+ * ldb*sizeof(dt) must be multiples of 16 and ldc a multiple of 4.  Rows of C are
+ * written in whole units of 16 bytes: where N is no multiple of 4, up to three
+ * columns past the Nth are overwritten.  The call is
  * enqueued on `stream`, allocates nothing and never synchronises.  Errors are
  * reported as in flce.h (a timed-out wait inside the kernel writes
  * FLCE_ETIMEOUT to *status).

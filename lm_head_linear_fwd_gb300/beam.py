@@ -53,9 +53,9 @@ def beam_select(logits, scores, beams, num=None, *, finished=None, pad_id=0, out
         if finished.dtype not in (torch.bool, torch.uint8):
             raise TypeError("finished must be bool or uint8")
     if out is None:
-        out = BeamOut(torch.empty(B, num, dtype=torch.float32, device=dev),
-                      torch.empty(B, num, dtype=torch.int64, device=dev),
-                      torch.empty(B, num, dtype=torch.int64, device=dev))
+        tokens = torch.empty(B, num, dtype=torch.int64, device=dev)
+        out = BeamOut(torch.empty(B, num, dtype=torch.float32, device=dev), tokens,
+                      torch.empty_like(tokens))
     else:
         for t, name, dt in ((out.scores, "scores", torch.float32),
                             (out.tokens, "tokens", torch.int64),
@@ -105,20 +105,21 @@ def beam_reorder_(states, parents, *, status=None) -> None:
     index = dev.index
     B, K = parents.shape
     R = B * K
-    rows, last, runs = [], None, None  # caches mostly come in one shape
+    rows, shape, stride, dtype, runs = [], None, None, None, ()
     for i, t in enumerate(states):
         if not isinstance(t, torch.Tensor) or t.get_device() != index:
             _on(t, f"states[{i}]", dev)
-        layout = (t.shape, t.stride(), t.dtype)
-        if layout != last:
-            if len(layout[0]) < 1 or layout[0][0] != R:
+        # caches mostly come in one layout
+        if t.shape != shape or t.stride() != stride or t.dtype is not dtype:
+            shape, stride, dtype = t.shape, t.stride(), t.dtype
+            if len(shape) < 1 or shape[0] != R:
                 raise ValueError(f"states[{i}] must have {R} rows")
-            runs = _runs(*layout[:2], t.element_size()) if t.numel() > 0 else ()
+            runs = _runs(shape, stride, t.element_size()) if t.numel() > 0 else ()
             if runs is None:
                 raise ValueError(f"states[{i}]: more than one gap in a row's order in memory")
-            last = layout
         if runs:
-            rows += (t.data_ptr(), *runs)
+            rows.append(t.data_ptr())
+            rows += runs
     if not rows:
         return
     if status is not None:

@@ -47,26 +47,31 @@ def _matrix8(q, name, device):
     """A matrix in 8 bits: rows, columns, row stride."""
     if not isinstance(q, Quant8):
         raise ValueError(f"{name} must be a Quant8")
-    data, scales = q.data, q.scales
-    if q.rows not in (1, 128):
+    data, scales, rows = q.data, q.scales, q.rows
+    if rows != 1 and rows != 128:
         raise ValueError(f"{name}.rows must be 1 or 128")
-    R, K, ld = _matrix(data, f"{name}.data", device)
+    R, K, ld = _matrix(data, "data", device)
     if data.dtype is not _E4M3:
         raise TypeError(f"{name}.data must be float8_e4m3fn")
-    _on(scales, f"{name}.scales", device)
-    shape = (R if q.rows == 1 else _ceil(R, 128), _ceil(K, 128))
-    if scales.dtype is not _F32 or scales.shape != shape or not scales.is_contiguous():
-        raise ValueError(f"{name}.scales must be a contiguous float32 {list(shape)} tensor")
-    return R, K, ld if R > 1 else _ceil(K, 16) * 16
+    if not isinstance(scales, torch.Tensor) or scales.get_device() != device.index:
+        _on(scales, f"{name}.scales", device)
+    G = -(-K // 128)
+    if scales.dtype is not _F32 or scales.shape != (R if rows == 1 else -(-R // 128), G) or \
+            not scales.is_contiguous():
+        raise ValueError(f"{name}.scales must be a contiguous float32 tensor: {rows} rows and "
+                         "128 columns to a scale")
+    return R, K, ld if R > 1 else -(-K // 16) * 16
 
 
 def _output8(q, name, R, K, rows, device):
     """An optional caller-owned matrix in 8 bits, or a new one; its row stride."""
     if q is None:
         q = _new8(R, K, rows, device)
-    elif _matrix8(q, name, device)[:2] != (R, K) or q.rows != rows:
+        return q, -(-K // 16) * 16
+    has_R, has_K, ld = _matrix8(q, name, device)
+    if has_R != R or has_K != K or q.rows != rows:
         raise ValueError(f"{name} must be [{R}, {K}] with {rows} rows to a scale")
-    return q, q.data.stride(0) if R > 1 else _ceil(K, 16) * 16
+    return q, ld
 
 
 # ------------------------------------------------- the norm of a residual stream
@@ -88,28 +93,31 @@ def rms_norm_add_fwd(x, residual=None, weight=None, eps=1e-5, *, want_y=True, wa
     bits with a scale per 128 columns.  residual None: the norm of x, which is not
     copied unless ``summed`` is given."""
     N, D, ldx = _matrix(x, "x")
-    dev = x.device
-    wdt = _norm_params(D, weight, None, dev)
-    ldr = lds = ldy = ldq = 0
+    dev, dt = x.device, x.dtype
+    if weight is None:
+        wdt, w = _abi.FLCE_F32, 0
+    else:
+        wdt, w = _dtype_code(_vector(weight, "weight", D, dev)), weight.data_ptr()
+    ldr = lds = ldy = ldq = r = sum_ = y_ = q_ = scales = 0
     if residual is not None:
-        ldr = _matrix(residual, "residual", dev)[2]
-        if residual.shape != (N, D) or residual.dtype is not x.dtype:
+        has_N, has_D, ldr = _matrix(residual, "residual", dev)
+        if has_N != N or has_D != D or residual.dtype is not dt:
             raise ValueError("residual must have the shape and dtype of x")
+        r = residual.data_ptr()
     if residual is not None or summed is not None:
-        summed = _output(summed, "summed", (N, D), x.dtype, dev)
-        lds = _row_stride(summed, "summed", N, D)
+        summed = _output(summed, "summed", (N, D), dt, dev)
+        lds, sum_ = _row_stride(summed, "summed", N, D), summed.data_ptr()
     if want_y or y is not None:
-        y = _output(y, "y", (N, D), x.dtype, dev)
-        ldy = _row_stride(y, "y", N, D)
+        y = _output(y, "y", (N, D), dt, dev)
+        ldy, y_ = _row_stride(y, "y", N, D), y.data_ptr()
     if want_quant or quant is not None:
         quant, ldq = _output8(quant, "quant", N, D, 1, dev)
+        q_, scales = quant.data.data_ptr(), quant.scales.data_ptr()
     elif y is None:
         raise ValueError("one of y and quant must be asked for")
     rstd = _output(rstd, "rstd", (N,), _F32, dev)
-    rc = _call.rms_norm_add_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, _addr(residual), ldr,
-                                _addr(weight), wdt, float(eps), _addr(summed), lds, _addr(y), ldy,
-                                0 if quant is None else quant.data.data_ptr(), ldq,
-                                0 if quant is None else quant.scales.data_ptr(), rstd.data_ptr(),
+    rc = _call.rms_norm_add_fwd(x.data_ptr(), _dtype_code(x), N, D, ldx, r, ldr, w, wdt,
+                                float(eps), sum_, lds, y_, ldy, q_, ldq, scales, rstd.data_ptr(),
                                 _stream(dev))
     _abi.check(rc, "rms_norm_add_fwd")
     return NormAddOut(y, summed, rstd, quant)
