@@ -2,7 +2,7 @@
 // has the formula, gemm8_pair.cuh the kernel for many).
 //
 // The weights are the 128 rows of the instruction's first operand and the tokens its
-// columns, 16 to 128 of them: for a few tokens the weights stream once through a deep
+// columns, 16 to 64 of them: for a few tokens the weights stream once through a deep
 // ring, and what is formed per thread is a row of weights, so that neighbouring
 // lanes write neighbouring elements of y.  Bound by the weights' bytes and a start of
 // some 8 us: 1 x 4096 x 128256 85 us (6.2 TB/s), 32 x 5120 x 151936 132 us (6.0).
@@ -21,14 +21,14 @@ template <int BN>
 struct Gemm8Geo {
   static constexpr int kStageA = kG8Rows * 128;
   static constexpr int kStageBytes = kStageA + BN * 128;
-  static constexpr int kStages = BN == 128 ? 6 : BN == 64 ? 8 : 10;
-  static constexpr int kBufs = BN == 128 ? 2 : 4;  // of a block's sums in tensor memory
-  static constexpr int kTmemCols = BN == 16 ? 64 : BN == 32 ? 128 : 256;
+  static constexpr int kStages = BN == 64 ? 8 : 10;
+  static constexpr int kBufs = 4;  // of a block's sums in tensor memory
+  static constexpr int kTmemCols = kBufs * BN;
   static constexpr int kScaleBytes = 2 * kG8Ahead * BN * 4;
   static constexpr int kSmemBytes = kStages * kStageBytes + kScaleBytes + 1024;
   // Warps that add up: each of two sets of four has half of the columns where they are
-  // many (with one set 128 x 4096 x 4096 took 31 us)
-  static constexpr int kSets = BN >= 64 ? 2 : 1;
+  // many
+  static constexpr int kSets = BN == 64 ? 2 : 1;
   static constexpr int kCols = BN / kSets;  // of a thread
   static constexpr int kAdders = 128 * kSets;
   static constexpr int kThreads = 64 + kAdders;  // and copies, and products
@@ -367,15 +367,13 @@ static int split_of(int64_t tiles, int64_t blocks) {
 // Tokens of a tile (0: a tile of gemm8_pair_kernel).  Up to 64 tokens one tile has them
 // all, and the weights are read once.  More than that go by 64 where this makes one
 // round of the SMs at most, and else to the pairs (M x N x 4096 in captured graphs: 200
-// x 4096 15 us, on pairs 20; 300 x 4096 27 and 20; 128 x 16384 27 and 21), but where
-// the pairs' second multiplication for scales of single rows costs more than half a
-// tile of zeros (128 x 128256: 174 us with tiles of 128 tokens, 187 on pairs).  Smaller
-// tiles where all these CTAs fill less than half of the SMs (77 x 768 x 1601: 6.4 us by
-// 16, 7.7 by 32, 8.9 by 64).
-static int tile_tokens(int64_t M, int64_t N, int64_t blocks, int b_rows) {
+// x 4096 15 us, on pairs 20; 300 x 4096 27 and 20; 128 x 128256 172 and 119, with
+// tiles of 128 tokens 144).  Smaller tiles where all these CTAs fill less than half of
+// the SMs (77 x 768 x 1601: 6.4 us by 16, 7.7 by 32, 8.9 by 64).
+static int tile_tokens(int64_t M, int64_t N, int64_t blocks) {
   const int64_t tiles_n = (N + kG8Rows - 1) / kG8Rows, sms = sm_count();
   int bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-  if (M > 64 && (M + 63) / 64 * tiles_n > sms) return b_rows == 1 && M <= 128 ? 128 : 0;
+  if (M > 64 && (M + 63) / 64 * tiles_n > sms) return 0;
   for (; bn > 16; bn /= 2) {
     const int64_t tiles = (M + bn - 1) / bn * tiles_n;
     if (2 * tiles * split_of(tiles, blocks) >= sms) break;
@@ -419,21 +417,19 @@ static int launch_gemm8(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_
 }
 
 // A lone CTA cannot run half of a pair: as many pairs as can be resident at once.
-template <bool kCols>
+template <bool kCols, bool kTma>
 static int launch_gemm8_pair(Gemm8Args g, const uint8_t* a, int64_t lda, const uint8_t* b,
                              int64_t ldb, int64_t K, cudaStream_t s) {
   using G = Gemm8Pair<kCols>;
-  auto* kernel = gemm8_pair_kernel<kCols>;
+  auto* kernel = gemm8_pair_kernel<kCols, kTma>;
   CUtensorMap ma, mb, my;
   int rc = map8(&ma, a, g.M, K, lda, 128);
   if (rc == FLCE_OK) rc = map8(&mb, b, g.N, K, ldb, 64);
-  const int es = g.y_f32 ? 4 : 2;
-  const bool tma_store =
-      aligned(g.y, 16) && g.ldy * es % 16 == 0 && g.ldy * es < (int64_t(1) << 40);
-  my = ma;  // not used without tma_store
-  if (rc == FLCE_OK && tma_store)
+  my = ma;  // not used without kTma
+  if (rc == FLCE_OK && kTma)
     rc = map8(&my, g.y, g.M, g.N, g.ldy, 32,
-              g.y_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, es);
+              g.y_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              g.y_f32 ? 4 : 2);
   static std::atomic<uint64_t> raised{0};
   if (rc == FLCE_OK) rc = raise_smem(kernel, G::kSmemBytes, raised);
   if (rc != FLCE_OK) return rc;
@@ -466,7 +462,7 @@ static int launch_gemm8_pair(Gemm8Args g, const uint8_t* a, int64_t lda, const u
   }
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)), 1, 1);
   const int group_m = static_cast<int>(std::min<int64_t>(8, g.tiles_m));
-  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, ma, mb, my, g, group_m, tma_store ? 1 : 0),
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, ma, mb, my, g, group_m),
                      "cudaLaunchKernelEx(gemm8_pair_kernel)");
 }
 
@@ -510,13 +506,16 @@ extern "C" int gemm8(const uint8_t* a, int64_t lda, const float* a_scales, int64
   g.bias = bias, g.bias_f32 = dt_bias == FLCE_F32;
   g.y = y, g.ldy = ldy, g.y_f32 = dt_y == FLCE_F32, g.accumulate = accumulate, g.status = status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  switch (tile_tokens(M, N, blocks, b_rows)) {
+  switch (tile_tokens(M, N, blocks)) {
     case 16: return launch_gemm8<16>(g, a, lda, b, ldb, K, s);
     case 32: return launch_gemm8<32>(g, a, lda, b, ldb, K, s);
     case 64: return launch_gemm8<64>(g, a, lda, b, ldb, K, s);
-    case 128: return launch_gemm8<128>(g, a, lda, b, ldb, K, s);
-    default:
-      return b_rows == 1 ? launch_gemm8_pair<true>(g, a, lda, b, ldb, K, s)
-                         : launch_gemm8_pair<false>(g, a, lda, b, ldb, K, s);
+    default: break;
   }
+  const int es = g.y_f32 ? 4 : 2;
+  const bool tma = aligned(y, 16) && ldy * es % 16 == 0 && ldy * es < (int64_t(1) << 40);
+  auto* pairs = b_rows == 1 ? tma ? launch_gemm8_pair<true, true> : launch_gemm8_pair<true, false>
+                : tma       ? launch_gemm8_pair<false, true>
+                            : launch_gemm8_pair<false, false>;
+  return pairs(g, a, lda, b, ldb, K, s);
 }

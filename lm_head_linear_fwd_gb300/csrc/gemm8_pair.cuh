@@ -14,10 +14,10 @@
 // about 800 cycles per block the products take 512 and the additions 256 (packed fp32
 // at half rate); the rest are the waits between them, which two warps to a scheduler
 // (their sums fill the registers) hide in part.  8192 x 4096 x 16384, scales of b for
-// 128 rows: 368 us, 3.0 PFLOP/s; for each row, twice the arithmetic, 675 us.  The
+// 128 rows: 369 us, 3.0 PFLOP/s; for each row, twice the arithmetic, 511 us.  The
 // scales loaded by the adding threads took 723 us (they spill), handed over for four
-// blocks at a time 385 us; tensor memory read without a load ahead 438; one lane in the
-// issuing warp's loop 446; sixteen adding warps of 64 columns 414 and 754.
+// blocks at a time 385 and 529; tensor memory read without a load ahead 438; one lane in the
+// issuing warp's loop 446; sixteen adding warps of 64 columns 414.
 //
 // Barriers as in the pair kernel of tc_gemm.cuh:
 //   full[s]   leader: both CTAs' copies have landed     empty[s]  both: both halves' were read
@@ -42,8 +42,8 @@ struct Gemm8Pair {
   static constexpr int kStageA = 128 * 128;
   static constexpr int kStageBytes = 2 * kStageA;
   static constexpr int kStages = 4;
-  static constexpr int kAhead = kCols ? 4 : 8;  // blocks whose scales are handed over together
-  static constexpr int kRing = kCols ? 3 : 2;   // of these
+  static constexpr int kAhead = 8;  // blocks whose scales are handed over together
+  static constexpr int kRing = 2;   // of these
   static constexpr int kScales = 128 + (kCols ? 256 : 4);  // a block's: rows, then columns
   static constexpr int kScaleBytes = kRing * kAhead * kScales * 4;
   static constexpr int kStaging = 8 * 2 * 4096;
@@ -117,6 +117,12 @@ __device__ __forceinline__ void mbar_arrive_read(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Two pairs from shared memory, here and no earlier (volatile): loaded ahead, the
+// columns' scales take the registers that the sums need (675 against 580 us then).
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+}
+
 // The scales of four blocks from k on, of 128 rows from `first` on: each to its block's
 // place, kScales further.  All loads are under way before the first is waited for.
 template <int kScales>
@@ -147,12 +153,13 @@ __device__ __forceinline__ void stage_scales(const float* scales, int64_t first,
   }
 }
 
-template <bool kCols>
+// kTma: the rows of y can be stored by copies (16-byte addresses and strides).
+template <bool kCols, bool kTma>
 __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
     gemm8_pair_kernel(const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ CUtensorMap map_y, const Gemm8Args g,
-                      const int group_m, const int tma_store) {
+                      const int group_m) {
   using G = Gemm8Pair<kCols>;
   constexpr int S = G::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -306,13 +313,16 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
           break;
         }
         float* to = scale_ring + slot * G::kAhead * G::kScales;
-        for (int c = k; c < min(k + G::kAhead, g.blocks); c += 4) {
-          float* at = to + (c - k) * G::kScales;
-          stage_scales<G::kScales>(g.a_scales, m0, g.M, c, g.blocks, wide, lane, at);
-          if (kCols) {
-            stage_scales<G::kScales>(g.b_scales, n0, g.N, c, g.blocks, wide, lane, at + 128);
-            stage_scales<G::kScales>(g.b_scales, n0 + 128, g.N, c, g.blocks, wide, lane, at + 256);
-          }
+        // the rows' and, each 128, the columns'
+#pragma unroll 1
+        for (int part = 0; part < (kCols ? 3 : 1); ++part) {
+          const float* scales = part == 0 ? g.a_scales : g.b_scales;
+          const int64_t from = part == 0 ? m0 : n0 + (part - 1) * 128;
+          const int64_t rows = part == 0 ? g.M : g.N;
+#pragma unroll 1
+          for (int c = k; c < min(k + G::kAhead, g.blocks); c += 4)
+            stage_scales<G::kScales>(scales, from, rows, c, g.blocks, wide, lane,
+                                     to + (c - k) * G::kScales + part * 128);
         }
         if (!kCols && lane < 2 * G::kAhead) {
           const int64_t n = min(n0 / kBlock8 + lane % 2, (g.N - 1) / kBlock8);
@@ -353,13 +363,12 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
         const bool last = k + 1 == g.blocks, slot_done = last || at == G::kAhead - 1;
         const float s = kCols ? row_s : __fmul_rn(row_s, col_s);
         const uint64_t s2 = pair_of(s, s);
-        const uint64_t* c2 = reinterpret_cast<const uint64_t*>(scales + 128 + half * 128);
         good &= mbar_wait(&sum_bar[2 * half + buf], buf_phase, abort_flag);
         __syncwarp();
         tc_fence_after();
         const uint32_t from = lanes + buf * 128;
-        // !kCols: kLoad columns are on their way while those before them are added (kCols
-        // has no registers for that: 729 against 675 us)
+        // !kCols: kLoad columns are on their way while those before them are added (438
+        // against 385 us; kCols the other way round, 511 and 534)
         constexpr int kLoad = 16, kLast = 128 / kLoad - 1;
         uint32_t r[2][kLoad];
         if (!kCols) tmem_ld_start(from, r[0]);
@@ -379,10 +388,22 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_read(read_leader + (2 * half + buf) * 8u);
           }
+          if constexpr (kCols) {
+            const uint32_t at_cols = smem_u32(scales + 128 + half * 128 + j * kLoad);
 #pragma unroll
-          for (int p = 0; p < kLoad / 2; ++p) {
-            if (kCols) v[p] = mul_pair(v[p], c2[j * (kLoad / 2) + p]);
-            fma_pair(v[p], s2, sums[j * (kLoad / 2) + p]);
+            for (int p = 0; p < kLoad / 2; p += 4) {
+              uint64_t c[4];
+              lds_pairs(at_cols + p * 8, c[0], c[1]);
+              lds_pairs(at_cols + p * 8 + 16, c[2], c[3]);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[p + q] = mul_pair(v[p + q], c[q]);
+                fma_pair(v[p + q], s2, sums[j * (kLoad / 2) + p + q]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int p = 0; p < kLoad / 2; ++p) fma_pair(v[p], s2, sums[j * (kLoad / 2) + p]);
           }
         }
         buf_phase ^= buf;
@@ -431,53 +452,106 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
         uint8_t* slab = slabs + next_slab * 4096;
         next_slab ^= 1;
         // a copy writes whole 16-byte units, also past the last column
-        const bool copy = tma_store && n + slab_cols <= g.N;
-        if (tma_store && lane == 0) bulk_wait_read_le1();  // the slab's last store has read it
+        const bool copy = kTma && n + slab_cols <= g.N;
+        if (kTma && lane == 0) bulk_wait_read_le1();  // the slab's last store has read it
         __syncwarp();
+        if constexpr (kTma) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint4 u;
-          if (g.y_f32) {
-            const float2 a = acc[c * 16 + 2 * j], b = acc[c * 16 + 2 * j + 1];
-            u = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
-                           __float_as_uint(b.y));
-          } else {
-            const int at = (c & 1) * 32 + 4 * j;
-            u = make_uint4(pack_bf16x2(acc[at].x, acc[at].y),
-                           pack_bf16x2(acc[at + 1].x, acc[at + 1].y),
-                           pack_bf16x2(acc[at + 2].x, acc[at + 2].y),
-                           pack_bf16x2(acc[at + 3].x, acc[at + 3].y));
+          for (int j = 0; j < 8; ++j) {
+            uint4 u;
+            if (g.y_f32) {
+              const float2 a = acc[c * 16 + 2 * j], b = acc[c * 16 + 2 * j + 1];
+              u = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                             __float_as_uint(b.y));
+            } else {
+              const int at = (c & 1) * 32 + 4 * j;
+              u = make_uint4(pack_bf16x2(acc[at].x, acc[at].y),
+                             pack_bf16x2(acc[at + 1].x, acc[at + 1].y),
+                             pack_bf16x2(acc[at + 2].x, acc[at + 2].y),
+                             pack_bf16x2(acc[at + 3].x, acc[at + 3].y));
+            }
+            *reinterpret_cast<uint4*>(slab + lane * 128 + ((j ^ (lane & 7)) << 4)) = u;
           }
-          *reinterpret_cast<uint4*>(slab + lane * 128 + ((j ^ (lane & 7)) << 4)) = u;
-        }
-        if (copy) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (g.accumulate)
-              tma_reduce_add_2d(&map_y, slab, static_cast<int>(n), static_cast<int>(m_first));
-            else
-              tma_store_2d(&map_y, slab, static_cast<int>(n), static_cast<int>(m_first));
-            bulk_commit();
+          if (copy) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (g.accumulate)
+                tma_reduce_add_2d(&map_y, slab, static_cast<int>(n), static_cast<int>(m_first));
+              else
+                tma_store_2d(&map_y, slab, static_cast<int>(n), static_cast<int>(m_first));
+              bulk_commit();
+            }
+          } else {
+            // element by element, lanes along a row
+            if (lane == 0) bulk_commit();  // the slabs' stores are counted
+            __syncwarp();
+            const int rows = static_cast<int>(min(int64_t(32), g.M - m_first));
+            const int width = static_cast<int>(min(static_cast<int64_t>(slab_cols), g.N - n));
+            for (int r = 0; r < rows; ++r) {
+              const int64_t at = (m_first + r) * g.ldy + n;
+              for (int e = lane; e < width; e += 32) {
+                const int byte = e * (g.y_f32 ? 4 : 2);
+                const uint8_t* from = slab + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
+                if (g.y_f32) {
+                  float* y = static_cast<float*>(g.y) + at + e;
+                  const float v = *reinterpret_cast<const float*>(from);
+                  *y = g.accumulate ? *y + v : v;
+                } else {
+                  static_cast<uint16_t*>(g.y)[at + e] = *reinterpret_cast<const uint16_t*>(from);
+                }
+              }
+            }
           }
         } else {
-          // element by element, lanes along a row
-          if (tma_store && lane == 0) bulk_commit();  // the slabs' stores are counted
-          __syncwarp();
           const int rows = static_cast<int>(min(int64_t(32), g.M - m_first));
           const int width = static_cast<int>(min(static_cast<int64_t>(slab_cols), g.N - n));
-          for (int r = 0; r < rows; ++r) {
-            const int64_t at = (m_first + r) * g.ldy + n;
-            for (int e = lane; e < width; e += 32) {
-              const int byte = e * (g.y_f32 ? 4 : 2);
-              const uint8_t* from = slab + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-              if (g.y_f32) {
-                float* y = static_cast<float*>(g.y) + at + e;
-                const float v = *reinterpret_cast<const float*>(from);
-                *y = g.accumulate ? *y + v : v;
-              } else {
-                static_cast<uint16_t*>(g.y)[at + e] = *reinterpret_cast<const uint16_t*>(from);
+          const int64_t first_at = m_first * g.ldy + n;
+          // bf16: pairs from the row's first 4-byte boundary on
+          const int64_t row0 =
+              static_cast<int64_t>(reinterpret_cast<uintptr_t>(g.y) >> 1) + first_at;
+          const bool shift = !g.y_f32 && ((row0 + lane * g.ldy) & 1) != 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint4 u;
+            if (g.y_f32) {
+              const float2 a = acc[c * 16 + 2 * j], b = acc[c * 16 + 2 * j + 1];
+              u = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                             __float_as_uint(b.y));
+            } else {
+              const float2* v = acc + (c & 1) * 32;
+              uint32_t w[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int i = 4 * j + q;
+                w[q] = pack_bf16x2(v[i].x, v[i].y);
+                const float next = i < 31 ? v[i + 1 < 32 ? i + 1 : 31].x : 0.0f;
+                if (shift) w[q] = pack_bf16x2(v[i].y, next);
               }
+              u = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            *reinterpret_cast<uint4*>(slab + lane * 128 + ((j ^ (lane & 7)) << 4)) = u;
+          }
+          // word by word, lanes along a row
+          if (shift && lane < rows)
+            Elem<__nv_bfloat16>::store(
+                static_cast<__nv_bfloat16*>(g.y) + first_at + lane * g.ldy, acc[(c & 1) * 32].x);
+          __syncwarp();
+#pragma unroll 4
+          for (int r = 0; r < rows; ++r) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                slab + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+            const int64_t at = first_at + r * g.ldy;
+            if (g.y_f32) {
+              float* y = static_cast<float*>(g.y) + at + lane;
+              if (lane < width) *y = g.accumulate ? *y + __uint_as_float(w) : __uint_as_float(w);
+            } else {
+              const int e = 2 * lane + static_cast<int>((row0 + r * g.ldy) & 1);
+              uint16_t* y = static_cast<uint16_t*>(g.y) + at + e;
+              if (e + 1 < width)
+                *reinterpret_cast<uint32_t*>(y) = w;
+              else if (e < width)
+                *y = static_cast<uint16_t>(w);
             }
           }
         }
