@@ -33,14 +33,11 @@ class Quant8:
     rows: int = 1         # rows to a scale: 1 or 128
 
 
-def _ceil(n, d):
-    return -(-n // d)
-
-
 def _new8(R, K, rows, device):
-    data = torch.empty(R, _ceil(K, 16) * 16, dtype=_E4M3, device=device)
-    return Quant8(data if K % 16 == 0 else data[:, :K],
-                  torch.empty(_ceil(R, rows), _ceil(K, 128), dtype=_F32, device=device), rows)
+    ld = -(-K // 16) * 16
+    return Quant8(torch.empty_strided((R, K), (ld, 1), dtype=_E4M3, device=device),
+                  torch.empty(R if rows == 1 else -(-R // 128), -(-K // 128), dtype=_F32,
+                              device=device), rows)
 
 
 def _matrix8(q, name, device):
