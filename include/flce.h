@@ -3,7 +3,8 @@
  *
  * Two loss operations, each split into a forward and a backward call (and,
  * in the sections at the end, the operators around them: the embedding lookup,
- * the norms, and the head with 4-bit weights):
+ * the norms, the head with 4-bit weights, matrices in 8 bits with the norm that
+ * writes them, and beam search):
  *
  *   ce_logits_*  masked cross-entropy over GIVEN logits [N, V]; the backward can
  *                write the gradient into the logits storage (in place).
