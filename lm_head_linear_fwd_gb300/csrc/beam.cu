@@ -5,7 +5,8 @@
 // at s_k + z_k[v] - lse(z_k); the `num` best of its K V continuations are wanted,
 // best first, of equal ones the one with the lowest k V + v.  Within a beam that
 // order is the logits' own, so the selection splits:
-//   beam_rows_kernel    a block takes a chunk of a row, reads it once, and leaves the
+//   beam_rows_kernel    a block takes a chunk of a row, reads it once (twice where its
+//                       logits rise), and leaves the
 //                       chunk's maximum and sum of exponentials and its `num` best
 //                       tokens, as 64-bit keys: the logit's bits in an order-keeping
 //                       form, then the token's complement, so that keys differ and
@@ -25,7 +26,7 @@
 namespace flce {
 
 constexpr int kBeamThreads = 256;
-constexpr int kBeamLong = 32, kBeamShort = 8;  // elements of a thread
+constexpr int kBeamLong = 32, kBeamShort = 8;  // elements of a thread in a tile
 constexpr int kBeamMost = 64;                  // beams of a request, and `num`
 constexpr int kBeamFew = 16;                   // `num` up to which threads go by fours
 constexpr int64_t kBeamVocab = int64_t(1) << 20;
@@ -56,7 +57,7 @@ struct BeamArgs {
   const float* scores;      // [B K]
   const uint8_t* finished;  // [B K] or null
   int64_t pad;
-  int K, num, chunks;
+  int K, num, chunks, tiles;
   uint64_t* keys;  // [B K, chunks, num]
   float2* sums;    // [B K, chunks]: maximum, sum of exp(z - maximum)
   float* out_scores;
@@ -70,128 +71,105 @@ __device__ __forceinline__ bool row_counts(const BeamArgs& a, int64_t row) {
   return !(a.finished != nullptr && a.finished[row] != 0) && s > -INFINITY && s < INFINITY;
 }
 
-// ELEMS elements to a thread.  The block's threads, four together where `num` is at
-// most kBeamFew, are groups; the num-th largest of the groups' largest keys is a bound
-// that the chunk's best num keys reach, and at most num groups have keys that do.
-// Bound by instructions and by the latency of a block's load and three barriers, four
-// blocks to an SM: 320 x 151936 fp32 52 us of 61 with the merge (3.7 TB/s), 128 x 128256
-// bf16 31.  Chunks of half the length took 83 and 41 us.
+// A block has `tiles` tiles of ELEMS elements to a thread, one after the other.
+// The block's threads, four together where `num` is at most kBeamFew, are groups; the
+// num-th largest of the groups' largest keys of a tile is a bound that the tile's best
+// num keys reach, and at most num groups have keys that do.  The first tile's bound
+// serves the whole chunk: what reaches it is written down without a wait, some num
+// keys to a tile, and ranked at the end.  Where that overflows (rows that rise) the
+// chunk is read again, with a bound and the best num so far for each tile.  Bound by
+// instructions (some 14 per logit), four blocks to an SM: 320 x 151936 fp32 33 of 41 us
+// with the merge (6 TB/s), 128 x 128256 bf16 24 us.  With a bound for every tile, of one
+// to a block, 52 of 61 and 31; eight tiles to a block 43 and 24.
 template <typename T, int ELEMS>
-__global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) {
-  constexpr int VEC = 16 / sizeof(T), NV = ELEMS / VEC;
-  constexpr int kWarps = kBeamThreads / 32;
-  __shared__ uint64_t tops[kBeamThreads];
-  __shared__ uint64_t best[kBeamMost * ELEMS > kBeamFew * 4 * ELEMS ? kBeamMost * ELEMS
-                                                                     : kBeamFew * 4 * ELEMS];
-  __shared__ float2 red[kWarps];
-  __shared__ uint64_t least_sh;
-  __shared__ int count;
-  const int64_t row = blockIdx.x / a.chunks;
-  const int chunk = static_cast<int>(blockIdx.x - row * a.chunks);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (!row_counts(a, row)) return;
-  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-  // chunks begin on 16-byte boundaries, `off` elements before the row for the first
-  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T);
-  const int V = static_cast<int>(a.V);
-  const int c0 = chunk * (kBeamThreads * ELEMS) - off;
-  constexpr int step = kBeamThreads * VEC;
-  const int first = c0 + static_cast<int>(threadIdx.x) * VEC;  // the thread's, then step on
-  const bool inside = c0 >= 0 && c0 + kBeamThreads * ELEMS <= V;
+struct BeamTile {
+  static constexpr int VEC = 16 / sizeof(T), NV = ELEMS / VEC;
+  static constexpr int kSize = kBeamThreads * ELEMS, kStep = kBeamThreads * VEC;
+  // keys that reach a tile's bound, and the best so far
+  static constexpr int kRoom = kBeamMost * ELEMS > kBeamFew * 4 * ELEMS ? kBeamMost * ELEMS
+                                                                        : kBeamFew * 4 * ELEMS;
   float v[ELEMS];
-  if (inside) {
+  int first;    // the thread's first place; -infinity outside the row
+  bool inside;  // the tile lies within the row
+  __device__ __forceinline__ int place(int i) const { return first + i / VEC * kStep + i % VEC; }
+  // begins on a 16-byte boundary
+  __device__ __forceinline__ void load(const T* z, int begin, int V) {
+    first = begin + static_cast<int>(threadIdx.x) * VEC;
+    inside = begin >= 0 && begin + kSize <= V;
+    if (inside) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      float f[VEC];
-      Elem<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z + first + k * step)), f);
+      for (int k = 0; k < NV; ++k) {
+        float f[VEC];
+        Elem<T>::unpack(__ldcs(reinterpret_cast<const uint4*>(z + first + k * kStep)), f);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[k * VEC + e] = f[e];
-    }
-  } else {
+        for (int e = 0; e < VEC; ++e) v[k * VEC + e] = f[e];
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < ELEMS; ++i) {
-      const int j = first + i / VEC * step + i % VEC;
-      v[i] = j >= 0 && j < V ? Elem<T>::load(z + j) : -INFINITY;
-    }
-  }
-  if (threadIdx.x == 0) count = 0;
-  float m = v[0];
-#pragma unroll
-  for (int i = 1; i < ELEMS; ++i) m = fmaxf(m, v[i]);
-  // the sum of exponentials: NaN and +infinity make it NaN, nothing but -infinity 0
-  float s = 0.0f;
-  if (m > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < ELEMS; ++i) s += ex2((v[i] - m) * kLog2e);
-  } else {
-#pragma unroll
-    for (int i = 0; i < ELEMS; ++i)
-      if (v[i] != v[i]) s = v[i];
-  }
-  float wm = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
-  if (m > -INFINITY) s *= ex2((m - wm) * kLog2e);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) red[warp] = make_float2(wm, s);
-  // the thread's largest key (0, below every key, without an element): the largest
-  // logit, of equal ones the first
-  int at = -1;
-  if (inside) {
-#pragma unroll
-    for (int i = ELEMS - 1; i >= 0; --i)
-      if (v[i] == m) at = i / VEC * step + i % VEC;
-    if (at >= 0) at += first;  // (all NaN: none)
-  } else {
-#pragma unroll
-    for (int i = ELEMS - 1; i >= 0; --i) {
-      const int j = first + i / VEC * step + i % VEC;
-      if (v[i] == m && j >= 0 && j < V) at = j;
+      for (int i = 0; i < ELEMS; ++i) {
+        const int j = place(i);
+        v[i] = j >= 0 && j < V ? Elem<T>::load(z + j) : -INFINITY;
+      }
     }
   }
-  uint64_t top = at >= 0 ? beam_key(m, static_cast<uint32_t>(at)) : 0;
-  const bool by_four = a.num <= kBeamFew;
-  if (by_four) {
+  __device__ __forceinline__ float largest() const {
+    float m = v[0];
 #pragma unroll
-    for (int o = 1; o < 4; o *= 2) {
-      const uint64_t other = __shfl_xor_sync(0xffffffffu, top, o);
-      top = other > top ? other : top;
-    }
-    if ((threadIdx.x & 3) == 0) tops[threadIdx.x / 4] = top;
-  } else {
-    tops[threadIdx.x] = top;
+    for (int i = 1; i < ELEMS; ++i) m = fmaxf(m, v[i]);
+    return m;
   }
-  __syncthreads();
-  {
+  // The tile's bound (see above): the same for every thread; 0, which every key reaches,
+  // where fewer than num groups have an element.  Two barriers.
+  __device__ __forceinline__ uint64_t bound(float m, int V, int num, uint64_t* tops,
+                                            uint64_t* bound_sh) const {
+    // the thread's largest key (0, below every key, without an element): the largest
+    // logit, of equal ones the first
+    int at = -1;
+    if (inside) {
+#pragma unroll
+      for (int i = ELEMS - 1; i >= 0; --i)
+        if (v[i] == m) at = i / VEC * kStep + i % VEC;
+      if (at >= 0) at += first;  // (all NaN: none)
+    } else {
+#pragma unroll
+      for (int i = ELEMS - 1; i >= 0; --i) {
+        const int j = place(i);
+        if (v[i] == m && j >= 0 && j < V) at = j;
+      }
+    }
+    uint64_t top = at >= 0 ? beam_key(m, static_cast<uint32_t>(at)) : 0;
+    const bool by_four = num <= kBeamFew;
+    if (by_four) {
+#pragma unroll
+      for (int o = 1; o < 4; o *= 2) {
+        const uint64_t other = __shfl_xor_sync(0xffffffffu, top, o);
+        top = other > top ? other : top;
+      }
+      if ((threadIdx.x & 3) == 0) tops[threadIdx.x / 4] = top;
+    } else {
+      tops[threadIdx.x] = top;
+    }
+    __syncthreads();
     // a group's rank: how many are larger.  By four each of its threads looks at a quarter.
-    const uint64_t mine = by_four ? top : tops[threadIdx.x];
     const int looked = by_four ? kBeamThreads / 16 : kBeamThreads;
     const uint64_t* at_tops = tops + (by_four ? (threadIdx.x & 3) * looked : 0);
     int rank = 0;
 #pragma unroll 8
-    for (int i = 0; i < looked; ++i) rank += at_tops[i] > mine ? 1 : 0;
+    for (int i = 0; i < looked; ++i) rank += at_tops[i] > top ? 1 : 0;
     if (by_four) {
       rank += __shfl_xor_sync(0xffffffffu, rank, 1);
       rank += __shfl_xor_sync(0xffffffffu, rank, 2);
     }
-    // (fewer groups with an element than num: 0, which every key reaches)
-    if (rank < a.num && mine == 0) least_sh = 0;
-    if (rank == a.num - 1 && mine != 0) least_sh = mine;
+    if (rank < num && top == 0) *bound_sh = 0;
+    if (rank == num - 1 && top != 0) *bound_sh = top;
+    __syncthreads();
+    return *bound_sh;
   }
-  if (threadIdx.x == kBeamThreads - 1) {
-    float bm = red[0].x, bs = 0.0f;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, red[w].x);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      bs += red[w].x > -INFINITY ? red[w].y * ex2((red[w].x - bm) * kLog2e) : red[w].y;
-    a.sums[row * a.chunks + chunk] = make_float2(bm, bs);
-  }
-  __syncthreads();
-  const uint64_t least = least_sh;
-  if (top >= least && top != 0) {
+  // Writes down the keys that reach `least`; those that find no room are counted.
+  __device__ __forceinline__ void collect(float m, uint64_t least, int V, uint64_t* keys,
+                                          int room, int* count) const {
     const float z_least = least != 0 ? key_logit(least) : -INFINITY;
+    if (!(m >= z_least)) return;
     uint32_t reach = 0;  // elements that may
 #pragma unroll
     for (int i = 0; i < ELEMS; ++i) reach |= v[i] >= z_least ? 1u << i : 0u;
@@ -201,19 +179,111 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) 
       float x = v[0];
 #pragma unroll
       for (int q = 1; q < ELEMS; ++q) x = q == i ? v[q] : x;
-      const int j = first + i / VEC * step + i % VEC;
+      const int j = place(i);
       const uint64_t key = beam_key(x, static_cast<uint32_t>(j));
-      if (key >= least && j >= 0 && j < V) best[atomicAdd(&count, 1)] = key;
+      if (key < least || j < 0 || j >= V) continue;
+      const int slot = atomicAdd(count, 1);
+      if (slot < room) keys[slot] = key;
     }
   }
-  __syncthreads();
-  uint64_t* out = a.keys + (row * a.chunks + chunk) * a.num;
-  const int n = count;
+};
+
+// The best num of n keys to `out`, largest first.
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int num, uint64_t* out) {
   for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-    const uint64_t key = best[i];
+    const uint64_t key = keys[i];
     int r = 0;
-    for (int k = 0; k < n; ++k) r += best[k] > key ? 1 : 0;
-    if (r < a.num) out[r] = key;
+    for (int k = 0; k < n; ++k) r += keys[k] > key ? 1 : 0;
+    if (r < num) out[r] = key;
+  }
+}
+
+template <typename T, int ELEMS>
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) {
+  using Tile = BeamTile<T, ELEMS>;
+  constexpr int kWarps = kBeamThreads / 32;
+  __shared__ uint64_t tops[kBeamThreads];
+  __shared__ uint64_t found[kBeamMost + Tile::kRoom];
+  __shared__ uint64_t kept[kBeamMost];
+  __shared__ float2 red[kWarps];
+  __shared__ uint64_t bound_sh;
+  __shared__ int count;
+  const int64_t row = blockIdx.x / a.chunks;
+  const int chunk = static_cast<int>(blockIdx.x - row * a.chunks);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!row_counts(a, row)) return;
+  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+  // chunks begin on 16-byte boundaries, `off` elements before the row for the first
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(z) & 15) / sizeof(T);
+  const int V = static_cast<int>(a.V);
+  const int begin = chunk * a.tiles * Tile::kSize - off;
+  const int end = min(V, begin + a.tiles * Tile::kSize);
+  if (threadIdx.x == 0) count = 0;
+  Tile tile;
+  // the sum of exponentials relative to the largest logit of the thread: NaN and
+  // +infinity make it NaN, nothing but -infinity 0
+  float m = -INFINITY, s = 0.0f;
+  uint64_t least = 0;
+  for (int at = begin; at < end || at == begin; at += Tile::kSize) {
+    tile.load(z, at, V);
+    const float tm = tile.largest();
+    if (tm > m) {
+      if (m > -INFINITY) s *= ex2((m - tm) * kLog2e);
+      m = tm;
+    }
+    if (m > -INFINITY) {
+      float t = 0.0f;
+#pragma unroll
+      for (int i = 0; i < ELEMS; ++i) t += ex2((tile.v[i] - m) * kLog2e);
+      s += t;
+    } else {
+#pragma unroll
+      for (int i = 0; i < ELEMS; ++i)
+        if (tile.v[i] != tile.v[i]) s = tile.v[i];
+    }
+    if (at == begin) least = tile.bound(tm, V, a.num, tops, &bound_sh);
+    tile.collect(tm, least, V, found, Tile::kRoom, &count);
+  }
+  float wm = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, o));
+  if (m > -INFINITY) s *= ex2((m - wm) * kLog2e);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) red[warp] = make_float2(wm, s);
+  __syncthreads();
+  if (threadIdx.x == kBeamThreads - 1) {
+    float bm = red[0].x, bs = 0.0f;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) bm = fmaxf(bm, red[w].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      bs += red[w].x > -INFINITY ? red[w].y * ex2((red[w].x - bm) * kLog2e) : red[w].y;
+    a.sums[row * a.chunks + chunk] = make_float2(bm, bs);
+  }
+  uint64_t* out = a.keys + (row * a.chunks + chunk) * a.num;
+  int n = count;
+  if (n <= Tile::kRoom) {
+    rank_keys(found, n, a.num, out);
+  } else {
+    // again, tile by tile, the best num so far first in `found`
+    n = 0;
+    for (int at = begin; at < end; at += Tile::kSize) {
+      tile.load(z, at, V);
+      const float tm = tile.largest();
+      uint64_t reach = tile.bound(tm, V, a.num, tops, &bound_sh);
+      if (n == a.num && found[n - 1] > reach) reach = found[n - 1];
+      if (threadIdx.x == 0) count = n;
+      __syncthreads();
+      tile.collect(tm, reach, V, found, kBeamMost + Tile::kRoom, &count);
+      __syncthreads();
+      rank_keys(found, count, a.num, kept);
+      n = min(count, a.num);
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += kBeamThreads) found[i] = kept[i];
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < n; i += kBeamThreads) out[i] = found[i];
   }
   for (int i = n + threadIdx.x; i < a.num; i += kBeamThreads) out[i] = 0;
 }
@@ -409,23 +479,32 @@ __global__ void __launch_bounds__(kReorderThreads)
 
 // ------------------------------------------------------------------------ host
 
-// Elements of a thread: long chunks where they fill the SMs twice, else short ones (4 x
-// 50257 fp32: 8 against 11 us).
-static int beam_elems(int64_t R, int64_t V) {
-  const bool fill = R * (V / (kBeamThreads * kBeamLong)) >= 2 * sm_count();
-  return fill || V > kBeamVocab / 2 ? kBeamLong : kBeamShort;  // (the merge holds a row's keys)
-}
+// How rows are cut: elements of a thread in a tile, tiles of a chunk.  Long tiles where
+// they fill half of the places for blocks, several to a chunk where there are more; else
+// short ones (4 x 50257 fp32: 8 against 11 us).
+struct BeamPlan {
+  int elems, tiles;
+  int64_t chunks;
+};
 
-static int64_t beam_chunks(int64_t V, int elems) {
+static BeamPlan beam_plan(int64_t R, int64_t V) {
+  const int64_t room = static_cast<int64_t>(sm_count()) * 4;  // blocks at a time
+  BeamPlan p{kBeamLong, 1, 0};
+  const int64_t tiles = R * (V / (kBeamThreads * kBeamLong));
+  if (tiles < room / 2 && V <= kBeamVocab / 2)  // (the merge holds a row's keys)
+    p.elems = kBeamShort;
+  else
+    p.tiles = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, tiles / room)));
   // a row may begin inside a 16-byte block: its first chunk is up to 7 elements short
-  const int64_t chunk = kBeamThreads * elems;
-  return (V + 7 + chunk - 1) / chunk;
+  const int64_t chunk = static_cast<int64_t>(kBeamThreads) * p.elems * p.tiles;
+  p.chunks = (V + 7 + chunk - 1) / chunk;
+  return p;
 }
 
 static bool beam_sizes(int64_t B, int64_t K, int64_t V, int64_t num) {
   return B >= 0 && B <= 0x7fffffff / kBeamMost && K >= 1 && K <= kBeamMost && V >= 1 &&
          V <= kBeamVocab && num >= 1 && num <= kBeamMost && num <= K * V &&
-         B * K * beam_chunks(V, kBeamShort) <= 0x7fffffff;
+         B * K * (V / (kBeamThreads * kBeamShort) + 1) <= 0x7fffffff;
 }
 
 template <typename U>
@@ -484,7 +563,7 @@ using namespace flce;
 
 extern "C" size_t beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V, int64_t num) {
   if (!beam_sizes(B, K, V, num) || B == 0) return 0;
-  const size_t lists = static_cast<size_t>(B * K * beam_chunks(V, beam_elems(B * K, V)));
+  const size_t lists = static_cast<size_t>(B * K * beam_plan(B * K, V).chunks);
   return round_up(lists * (num * sizeof(uint64_t) + sizeof(float2)), 256);
 }
 
@@ -522,17 +601,19 @@ extern "C" int beam_select(const void* logits, int dt, int64_t B, int64_t K, int
   BeamArgs a{};
   a.logits = logits, a.V = V, a.ld = ld, a.scores = scores, a.finished = finished;
   a.pad = pad_id, a.K = static_cast<int>(K), a.num = static_cast<int>(num);
-  const int elems = beam_elems(R, V);
-  a.chunks = static_cast<int>(beam_chunks(V, elems));
+  const BeamPlan plan = beam_plan(R, V);
+  a.chunks = static_cast<int>(plan.chunks);
+  a.tiles = plan.tiles;
   a.keys = static_cast<uint64_t*>(ws);
   a.sums = reinterpret_cast<float2*>(a.keys + R * a.chunks * num);
   a.out_scores = out_scores, a.out_tokens = out_tokens, a.out_parents = out_parents;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(a.chunks * R);
-  auto* rows = dt == FLCE_BF16 ? elems == kBeamLong ? beam_rows_kernel<__nv_bfloat16, kBeamLong>
-                                                    : beam_rows_kernel<__nv_bfloat16, kBeamShort>
-               : elems == kBeamLong ? beam_rows_kernel<float, kBeamLong>
-                                    : beam_rows_kernel<float, kBeamShort>;
+  const bool longer = plan.elems == kBeamLong;
+  auto* rows = dt == FLCE_BF16 ? longer ? beam_rows_kernel<__nv_bfloat16, kBeamLong>
+                                        : beam_rows_kernel<__nv_bfloat16, kBeamShort>
+               : longer        ? beam_rows_kernel<float, kBeamLong>
+                               : beam_rows_kernel<float, kBeamShort>;
   rows<<<grid, kBeamThreads, 0, s>>>(a);
   // a warp for each beam, where their keys fit shared memory together
   const int64_t list = static_cast<int64_t>(a.chunks) * num * 8, best = K * num * 12;

@@ -84,6 +84,33 @@ def test_ties_and_masks(lh, dtype):
         _check(lh.beam_select(z, s, K, num), E.beam(z, s, K, num, None, 0))
 
 
+@pytest.mark.parametrize("R,V,dtype,shift", [(320, 70001, F32, 1), (600, 70000, BF, 0),
+                                             (1280, 131072, BF, 0)])
+def test_many_long_rows(lh, R, V, dtype, shift):
+    """Enough rows for several tiles to a block: rows that rise, fall and stay, whose
+    candidates overflow the first tile's bound, masked parts, ties."""
+    K = 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    z = torch.empty(R * V + shift, dtype=dtype, device="cuda")[shift:].view(R, V)
+    z.normal_(0.0, 3.0, generator=g)
+    z[0] = torch.arange(V, device="cuda") / 4096.0
+    z[1] = -torch.arange(V, device="cuda") / 4096.0
+    z[5] = 0.25
+    z[9, :40000] = NINF
+    z[10] = NINF
+    z[10, V - 1] = 1.0
+    z[17] = z[17].round()
+    z[18, 20000:60000] += 30.0
+    z[R - 1] = torch.arange(V, device="cuda") // 8192
+    s = _scores(R, 2)
+    for num in (1, 4, 16, 40):
+        o = lh.beam_select(z, s, K, num)
+        for b in (0, 1, 2, 4, 33, R // K - 1):
+            rows = slice(b * K, b * K + K)
+            part = lh.BeamOut(o.scores[b:b + 1], o.tokens[b:b + 1], o.parents[b:b + 1])
+            _check(part, E.beam(z[rows], s[rows], K, num, None, 0))
+
+
 def test_buffers_and_graph(lh):
     """Caller-owned outputs and workspace; captured with the reordering and replayed."""
     B, K, V = 3, 4, 3000
