@@ -6,11 +6,10 @@
 // best first, of equal ones the one with the lowest k V + v.  Within a beam that
 // order is the logits' own, so the selection splits:
 //   beam_rows_kernel    a block takes a chunk of a row, reads it once (twice where its
-//                       logits rise), and leaves the
-//                       chunk's maximum and sum of exponentials and its `num` best
-//                       tokens, as 64-bit keys: the logit's bits in an order-keeping
-//                       form, then the token's complement, so that keys differ and
-//                       the larger one comes first;
+//                       logits rise), and leaves the chunk's maximum and sum of
+//                       exponentials and its `num` best tokens, as 64-bit keys: the
+//                       logit's bits in an order-keeping form, then the token's
+//                       complement, so that keys differ and the larger one comes first;
 //   beam_merge_kernel   a block takes a request: every row's lse and best `num` keys
 //                       from its chunks', then the request's from its rows'.
 // Bound by the bytes of the logits, for few rows by the latency of the two launches.
@@ -29,6 +28,9 @@ constexpr int kBeamThreads = 256;
 constexpr int kBeamLong = 32, kBeamShort = 8;  // elements of a thread in a tile
 constexpr int kBeamMost = 64;                  // beams of a request, and `num`
 constexpr int kBeamFew = 16;                   // `num` up to which threads go by fours
+// Keys that a chunk writes down under one bound: 300 are expected of 4 tiles at the largest
+// `num`; ranking costs their square.
+constexpr int kBeamOnce = 512;
 constexpr int64_t kBeamVocab = int64_t(1) << 20;
 constexpr int kBeamMergeThreads = 512;
 
@@ -78,14 +80,15 @@ __device__ __forceinline__ bool row_counts(const BeamArgs& a, int64_t row) {
 // serves the whole chunk: what reaches it is written down without a wait, some num
 // keys to a tile, and ranked at the end.  Where that overflows (rows that rise) the
 // chunk is read again, with a bound and the best num so far for each tile.  Bound by
-// instructions (some 14 per logit), four blocks to an SM: 320 x 151936 fp32 33 of 41 us
-// with the merge (6 TB/s), 128 x 128256 bf16 24 us.  With a bound for every tile, of one
-// to a block, 52 of 61 and 31; eight tiles to a block 43 and 24.
+// instructions (some 14 per logit), four blocks to an SM: 320 x 151936 fp32 34 of 42 us
+// with the merge (5.7 TB/s), 128 x 128256 bf16 24 to 27 us.  With a bound for every tile,
+// of one to a block, 52 of 61 and 31; eight tiles to a block 43 and 24.  The fp32 rows
+// with their first half masked take 72 us, all equal 60, sorted upwards 115.
 template <typename T, int ELEMS>
 struct BeamTile {
   static constexpr int VEC = 16 / sizeof(T), NV = ELEMS / VEC;
   static constexpr int kSize = kBeamThreads * ELEMS, kStep = kBeamThreads * VEC;
-  // keys that reach a tile's bound, and the best so far
+  // keys that reach a tile's own bound, at most
   static constexpr int kRoom = kBeamMost * ELEMS > kBeamFew * 4 * ELEMS ? kBeamMost * ELEMS
                                                                         : kBeamFew * 4 * ELEMS;
   float v[ELEMS];
@@ -165,7 +168,8 @@ struct BeamTile {
     __syncthreads();
     return *bound_sh;
   }
-  // Writes down the keys that reach `least`; those that find no room are counted.
+  // Writes down the keys that reach `least`.  *count passes `room` where one finds no
+  // room; the rest are then left, for the chunk is read again.
   __device__ __forceinline__ void collect(float m, uint64_t least, int V, uint64_t* keys,
                                           int room, int* count) const {
     const float z_least = least != 0 ? key_logit(least) : -INFINITY;
@@ -173,6 +177,14 @@ struct BeamTile {
     uint32_t reach = 0;  // elements that may
 #pragma unroll
     for (int i = 0; i < ELEMS; ++i) reach |= v[i] >= z_least ? 1u << i : 0u;
+    if ((reach & (reach - 1)) != 0) {
+      // Equal logits reach it up to its token.  Masked and constant tiles are equal all
+      // over: not by the loop below, an element at a time.
+      const uint32_t last = key_token(least);
+#pragma unroll
+      for (int i = 0; i < ELEMS; ++i)
+        if (v[i] == z_least && static_cast<uint32_t>(place(i)) > last) reach &= ~(1u << i);
+    }
     while (reach != 0) {
       const int i = __ffs(reach) - 1;
       reach &= reach - 1;
@@ -183,7 +195,8 @@ struct BeamTile {
       const uint64_t key = beam_key(x, static_cast<uint32_t>(j));
       if (key < least || j < 0 || j >= V) continue;
       const int slot = atomicAdd(count, 1);
-      if (slot < room) keys[slot] = key;
+      if (slot >= room) return;
+      keys[slot] = key;
     }
   }
 };
@@ -204,6 +217,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) 
   constexpr int kWarps = kBeamThreads / 32;
   __shared__ uint64_t tops[kBeamThreads];
   __shared__ uint64_t found[kBeamMost + Tile::kRoom];
+  static_assert(kBeamOnce <= kBeamMost + Tile::kRoom, "the first reading's keys fit");
   __shared__ uint64_t kept[kBeamMost];
   __shared__ float2 red[kWarps];
   __shared__ uint64_t bound_sh;
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) 
         if (tile.v[i] != tile.v[i]) s = tile.v[i];
     }
     if (at == begin) least = tile.bound(tm, V, a.num, tops, &bound_sh);
-    tile.collect(tm, least, V, found, Tile::kRoom, &count);
+    tile.collect(tm, least, V, found, kBeamOnce, &count);
   }
   float wm = m;
 #pragma unroll
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_rows_kernel(BeamArgs a) 
   }
   uint64_t* out = a.keys + (row * a.chunks + chunk) * a.num;
   int n = count;
-  if (n <= Tile::kRoom) {
+  if (n <= kBeamOnce) {
     rank_keys(found, n, a.num, out);
   } else {
     // again, tile by tile, the best num so far first in `found`

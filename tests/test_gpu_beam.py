@@ -111,6 +111,31 @@ def test_many_long_rows(lh, R, V, dtype, shift):
             _check(part, E.beam(z[rows], s[rows], K, num, None, 0))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("num", [5, 64])
+def test_masked_long_rows(lh, dtype, num):
+    """Several tiles to a block over a vocabulary that is masked in part: tiles without a
+    logit before, between and behind others, fewer logits than are asked for, equal ones
+    around a tile's end."""
+    R, V, K = 320, 70000, 4
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = torch.empty(R, V, dtype=dtype, device="cuda").normal_(0.0, 3.0, generator=g)
+    z[0:4, :V // 2] = NINF
+    z[4:8, V // 2:] = NINF
+    z[8:12, :8192 + 17] = NINF
+    z[12:16, 100:V - 100] = torch.finfo(dtype).min
+    z[16:20] = NINF
+    z[16:20, 8191:8195] = 2.0
+    z[20:24] = 0.0
+    z[24:28, 8192:] = z[24:28, :8192].max()
+    s = _scores(R, 4)
+    o = lh.beam_select(z, s, K, num)
+    for b in range(8):
+        rows = slice(b * K, b * K + K)
+        part = lh.BeamOut(o.scores[b:b + 1], o.tokens[b:b + 1], o.parents[b:b + 1])
+        _check(part, E.beam(z[rows], s[rows], K, num, None, 0))
+
+
 def test_buffers_and_graph(lh):
     """Caller-owned outputs and workspace; captured with the reordering and replayed."""
     B, K, V = 3, 4, 3000
