@@ -155,12 +155,17 @@ def rms_norm_add_bwd(summed, grad_y, grad_summed, rstd, weight=None, *, want_gra
 
 
 class _RMSNormAdd(torch.autograd.Function):
+    """Takes tensors of any shape, so that x and residual get one tensor as gradient:
+    autograd then gives each leaf memory of its own, which it does not for two views."""
     @staticmethod
     def forward(ctx, x, residual, weight, eps):
-        o = rms_norm_add_fwd(_rows_of(x), _rows_of(residual), weight, eps)
-        ctx.save_for_backward(o.summed, weight, o.rstd)
+        D = x.shape[-1]
+        y, summed = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+        o = rms_norm_add_fwd(_rows_of(x.reshape(-1, D)), _rows_of(residual.reshape(-1, D)), weight,
+                             eps, y=y.view(-1, D), summed=summed.view(-1, D))
+        ctx.save_for_backward(summed, weight, o.rstd)
         ctx.set_materialize_grads(False)
-        return o.y, o.summed
+        return y, summed
 
     @staticmethod
     @once_differentiable
@@ -169,9 +174,12 @@ class _RMSNormAdd(torch.autograd.Function):
         need_x, need_r, need_w, _ = ctx.needs_input_grad
         if gy is None:  # only the stream goes on
             return gs if need_x else None, gs if need_r else None, None, None
-        o = rms_norm_add_bwd(summed, _rows_of(gy), None if gs is None else _rows_of(gs), rstd,
-                             weight, want_grad_x=need_x or need_r, want_grad_weight=need_w)
-        return o.grad_x if need_x else None, o.grad_x if need_r else None, o.grad_weight, None
+        D = summed.shape[-1]
+        o = rms_norm_add_bwd(summed.view(-1, D), _rows_of(gy.reshape(-1, D)),
+                             None if gs is None else _rows_of(gs.reshape(-1, D)), rstd, weight,
+                             want_grad_x=need_x or need_r, want_grad_weight=need_w)
+        g = None if o.grad_x is None else o.grad_x.view(summed.shape)
+        return g if need_x else None, g if need_r else None, o.grad_weight, None
 
 
 def rms_norm_add(x, residual, weight=None, *, eps=1e-5):
@@ -181,9 +189,7 @@ def rms_norm_add(x, residual, weight=None, *, eps=1e-5):
         raise ValueError("x must have a last dimension to normalise")
     if not isinstance(residual, torch.Tensor) or residual.shape != x.shape:
         raise ValueError("residual must have the shape of x")
-    D = x.shape[-1]
-    y, summed = _RMSNormAdd.apply(x.reshape(-1, D), residual.reshape(-1, D), weight, float(eps))
-    return y.view(x.shape), summed.view(x.shape)
+    return _RMSNormAdd.apply(x, residual, weight, float(eps))
 
 
 # --------------------------------------------------------------- to 8 bits, products

@@ -206,3 +206,27 @@ def test_autograd(lh, dtype):
         assert abs((f[0] - f[1]) / (2 * h) - (g.double() * v.double()).sum()) < 0.05
     y, s = lh.rms_norm_add(x.view(2, 3, D), res.view(2, 3, D), w)
     assert y.shape == s.shape == (2, 3, D)
+
+
+@pytest.mark.parametrize("use", ["both", "y", "summed"])
+@pytest.mark.parametrize("shape", [(6, 40), (2, 3, 40), (40,)])
+def test_gradients_of_leaves_accumulate(lh, shape, use):
+    """x and residual get equal gradients, each in memory of its own: a second backward
+    pass adds to each once (g + g = 2 g exactly)."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, r = (torch.randn(shape, device="cuda", generator=g).requires_grad_() for _ in range(2))
+    w = torch.randn(40, device="cuda", generator=g).requires_grad_()
+    gy, gs = (torch.randn(shape, device="cuda", generator=g) for _ in range(2))
+    kept = gs.clone()
+    for passes in (1, 2, 3):
+        y, s = lh.rms_norm_add(x, r, w)
+        outs, grads = {"both": ((y, s), (gy, gs)), "y": ((y,), (gy,)),
+                       "summed": ((s,), (gs,))}[use]
+        torch.autograd.backward(outs, grads)
+        if passes == 1:
+            first = x.grad.clone()
+            assert torch.equal(r.grad, first)
+        assert x.grad.data_ptr() != r.grad.data_ptr()
+        if passes == 2:
+            assert torch.equal(x.grad, 2 * first) and torch.equal(r.grad, 2 * first)
+    assert torch.equal(gs, kept)
