@@ -8,6 +8,9 @@ buffers optional):
 Autograd front ends:
     rms_norm_add(x, residual, weight=None, *, eps=1e-5) -> y, summed
     linear8(x, W)
+
+A step that calls ``backward()`` is captured as ``ops`` says: run before on the
+capture stream, with no eager graph of the same leaves alive.
 """
 from __future__ import annotations
 

@@ -232,3 +232,35 @@ def test_side_stream_and_graph(lh):
         graph.replay()
         want = step()
         assert torch.equal(y, want[0]) and torch.equal(summed, want[1])
+
+
+def test_captured_training_step(lh):
+    """Norm, product and both backward passes captured on one stream, replayed on new
+    inputs: the eager step's gradients."""
+    N, K, M = 300, 640, 200
+    W, w = _randn((M, K), BF, 3), torch.ones(K, device="cuda")
+    gy = _randn((N, M), BF, 4).reshape(2, N // 2, M)
+    leaves = [_randn((N, K), BF, seed).reshape(2, N // 2, K).clone() for seed in (1, 2)]
+    leaves = [t.requires_grad_() for t in (*leaves, w.clone(), W.clone())]
+
+    def step(x, res, w, W):
+        y, summed = lh.rms_norm_add(x, res, w)
+        torch.autograd.backward((lh.linear8(y, W), summed), (gy, summed.detach()))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(*leaves)
+    torch.cuda.current_stream().wait_stream(s)
+    for t in leaves:
+        t.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(*leaves)
+    for seed in (5, 6):
+        with torch.no_grad():
+            leaves[0].copy_(_randn((N, K), BF, seed).view_as(leaves[0]))
+        graph.replay()
+        eager = [t.detach().clone().requires_grad_() for t in leaves]
+        step(*eager)
+        for a, b in zip(leaves, eager):
+            assert torch.equal(a.grad, b.grad)
