@@ -233,8 +233,9 @@ def gemm8(a: Quant8, b: Quant8, bias=None, *, out=None, out_dtype=torch.float32,
           accumulate=False, status=None) -> torch.Tensor:
     """a b^T (+ bias [N], bf16 or fp32) of a [M, K] (rows 1) and b [N, K] (rows 1 or
     128): [M, N] in ``out`` or a new tensor of ``out_dtype`` (bf16 or fp32).  From one
-    token's head or layer to a long batch's.  ``accumulate`` adds to the fp32
-    ``out``.  A wait inside the kernel that gives up leaves NaN, and FLCE_ETIMEOUT
+    token's head or layer to a long batch's (whose results are stored fastest in rows
+    of a multiple of 16 bytes: an ``out`` with padding where N is odd).  ``accumulate``
+    adds to the fp32 ``out``.  A wait inside the kernel that gives up leaves NaN, and FLCE_ETIMEOUT
     in ``status`` (new_status), if given."""
     if not isinstance(a, Quant8) or a.rows != 1:
         raise ValueError("a must be a Quant8 with one row to a scale")
