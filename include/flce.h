@@ -621,11 +621,13 @@ FLCE_API int quantize8(const void* x, int dt, int64_t R, int64_t C, int64_t ldx,
 
 /* y [M, N] (dtype dt_y, row stride ldy) = a b^T (+ bias [N], dtype dt_bias, or NULL)
  * of a [M, K] (rows = 1) and b [N, K] (rows = b_rows, 1 or 128) in 8 bits.  A block's
- * 128 products are summed by the tensor cores in fp32; these sums times the two
- * scales add up in fp32 in a fixed order.  The product of two scales that meet has to
- * lie within fp32's range: beyond it the block counts as infinite (NaN where its sum
- * is 0), below as 0.  accumulate != 0 adds to y (FLCE_F32 only), which may be the
- * memory's own addition, that takes subnormal numbers for 0.  A layer's training pass is three of these:
+ * 128 products are summed by the tensor cores in fp32; these sums times the product
+ * of the two scales, formed first, add up in fp32 in a fixed order.  That product has to
+ * lie within the range of fp32's normal numbers, whatever the scales are: above it the
+ * block counts as infinite (NaN where its sum is 0), below it the product keeps fewer
+ * bits, down to 0.  accumulate != 0 adds to y (FLCE_F32 only), which may be the
+ * memory's own addition, that takes subnormal numbers for 0.  A layer's training pass
+ * is three of these:
  *   y = x8 w8^T,   grad_x = g8 (w8^T)^T,   grad_w = (g8^T) (x8^T)^T
  * with x, grad_y by rows and w by squares, each with its transpose from quantize8.
  * M == 0 is valid.  y overlaps no input.  A wait inside the kernel that gives up

@@ -240,11 +240,12 @@ __global__ void __launch_bounds__(Gemm8Geo<BN>::kThreads, 1)
             tmem_ld(lanes + buf * BN + j, v);
 #pragma unroll
             for (int e = 0; e < G::kLoad; e += 4) {
+              // the scales' product first: a sum times one of them may leave fp32's range
               const float4 s = s4[(j + e) / 4];
-              acc[j + e] = __fmaf_rn(__fmul_rn(v[e], s.x), rs[i], acc[j + e]);
-              acc[j + e + 1] = __fmaf_rn(__fmul_rn(v[e + 1], s.y), rs[i], acc[j + e + 1]);
-              acc[j + e + 2] = __fmaf_rn(__fmul_rn(v[e + 2], s.z), rs[i], acc[j + e + 2]);
-              acc[j + e + 3] = __fmaf_rn(__fmul_rn(v[e + 3], s.w), rs[i], acc[j + e + 3]);
+              acc[j + e] = __fmaf_rn(v[e], __fmul_rn(s.x, rs[i]), acc[j + e]);
+              acc[j + e + 1] = __fmaf_rn(v[e + 1], __fmul_rn(s.y, rs[i]), acc[j + e + 1]);
+              acc[j + e + 2] = __fmaf_rn(v[e + 2], __fmul_rn(s.z, rs[i]), acc[j + e + 2]);
+              acc[j + e + 3] = __fmaf_rn(v[e + 3], __fmul_rn(s.w, rs[i]), acc[j + e + 3]);
             }
           }
           tc_fence_before();

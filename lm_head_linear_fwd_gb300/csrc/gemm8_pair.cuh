@@ -14,10 +14,12 @@
 // about 800 cycles per block the products take 512 and the additions 256 (packed fp32
 // at half rate); the rest are the waits between them, which two warps to a scheduler
 // (their sums fill the registers) hide in part.  8192 x 4096 x 16384, scales of b for
-// 128 rows: 369 us, 3.0 PFLOP/s; for each row, twice the arithmetic, 511 us.  The
+// 128 rows: 371 us, 3.0 PFLOP/s; for each row, twice the arithmetic, 531 us (519 with the
+// sum times one scale formed first, which leaves fp32's range where the other scale would
+// bring it back; the scales' products formed while the sums are on their way 564).  The
 // scales loaded by the adding threads took 723 us (they spill), handed over for four
-// blocks at a time 385 and 529; tensor memory read without a load ahead 438; one lane in the
-// issuing warp's loop 446; sixteen adding warps of 64 columns 414.
+// blocks at a time 385 and 529; tensor memory read without a load ahead 438; one lane in
+// the issuing warp's loop 446; sixteen adding warps of 64 columns 414.
 //
 // Barriers as in the pair kernel of tc_gemm.cuh:
 //   full[s]   leader: both CTAs' copies have landed     empty[s]  both: both halves' were read
@@ -397,8 +399,8 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
               lds_pairs(at_cols + p * 8 + 16, c[2], c[3]);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                v[p + q] = mul_pair(v[p + q], c[q]);
-                fma_pair(v[p + q], s2, sums[j * (kLoad / 2) + p + q]);
+                // the scales' product first: a sum times one of them may leave fp32's range
+                fma_pair(v[p + q], mul_pair(c[q], s2), sums[j * (kLoad / 2) + p + q]);
               }
             }
           } else {
