@@ -676,8 +676,9 @@ typedef struct {
  * row b K + k becomes what row b K + parents[b, k] was.  `states` is an array of the
  * HOST, read before the call returns.  Rows that stay are not touched.  A parent
  * outside [0, K) leaves its row as it was and sets FLCE_ELABEL in *status (may be
- * NULL).  K at most 64.  Runs of a state do not overlap, and states do not overlap each other: what the
- * strides show to overlap is refused (FLCE_ESHAPE, FLCE_EINVAL). */
+ * NULL).  K at most 64.  Runs of a state do not overlap, and states overlap neither
+ * each other nor the parents or the status word: what the strides show to overlap is
+ * refused (FLCE_ESHAPE, FLCE_EINVAL). */
 FLCE_API int beam_reorder(const flce_beam_state_t* states, int n, int64_t B, int64_t K,
                           const int64_t* parents, int32_t* status, flce_stream_t stream);
 

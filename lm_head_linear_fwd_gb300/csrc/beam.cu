@@ -570,6 +570,21 @@ static bool meet(const flce_beam_state_t& a, const flce_beam_state_t& b, int64_t
   if (a.outer == 0 || a.inner == 0 || b.outer == 0 || b.inner == 0) return false;
   return overlap(whole_rows(a, R), whole_rows(b, R)) && overlap(lines(a, R), lines(b, R));
 }
+// Whether a state shares a byte with consecutive ones.  The runs of the shorter stride lie
+// within a step of the longer one, and bytes as long as that step hold a run: the steps
+// that begin near them are looked at, three at most before one is found or all are passed.
+static bool meet(const flce_beam_state_t& t, const Span& bytes, int64_t R) {
+  if (t.outer == 0 || t.inner == 0 || bytes.empty()) return false;
+  const bool by_row = t.outer == 1 || (R > 1 && t.row_stride >= t.outer_stride);
+  const int64_t steps = by_row ? R : t.outer, step = by_row ? t.row_stride : t.outer_stride;
+  const int64_t runs = by_row ? t.outer : R, stride = by_row ? t.outer_stride : t.row_stride;
+  const uintptr_t data = reinterpret_cast<uintptr_t>(t.data);
+  int64_t i = steps > 1 && bytes.p > data ? static_cast<int64_t>(bytes.p - data) / step : 0;
+  for (; i < steps && data + static_cast<uintptr_t>(i * step) < bytes.end(); ++i)
+    if (overlap(Span(static_cast<char*>(t.data) + i * step, runs, t.inner, stride, 1), bytes))
+      return true;
+  return false;
+}
 
 }  // namespace flce
 
@@ -667,9 +682,14 @@ extern "C" int beam_reorder(const flce_beam_state_t* states, int n, int64_t B, i
     if (reorder_blocks(t, B, reorder_unit(t, R)) > 0x7fffffff) return FLCE_ESHAPE;
   }
   if (R == 0) return FLCE_OK;
-  for (int i = 0; i < n; ++i)
+  // blocks read the parents, and report, while others already write
+  const Span order(parents, 1, R, R, 8), word(status, 1, 1, 1, 4);
+  if (overlap(order, word)) return FLCE_EINVAL;
+  for (int i = 0; i < n; ++i) {
+    if (meet(states[i], order, R) || meet(states[i], word, R)) return FLCE_EINVAL;
     for (int j = 0; j < i; ++j)
       if (meet(states[i], states[j], R)) return FLCE_EINVAL;
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // one launch for the states of each unit
   for (int unit = 16; unit > 0; unit /= 2) {
