@@ -260,9 +260,11 @@ def gemm8(a: Quant8, b: Quant8, bias=None, *, out=None, out_dtype=torch.float32,
 
 
 class _Linear8(torch.autograd.Function):
+    """recorded: whether a backward pass can follow (needs_input_grad does not say so: it
+    stays true for a leaf where gradients are switched off)."""
     @staticmethod
-    def forward(ctx, x, W):
-        need_x, need_w = ctx.needs_input_grad
+    def forward(ctx, x, W, recorded):
+        need_x, need_w = (need and recorded for need in ctx.needs_input_grad[:2])
         x8, x8t = _quantize8(_rows_of(x), 1, True, need_w, None, None)
         w8, w8t = _quantize8(_rows_of(W), 128, True, need_x, None, None)
         ctx.dtypes = x.dtype, W.dtype
@@ -276,10 +278,10 @@ class _Linear8(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, g):
         xt, xt_scales, wt, wt_scales = ctx.saved_tensors
-        need_x, need_w = ctx.needs_input_grad
+        need_x, need_w, _ = ctx.needs_input_grad
         dx, dw = ctx.dtypes
         if not (need_x or need_w):
-            return None, None
+            return None, None, None
         g8, g8t = _quantize8(_rows_of(g), 1, need_x, need_w, None, None)
         gx = gemm8(g8, Quant8(wt, wt_scales, 128), out_dtype=dx) if need_x else None
         gW = None
@@ -287,7 +289,7 @@ class _Linear8(torch.autograd.Function):
             gW = torch.zeros(g.shape[1], xt.shape[0], dtype=dw, device=g.device)
         elif need_w:
             gW = gemm8(g8t, Quant8(xt, xt_scales), out_dtype=dw)
-        return gx, gW
+        return gx, gW, None
 
 
 def linear8(x, W):
@@ -298,5 +300,5 @@ def linear8(x, W):
         raise ValueError("x must have a last dimension")
     if not isinstance(W, torch.Tensor) or W.dim() != 2 or W.shape[1] != x.shape[-1]:
         raise ValueError(f"W must be [N, {x.shape[-1]}]")
-    y = _Linear8.apply(x.reshape(-1, x.shape[-1]), W)
+    y = _Linear8.apply(x.reshape(-1, x.shape[-1]), W, torch.is_grad_enabled())
     return y.view(*x.shape[:-1], W.shape[0])
