@@ -305,10 +305,11 @@ __device__ __forceinline__ void store_vector(char* p, int k, bool in_row, int D,
 
 // A weight vector in shared memory as fp32: of each row vector's VEC weights
 // four together, the quarters of all vectors first, so that 16-byte reads of
-// neighbouring threads lie next to each other.  Zeros past the end.
+// neighbouring threads lie next to each other, a quarter's `pitch` from the next one's.
+// Zeros past the end of the last vector.
 template <int VEC>
 __device__ __forceinline__ void stage_weights(float4* to, const void* p, int f32, float other,
-                                              int D) {
+                                              int D, int pitch) {
   const int nvec = (D + VEC - 1) / VEC;
   const bool wide = (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 #pragma unroll 4
@@ -329,17 +330,17 @@ __device__ __forceinline__ void stage_weights(float4* to, const void* p, int f32
                      : Elem<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(p) + j + e);
       }
     }
-    to[c % (VEC / 4) * nvec + c / (VEC / 4)] = make_float4(v[0], v[1], v[2], v[3]);
+    to[c % (VEC / 4) * pitch + c / (VEC / 4)] = make_float4(v[0], v[1], v[2], v[3]);
   }
 }
 
 // The weights of vector i.
 template <int VEC>
-__device__ __forceinline__ void weight_vec(const float4* w, int nvec, int i,
+__device__ __forceinline__ void weight_vec(const float4* w, int pitch, int i,
                                            float2 (&pairs)[VEC / 2]) {
 #pragma unroll
   for (int q = 0; q < VEC / 4; ++q) {
-    const float4 v = w[q * nvec + i];
+    const float4 v = w[q * pitch + i];
     pairs[2 * q] = make_float2(v.x, v.y);
     pairs[2 * q + 1] = make_float2(v.z, v.w);
   }
@@ -400,8 +401,8 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_fwd_kernel(NormArgs a) {
   }
   cp_async_commit();
   const float4* bias = weights + nvec * (VEC / 4);
-  stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
-  if (kCenter) stage_weights<VEC>(weights + nvec * (VEC / 4), a.bias, a.w_f32, 0.0f, D);
+  stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D, nvec);
+  if (kCenter) stage_weights<VEC>(weights + nvec * (VEC / 4), a.bias, a.w_f32, 0.0f, D, nvec);
   bool staged = false;  // the block's weights are there: needed late in the first row
   const float inv_n = 1.0f / static_cast<float>(D);
   for (; turns > 0; turns -= kRows, rows -= kRows) {
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(kBwdThreads<kElems>) norm_bwd_kernel(NormBwdAr
     fetch(odd, 1);
     fetch_more(odd, 1);
   }
-  stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
+  stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D, nvec);
   float2 dw[NV][P] = {}, db[NV][P] = {};
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(D);

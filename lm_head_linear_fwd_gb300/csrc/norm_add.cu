@@ -40,6 +40,8 @@ __device__ __forceinline__ float rounded(float x) {
   return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(x)) : x;
 }
 
+constexpr int kZeroWeights = 32;
+
 // Rows on 16-byte boundaries.  65536 x 5120 bf16: 362 us with y in 8 bits, 416 in bf16
 // (both 6.5 TB/s); 8192 x 4096 to 8 bits 42 us.  With two rows at a time of 16 elements
 // per thread, as in norm_fwd_kernel, and two divisions per block and lane: 412, 415, 49.
@@ -65,7 +67,13 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_add_fwd_kernel(NormAddArg
   uint8_t* q = kQuant ? a.q + row * a.ldq : nullptr;
   float* scales = kQuant ? a.scales + row * blocks : nullptr;
   float* rstd_out = a.rstd != nullptr ? a.rstd + row : nullptr;
-  char* places = reinterpret_cast<char*>(weights + nvec * (VEC / 4));
+  // A vector of zeros behind the weights, for the threads' places past the row's end: 0 times
+  // the last weights, if these are infinite, would be NaN in their block.  (128 bytes leave
+  // the copies where they were: one vector's cost 4 of 78 us.)
+  const int pitch = nvec + kZeroWeights / VEC;
+  if (threadIdx.x < VEC / 4)
+    weights[threadIdx.x * pitch + nvec] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  char* places = reinterpret_cast<char*>(weights + pitch * (VEC / 4));
   const Copy copy(places, team), rcopy(places + Copy::bytes(blockDim.x, a.team), team);
   copy.clear(false, team);
   rcopy.clear(!add, team);
@@ -74,7 +82,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_add_fwd_kernel(NormAddArg
     if (add) rcopy.start(res.p, D, team);
   }
   cp_async_commit();
-  stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D);
+  stage_weights<VEC>(weights, a.weight, a.w_f32, 1.0f, D, pitch);
   bool staged = false;  // the block's weights are there: needed late in the first row
   const float inv_n = 1.0f / static_cast<float>(D);
   for (int parity = 0; turns > 0; --turns, --rows, parity ^= 1) {
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_add_fwd_kernel(NormAddArg
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float2 w[P];
-      weight_vec<VEC>(weights, nvec, min(team.at(k), nvec - 1), w);
+      weight_vec<VEC>(weights, pitch, min(team.at(k), nvec), w);
       m[k] = 0.0f;
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -445,7 +453,8 @@ static int launch_norm_add_whole(NormAddArgs a, cudaStream_t s) {
   a.team = p.team;
   a.teams = p.teams;
   const int threads = p.team * p.teams;
-  const size_t smem = weight_bytes(a.D) + 2 * RowCopy<T, true, kElems>::bytes(threads, p.team);
+  const size_t smem = weight_bytes(a.D + kZeroWeights) +
+                      2 * RowCopy<T, true, kElems>::bytes(threads, p.team);
   if (smem > kSmemMost) return 1;
   kernel<<<static_cast<unsigned>(p.blocks), threads, smem, s>>>(a);
   return launch_status("norm_add_fwd_kernel launch");
