@@ -655,9 +655,9 @@ FLCE_API int gemm8(const uint8_t* a, int64_t lda, const float* a_scales, int64_t
  * not used, it goes on with pad_id (in [0, V)) at its own score, and all else has
  * -infinity.  So has everything of a beam whose score is not finite, or whose logits
  * have no distribution (a NaN, +infinity, or nothing but -infinity).
- * K and num at most 64, num <= K V, V <= 2^20, B K ceil((V + 7) / 2048) below 2^31.  B == 0 is valid.  Outputs and workspace overlap neither inputs nor each
- * other.  ws: beam_select_workspace_bytes bytes (on the current device), 16-byte
- * aligned. */
+ * K and num at most 64, num <= K V, V <= 2^20, 64 B and B K ceil((V + 7) / 2048) below
+ * 2^31.  B == 0 is valid.  Outputs and workspace overlap neither inputs nor each other.
+ * ws: beam_select_workspace_bytes bytes (on the current device), 16-byte aligned. */
 FLCE_API size_t beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V, int64_t num);
 FLCE_API int beam_select(const void* logits, int dt, int64_t B, int64_t K, int64_t V, int64_t ld,
                          const float* scores, const uint8_t* finished, int64_t pad_id,

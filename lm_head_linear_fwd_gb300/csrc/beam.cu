@@ -516,9 +516,10 @@ static BeamPlan beam_plan(int64_t R, int64_t V) {
 }
 
 static bool beam_sizes(int64_t B, int64_t K, int64_t V, int64_t num) {
+  constexpr int64_t kChunk = kBeamThreads * kBeamShort;  // of the most blocks (beam_plan)
   return B >= 0 && B <= 0x7fffffff / kBeamMost && K >= 1 && K <= kBeamMost && V >= 1 &&
          V <= kBeamVocab && num >= 1 && num <= kBeamMost && num <= K * V &&
-         B * K * (V / (kBeamThreads * kBeamShort) + 1) <= 0x7fffffff;
+         B * K * ((V + 7 + kChunk - 1) / kChunk) <= 0x7fffffff;
 }
 
 template <typename U>
