@@ -41,7 +41,8 @@
  * Memory.  Every pointer is a DEVICE pointer unless stated otherwise; the
  * caller allocates every buffer (inputs, outputs, workspace) and keeps
  * ownership.  The library never allocates or frees device memory, never
- * synchronises, and enqueues all its work on the caller's `stream`.
+ * synchronises, and enqueues all its work on the caller's `stream`, which with the
+ * pointers belongs to the current device.
  * Matrices are row-major with unit stride along the last dimension.
  *
  * Errors.  Every entry point returns a flce_status_t.  Errors that the host can

@@ -59,7 +59,19 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on_current(device):
+    """The library launches on the current device, whatever the stream: the default one's
+    handle is the same on all."""
+    if device.index is not None and device.index != _current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device: call "
+                         f"this under torch.cuda.device({device.index})")
+
+
 def _stream(device) -> int:
+    _on_current(device)
     return torch.cuda.current_stream(device).cuda_stream
 
 

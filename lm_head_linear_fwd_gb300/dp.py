@@ -41,10 +41,11 @@ def local_valid_count(labels: torch.Tensor, V: int, ignore_index: int = -100) ->
     in [0, V), counted by the library's kernel."""
     if not labels.is_cuda:
         raise ValueError("labels must be a CUDA tensor")
+    from .api import _stream
     labels = labels.contiguous()
     out = torch.empty(1, dtype=torch.int64, device=labels.device)
     rc = _abi.flce_count_valid(labels.data_ptr(), labels.numel(), int(V), int(ignore_index),
-                               out.data_ptr(), torch.cuda.current_stream(labels.device).cuda_stream)
+                               out.data_ptr(), _stream(labels.device))
     _abi.check(rc, "flce_count_valid")
     return out
 

@@ -30,7 +30,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .api import _cuda, _dtype_code, new_status
+from .api import _cuda, _dtype_code, _on_current, new_status
 from .api import _stream as _stream_of
 
 _call = _abi.packed
@@ -45,6 +45,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream(device):
     if _raw_stream is None or device.index is None:
         return _stream_of(device)
+    _on_current(device)
     return _raw_stream(device.index)
 
 
