@@ -871,8 +871,11 @@ static int launch_norm_bwd_held(NormBwdArgs& a, int elems, bool whole, cudaStrea
   if (whole)
     return elems == 8 ? launch_norm_bwd_k<T, true, kCenter, 8, 2, kAdd>(a, s)
                       : launch_norm_bwd_k<T, true, kCenter, 16, kAhead16, kAdd>(a, s);
-  return elems == 8 ? launch_norm_bwd_k<T, false, kCenter, 8, 2, kAdd>(a, s)
-                    : launch_norm_bwd_k<T, false, kCenter, 16, 1, kAdd>(a, s);
+  if constexpr (kAdd)
+    return FLCE_ENOSUP;  // norm_add_bwd_any_kernel has taken them
+  else
+    return elems == 8 ? launch_norm_bwd_k<T, false, kCenter, 8, 2, false>(a, s)
+                      : launch_norm_bwd_k<T, false, kCenter, 16, 1, false>(a, s);
 }
 
 template <typename T, bool kCenter, bool kAdd>

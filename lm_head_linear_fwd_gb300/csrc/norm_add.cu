@@ -488,6 +488,11 @@ static int launch_norm_add(NormAddArgs a, int dt, cudaStream_t s) {
   return launch_status("norm_add_fwd_long_kernel launch");
 }
 
+// All rows that norm_bwd_kernel can hold: it is not there for those off 16-byte boundaries.
+static_assert(kAnyBwdThreads / 32 * 2 * kBlock8 >= kBwdThreads<16> * 16 &&
+                  kBwdThreads<16> * 16 >= kBwdThreads<8> * 8,
+              "rows off 16-byte boundaries are held by norm_add_bwd_any_kernel");
+
 // Launches norm_add_bwd_any_kernel; returns 1 (nothing launched) where rows begin on
 // 16-byte boundaries or are too wide.  The arguments have been checked.
 template <typename T>
@@ -564,15 +569,16 @@ extern "C" int rms_norm_add_bwd(const void* summed, int dt, int64_t N, int64_t D
                                 int64_t ldgs, const void* weight, int wdt, const float* rstd,
                                 void* grad_x, int64_t ldgx, float* grad_weight, int accumulate,
                                 void* ws, size_t ws_bytes, flce_stream_t stream) {
+  if (grad_summed == nullptr || grad_x == nullptr || N == 0)
+    return rms_norm_bwd(summed, dt, N, D, lds, grad_y, ldgy, weight, wdt, rstd, grad_x, ldgx,
+                        grad_weight, accumulate, ws, ws_bytes, stream);
   NormBwdArgs a{};
   a.x = summed, a.N = N, a.D = D, a.ldx = lds, a.dy = grad_y, a.lddy = ldgy;
   a.more = grad_summed, a.ldmore = ldgs, a.weight = weight, a.rstd = rstd;
   a.dx = grad_x, a.lddx = ldgx, a.dw = grad_weight, a.accumulate = accumulate;
-  if (grad_x == nullptr || N == 0) a.more = nullptr;
   auto any = [](NormBwdArgs b, int dtype, cudaStream_t s) {
     return dtype == FLCE_BF16 ? launch_norm_add_bwd_any<__nv_bfloat16>(b, dtype, s)
                               : launch_norm_add_bwd_any<float>(b, dtype, s);
   };
-  return a.more != nullptr ? norm_bwd<false, true>(a, dt, wdt, ws, ws_bytes, stream, any)
-                           : norm_bwd<false, false>(a, dt, wdt, ws, ws_bytes, stream);
+  return norm_bwd<false, true>(a, dt, wdt, ws, ws_bytes, stream, any);
 }
