@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(Gemm8Geo<BN>::kThreads, 1)
       // the order of the ranks.  The ring is free in every CTA (its blocks' sums are
       // read), and takes the shares as [from][column][row].
       const int part = BN / g.split;
+      __syncwarp();  // (one lane arrives and reports: the barrier wants whole warps)
       cluster_sync();
       const uint32_t mine =
           smem_u32(smem) + static_cast<uint32_t>((rank * part * kG8Rows + row) * 4);

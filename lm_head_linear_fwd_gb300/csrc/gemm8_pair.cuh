@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
         }
       }
     }
+    __syncwarp();  // one lane has copied: the barrier at the end wants whole warps
   } else if (warp <= 2) {
     if (leader) {
       // products of one half of the tile's columns: the sums of one block after the other
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(Gemm8Pair<kCols>::kThreads, 1)
         }
       }
     }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // sums: a thread has 128 columns of one row
