@@ -12,7 +12,7 @@
 //                       complement, so that keys differ and the larger one comes first;
 //   beam_merge_kernel   a block takes a request: every row's lse and best `num` keys
 //                       from its chunks', then the request's from its rows'.
-// Bound by the bytes of the logits, for few rows by the latency of the two launches.
+// Bound by latency: of a block's steps for many rows, of the two launches for few.
 //
 // beam_reorder_kernel moves rows of caches and histories.  Their order is a map that
 // repeats some beams and drops others, in place: a thread owns 16 bytes of each of a
@@ -79,11 +79,14 @@ __device__ __forceinline__ bool row_counts(const BeamArgs& a, int64_t row) {
 // num keys reach, and at most num groups have keys that do.  The first tile's bound
 // serves the whole chunk: what reaches it is written down without a wait, some num
 // keys to a tile, and ranked at the end.  Where that overflows (rows that rise) the
-// chunk is read again, with a bound and the best num so far for each tile.  Bound by
-// instructions (some 14 per logit), four blocks to an SM: 320 x 151936 fp32 34 of 42 us
-// with the merge (5.7 TB/s), 128 x 128256 bf16 24 to 27 us.  With a bound for every tile,
-// of one to a block, 52 of 61 and 31; eight tiles to a block 43 and 24.  The fp32 rows
-// with their first half masked take 72 us, all equal 60, sorted upwards 115.
+// chunk is read again, with a bound and the best num so far for each tile.  Bound by the
+// latency of a block's loads, bound and ranking at four blocks to an SM (28 warps, issue
+// slots 47% full with some 14 instructions per logit): 320 x 151936 fp32 34 of 42 us with
+// the merge (5.7 TB/s; the bytes take 28.7), 128 x 128256 bf16 26 to 27 us (4.8: half the
+// bytes, the same instructions, and 768 blocks for 608 places of which 128 have less than a
+// tile).  With a bound for every tile, of one to a block, 52 of 61 and 31; eight tiles to a
+// block 43 and 24.  The fp32 rows with their first half masked take 72 us, all equal 60,
+// sorted upwards 115.
 template <typename T, int ELEMS>
 struct BeamTile {
   static constexpr int VEC = 16 / sizeof(T), NV = ELEMS / VEC;
@@ -495,7 +498,9 @@ __global__ void __launch_bounds__(kReorderThreads)
 
 // How rows are cut: elements of a thread in a tile, tiles of a chunk.  Long tiles where
 // they fill half of the places for blocks, several to a chunk where there are more; else
-// short ones (4 x 50257 fp32: 8 against 11 us).
+// short ones (4 x 50257 fp32: 8.8 against 9.3 us.  A long vocabulary pays for them in the
+// merge, whose block has the chunks of all rows of a request: 8 x 128256 bf16 of one
+// request 27.7 against 14.8).
 struct BeamPlan {
   int elems, tiles;
   int64_t chunks;

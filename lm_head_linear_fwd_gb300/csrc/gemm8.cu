@@ -369,9 +369,9 @@ static int split_of(int64_t tiles, int64_t blocks) {
 // Tokens of a tile (0: a tile of gemm8_pair_kernel).  Up to 64 tokens one tile has them
 // all, and the weights are read once.  More than that go by 64 where this makes one
 // round of the SMs at most, and else to the pairs (M x N x 4096 in captured graphs: 200
-// x 4096 15 us, on pairs 20; 300 x 4096 27 and 20; 128 x 128256 172 and 119, with
-// tiles of 128 tokens 144).  Smaller tiles where all these CTAs fill less than half of
-// the SMs (77 x 768 x 1601: 6.4 us by 16, 7.7 by 32, 8.9 by 64).
+// x 4096 15.5 us, on pairs 17.3; 300 x 4096 27.1 and 17.4; 128 x 128256 172 and 114; 160 x
+// 128256 242 and 115).  Smaller tiles where all these CTAs fill less than half of the SMs
+// (77 x 768 x 1601: 6.3 us by 16, 7.9 by 32, 8.7 by 64).
 static int tile_tokens(int64_t M, int64_t N, int64_t blocks) {
   const int64_t tiles_n = (N + kG8Rows - 1) / kG8Rows, sms = sm_count();
   int bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;

@@ -14,7 +14,7 @@
 // about 800 cycles per block the products take 512 and the additions 256 (packed fp32
 // at half rate); the rest are the waits between them, which two warps to a scheduler
 // (their sums fill the registers) hide in part.  8192 x 4096 x 16384, scales of b for
-// 128 rows: 371 us, 3.0 PFLOP/s; for each row, twice the arithmetic, 531 us (519 with the
+// 128 rows: 373 us, 2.9 PFLOP/s; for each row, twice the arithmetic, 531 us (519 with the
 // sum times one scale formed first, which leaves fp32's range where the other scale would
 // bring it back; the scales' products formed while the sums are on their way 564).  The
 // scales loaded by the adding threads took 723 us (they spill), handed over for four

@@ -42,8 +42,8 @@ __device__ __forceinline__ float rounded(float x) {
 
 constexpr int kZeroWeights = 32;
 
-// Rows on 16-byte boundaries.  65536 x 5120 bf16: 362 us with y in 8 bits, 416 in bf16
-// (both 6.5 TB/s); 8192 x 4096 to 8 bits 42 us.  With two rows at a time of 16 elements
+// Rows on 16-byte boundaries.  65536 x 5120 bf16: 363 us with y in 8 bits, 415 in bf16
+// (both 6.5 TB/s); 8192 x 4096 to 8 bits 43.5 us.  With two rows at a time of 16 elements
 // per thread, as in norm_fwd_kernel, and two divisions per block and lane: 412, 415, 49.
 template <typename T, int kElems, bool kQuant>
 __global__ void __launch_bounds__(kFwdThreads<T>) norm_add_fwd_kernel(NormAddArgs a) {
@@ -178,8 +178,9 @@ __global__ void __launch_bounds__(kFwdThreads<T>) norm_add_fwd_kernel(NormAddArg
 
 // Rows that begin anywhere: element by element, 32 neighbouring ones to a warp's access.
 // A warp has blocks of 128 columns, kAnyBlocks of them at most, in registers; `team`
-// warps have a row.  Bound by those accesses and by what registers leave of an SM's
-// warps: 8191 x 1601 bf16 29 us, to 8 bits 37, fp32 44; four blocks to a warp 33, 48
+// warps have a row.  Bound by the latency of a row's loads, sums and stores, one after the
+// other, with what registers leave of an SM's warps (27; issue slots 54% full): 8191 x
+// 1601 bf16 29 us, to 8 bits 37, fp32 44; four blocks to a warp 33, 48
 // and 67 us, one 32, 42 and 43; whole 16-byte blocks shifted together, as in
 // norm_fwd_kernel, 52, 55 and 75.
 constexpr int kAnyThreads = 512;
